@@ -92,7 +92,7 @@ def draw(rng):
     pairs = _between(rng, 2, 32)
     rows = max(8 * pairs, _between(rng, 100, min(8192, most)))
     average = rng.random() < 0.3
-    return dict(PREFERENCE, **{**same, "pairs": pairs, "rows": rows, "kind": rng.choice(["sigmoid", "sigmoid", "ipo"]),
+    return dict(PREFERENCE, **{**same, "pairs": pairs, "rows": rows, "kind": rng.choice(["sigmoid", "sigmoid", "squared"]),
                                "beta": 2.0 if average else 0.1, "average": average, "reference": not average,
                                "smoothing": rng.choice([0.0, 0.1]), "prompt": rng.choice([0.0, 0.4]),
                                "tail": rng.choice([0, 0, rows // 20]),
@@ -276,7 +276,7 @@ def _plain_preference(st, step):
         ref = st["ref"].double()
         h = h - (ref[:P] - ref[P:])
     beta, eps = c["beta"], c["smoothing"]
-    if c["kind"] == "ipo":
+    if c["kind"] == "squared":
         off = h - c["margin"] - 0.5 / beta
         loss, dh = off * off, 2 * off
     else:
@@ -385,7 +385,7 @@ def exact(case, seed):
             h = h - st["ref"][:P].double() + st["ref"][P:].double()
         h = h.requires_grad_()
         z = case["beta"] * h - case["margin"]
-        if case["kind"] == "ipo":
+        if case["kind"] == "squared":
             pairs = (h - case["margin"] - 1 / (2 * case["beta"])) ** 2
         else:
             eps = case["smoothing"]
