@@ -3,7 +3,9 @@
  * NVIDIA GB300 (sm_103a): per-row loss, mean loss, fused loss + gradient,
  * and the row argmax that closes a decode step; beside them, the rows a
  * language model's step reads from the same logits (softmax, log-softmax,
- * sampling candidates) and the join of split partial sums.
+ * sampling candidates) and the join of split partial sums; and the objectives
+ * over sampled answers and pairs of answers (token log-probabilities, the
+ * clipped policy loss, the preference loss), each with its gradient.
  *
  * Definitions follow the API reference page "gizml:netops"
  * (gizstack.com/docs/reference/gizml/netops.md), section Functions:
@@ -346,6 +348,140 @@ CE_API int ce_grad_from_stats(const float *logits, int64_t rows, int64_t vocab, 
                               const int64_t *labels, const float *combined, double scale, float *grad,
                               ce_stream_t stream);
 
+/*
+ * Objectives over sampled answers and over pairs of answers. They read the
+ * same [rows, stride] logits and int64 labels as the calls above, in three
+ * types, and share these conventions:
+ *  - dtype: CE_F32, CE_BF16 or CE_F16, the type of the logits and of their
+ *    gradient. Everything else of a row is f32; row statistics, losses and
+ *    the gradient are computed in f32 and a gradient is rounded once, at the
+ *    end. Sums over rows are f64, rounded once to the f32 they are given as.
+ *  - temperature T > 0 (1e-6 <= T <= 1e6): the distribution of a row is
+ *    softmax(x / T); gradients are with respect to x.
+ *  - weights: [rows] f32, or NULL (every row counts 1). A row of weight 0 (a
+ *    prompt or padding token) takes no part: its logits, its label and its
+ *    other inputs may hold anything and are not read, its outputs are 0 and
+ *    its gradient row is zeros.
+ *  - gradients are with respect to the scaled loss and are written to rows
+ *    grad_stride elements apart (grad_stride >= vocab; columns vocab and up
+ *    are not written). grad == logits (in place) is allowed when grad_stride
+ *    == stride; any other overlap is CE_EINVAL.
+ *  - A label outside [0, vocab) on a row that counts gives that row a NaN
+ *    log-probability (and so a NaN loss and gradient row) and increments the
+ *    device counter. A row holding a NaN or +inf, or nothing above -inf, is
+ *    NaN likewise. -inf logits of other rows have probability 0; a label
+ *    there has log-probability -inf.
+ *  - log-probabilities and entropies carry an absolute error of a few f32
+ *    roundings of log(s), not a relative one near 0; ce_rows keeps the
+ *    relative accuracy of tiny losses.
+ *  - rows == 0 is valid: the scalar loss is still written (0).
+ *  - The calls keep nothing between them and are safe side by side on several
+ *    streams, given each its own outputs and work buffer.
+ */
+enum ce_dtype { CE_F32 = 0, CE_BF16 = 1, CE_F16 = 2 };
+
+/*
+ * logp_rows: the log-probability of each row's label,
+ *     logp = (x[label] - m) / T - log(s),  m = max_j x_j,  s = sum_j exp((x_j - m) / T),
+ * and, with `entropy`, the row's entropy H = -sum_j p_j log p_j, from one read
+ * of the logits: what the two losses below take as the sampling policy's and
+ * the reference's log-probabilities, for a decode step's few rows or a whole
+ * batch. An entry of probability 0 adds 0 to the entropy.
+ *   logp:    [rows] f32, written.   entropy: [rows] f32, or NULL.
+ */
+CE_API int logp_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,
+                     const int64_t *labels, const float *weights, double temperature, float *logp, float *entropy,
+                     ce_stream_t stream);
+
+/* The policy loss's constants. clip_low, clip_high >= 0, INFINITY: no clip on
+ * that side; kl_coef, entropy_coef and scale finite. */
+typedef struct ce_policy {
+    double scale, temperature, clip_low, clip_high, kl_coef, entropy_coef;
+} ce_policy;
+
+/*
+ * policy_loss: the clipped policy loss of tokens sampled by an older policy,
+ * with a KL term to a reference policy and an entropy bonus. Per row, with
+ * r = exp(logp - old_logp), A the advantage and d = ref_logp - logp:
+ *     l = max(-A r, -A clamp(r, 1 - clip_low, 1 + clip_high))
+ *         + kl_coef (exp(d) - 1 - d) - entropy_coef H
+ *     loss = scale * sum_i weights_i l_i
+ *   old_logp, advantages: [rows] f32.   ref_logp: [rows] f32, or NULL when
+ *   kl_coef == 0 (then never read).
+ *   loss_rows: [rows] f32, the l_i (unweighted).   logp: [rows] f32.
+ *   entropy: [rows] f32, or NULL.   loss: 1 f32, all written on the device.
+ */
+CE_API int policy_loss(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,
+                       const int64_t *labels, const float *old_logp, const float *advantages, const float *ref_logp,
+                       const float *weights, const ce_policy *policy, float *loss_rows, float *logp, float *entropy,
+                       float *loss, ce_stream_t stream);
+
+/*
+ * policy_step: policy_loss and its gradient, with
+ *     g = [-A r where -A r is the larger term, or the terms are equal] + kl_coef (1 - exp(d)):
+ *     grad[i, j] = scale weights_i / T (g ([j == label] - p_j) + entropy_coef p_j (log p_j + H)).
+ * Each logit is read once from HBM and each gradient written once (rows of
+ * more than about 3.5 MB are read three times).
+ */
+CE_API int policy_step(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,
+                       const int64_t *labels, const float *old_logp, const float *advantages, const float *ref_logp,
+                       const float *weights, const ce_policy *policy, void *grad, int64_t grad_stride,
+                       float *loss_rows, float *logp, float *entropy, float *loss, ce_stream_t stream);
+
+enum ce_preference_kind { CE_PREF_SIGMOID = 0, CE_PREF_HINGE = 1, CE_PREF_SQUARED = 2 };
+
+/* The preference loss's constants: beta > 0, 0 <= label_smoothing <= 0.5
+ * (sigmoid only), margin and scale finite; average: sequences are averaged
+ * over their tokens (by weight) rather than summed. */
+typedef struct ce_preference {
+    double scale, temperature, beta, label_smoothing, margin;
+    int kind, average;
+} ce_preference;
+
+/*
+ * preference_loss: the loss of `pairs` pairs of sequences, one preferred to
+ * the other. The batch's rows hold 2 * pairs sequences, sequence s being rows
+ * offsets[s] .. offsets[s + 1] - 1; sequence p is the chosen one of pair p and
+ * sequence pairs + p the rejected one. With L_s the sum of weights * logp over
+ * a sequence (average: divided by its sum of weights; 0 where that is 0), R_s
+ * the same of the reference model (0 without one),
+ *     h = (L_p - L_{pairs+p}) - (R_p - R_{pairs+p}),  z = beta h - margin:
+ *     sigmoid  l = -(1 - eps) log sigma(z) - eps log sigma(-z)
+ *     hinge    l = max(0, 1 - z)
+ *     squared  l = (h - margin - 1 / (2 beta))^2
+ *     loss = scale * sum_p l_p
+ *   offsets: [2 * pairs + 1] int64 on the device, non-decreasing, within
+ *     [0, rows]. Rows in no sequence count as rows of weight 0. A sequence may
+ *     be empty (L = 0). Nothing is read or written out of range whatever the
+ *     table holds: a pair with a range that is not valid has a NaN loss (so the
+ *     sum is NaN too), its bad sequence no rows, and each bad range increments
+ *     the device counter; of a table that decreases somewhere, the other pairs
+ *     may have lost rows as well.
+ *   ref_logp: [2 * pairs] f32, the R_s (seq_logp of a call on the reference
+ *     model's logits), or NULL.
+ *   logp: [rows] f32.   seq_logp: [2 * pairs] f32, the L_s.
+ *   loss_pairs: [pairs] f32, the l_p.   loss: 1 f32, all written on the device.
+ *   work: 16 bytes of scratch, 16-byte aligned; two calls that may run at the
+ *     same time need one each.
+ */
+CE_API int preference_loss(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,
+                           const int64_t *labels, const float *weights, const int64_t *offsets, int64_t pairs,
+                           const float *ref_logp, const ce_preference *preference, float *logp, float *seq_logp,
+                           float *loss_pairs, float *loss, void *work, ce_stream_t stream);
+
+/*
+ * preference_step: preference_loss and its gradient: a row of a chosen (+) or
+ * rejected (-) sequence gets +- scale dl/dh weight / (sum of weights | 1) / T
+ * * ([j == label] - p_j); rows in no sequence get zeros. The factor of a row is
+ * known only once its pair has been read, so the logits are read twice.
+ *   work: 16 * (rows + 1) bytes, 16-byte aligned, as above.
+ */
+CE_API int preference_step(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,
+                           const int64_t *labels, const float *weights, const int64_t *offsets, int64_t pairs,
+                           const float *ref_logp, const ce_preference *preference, void *grad, int64_t grad_stride,
+                           float *logp, float *seq_logp, float *loss_pairs, float *loss, void *work,
+                           ce_stream_t stream);
+
 /* Human-readable text of a status code (a static string). */
 CE_API const char *ce_status_string(int status);
 
@@ -357,8 +493,9 @@ CE_API int ce_last_cuda_error(void);
 
 /*
  * Device-side error counter of the current device, for tests and
- * diagnostics: *out = rows seen with a label outside [0, vocab) since the
- * last reset. This call WAITS for `stream` to finish.
+ * diagnostics: *out = rows seen with a label outside [0, vocab), and bad
+ * sequence ranges, since the last reset. This call WAITS for `stream` to
+ * finish.
  */
 CE_API int ce_device_error_count(ce_stream_t stream, int64_t *out);
 

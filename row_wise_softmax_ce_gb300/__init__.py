@@ -31,6 +31,16 @@ Functions, and section Methods for the argmax rule):
                    and gradient of rows whose vocabulary is split over slices,
                    from one exchange of 16 bytes per row and slice
 
+and the objectives over sampled answers and over pairs of answers, whose logits
+may also be bfloat16 or float16 (formulas in ``include/ce_rows.h``):
+
+- ``logp_rows``    the log-probability of each row's label at a temperature, and
+                   the row's entropy
+- ``policy_loss`` / ``policy_step``  the clipped policy loss with a KL term and an
+                   entropy bonus, and its gradient
+- ``preference_loss`` / ``preference_step``  the loss of pairs of sequences
+                   (sigmoid, hinge, squared), and its gradient
+
 Logits are a CUDA float32 tensor ``[rows, cols]`` whose rows are contiguous
 (``stride(1) == 1``); its row stride ``stride(0)`` may exceed ``vocab``
 (padded rows), and ``vocab`` defaults to ``cols``. Labels are int64 ``[rows]``.
@@ -52,11 +62,26 @@ HEADER = os.path.join(os.path.dirname(_PKG), "include", "ce_rows.h")
 CE_OK, CE_EINVAL, CE_EALIGN, CE_ECUDA, CE_EDEVICE, CE_ERANGE = 0, -1, -2, -3, -4, -5
 PATH_AUTO, PATH_STAGED, PATH_STREAM, PATH_STAGED_PER_ROW, PATH_FLAT, PATH_WARP, PATH_RING = 0, 1, 2, 4, 5, 6, 7
 OP_ROWS, OP_GRAD, OP_ARGMAX, OP_SOFTMAX, OP_LOG_SOFTMAX, OP_CANDIDATES = 0, 1, 2, 3, 4, 5
+# logits of the objectives (enum ce_dtype) and kinds of preference loss (enum ce_preference_kind)
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "squared": 2}
 # candidatesInto's workgroup, TOP_EACH and CANDIDATE_ROW (gizml:netops, Constants)
 CANDIDATE_THREADS, TOP_EACH, CANDIDATE_ROW = 256, 4, 2048
 
 _lock = threading.Lock()
 _lib = None
+
+
+class Policy(ctypes.Structure):
+    """struct ce_policy"""
+    _fields_ = [(n, ctypes.c_double) for n in ("scale", "temperature", "clip_low", "clip_high", "kl_coef",
+                                               "entropy_coef")]
+
+
+class Preference(ctypes.Structure):
+    """struct ce_preference"""
+    _fields_ = [(n, ctypes.c_double) for n in ("scale", "temperature", "beta", "label_smoothing", "margin")] + \
+               [(n, ctypes.c_int) for n in ("kind", "average")]
 
 
 class CeError(RuntimeError):
@@ -99,6 +124,11 @@ def _bind(lib):
         "ce_grad_host": [vp, i64, i64, i64, vp, ctypes.c_double, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp],
         "ce_plan": [i32, i64, i64, i64, ctypes.POINTER(ctypes.c_int64)],
         "ce_debug_read": [vp, i64, vp, vp],
+        "logp_rows": [vp, i32, i64, i64, i64, vp, vp, ctypes.c_double, vp, vp, vp],
+        "policy_loss": [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp],
+        "policy_step": [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp],
+        "preference_loss": [vp, i32, i64, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp],
+        "preference_step": [vp, i32, i64, i64, i64, vp, vp, vp, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -505,6 +535,193 @@ def ce_grad_from_stats(shard: torch.Tensor, labels: torch.Tensor, col0: int, com
                                                                labels.data_ptr(), combined.data_ptr(),
                                                                float(scale), grad.data_ptr(), _stream(dev)))
     return grad
+
+
+# -- objectives over sampled answers and over pairs of answers ---------------------
+
+def _objective_view(logits: torch.Tensor, vocab: int | None):
+    """(dtype, rows, vocab, stride) of f32, bf16 or f16 logits with contiguous rows."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in DTYPES:
+        raise TypeError("logits must be a float32, bfloat16 or float16 torch.Tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits must be on a CUDA device")
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D [rows, cols]")
+    rows, cols = logits.shape
+    if rows > 0 and cols > 1 and logits.stride(1) != 1:
+        raise ValueError("each row of logits must be contiguous (stride(1) == 1)")
+    stride = logits.stride(0) if rows > 1 else max(cols, 1)
+    vocab = cols if vocab is None else int(vocab)
+    if not 1 <= vocab <= cols:
+        raise ValueError(f"need 1 <= vocab <= logits.shape[1] (vocab={vocab}, cols={cols})")
+    if rows > 1 and stride < vocab:
+        raise ValueError("rows of logits overlap (stride(0) < vocab)")
+    return DTYPES[logits.dtype], rows, vocab, max(stride, vocab)
+
+
+def _per_row(t, n, device, name):
+    """A contiguous f32 [n] input's pointer (None for None)."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor [{n}] on {device}")
+    return t.data_ptr()
+
+
+def _grad_out(grad, logits, rows, vocab):
+    """The gradient's tensor and row stride: allocated dense, or the caller's
+    [rows, >= vocab] tensor of the logits' type with contiguous rows."""
+    if grad is None:
+        grad = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+    elif grad.dtype != logits.dtype or grad.device != logits.device or grad.dim() != 2 or grad.shape[0] != rows or \
+            grad.shape[1] < vocab or (rows > 0 and grad.shape[1] > 1 and grad.stride(1) != 1):
+        raise ValueError(f"grad must be a {logits.dtype} [rows={rows}, >= {vocab}] tensor with contiguous rows on "
+                         f"{logits.device}")
+    stride = grad.stride(0) if rows > 1 else vocab
+    if rows > 1 and stride < vocab:
+        raise ValueError("rows of grad overlap (stride(0) < vocab)")
+    return grad, stride
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def logp_rows(logits: torch.Tensor, labels: torch.Tensor, weights: torch.Tensor | None = None,
+              temperature: float = 1.0, vocab: int | None = None, entropy: bool | torch.Tensor = False,
+              out: torch.Tensor | None = None):
+    """The log-probability of each row's label under softmax(logits /
+    temperature), f32 ``[rows]``; with ``entropy`` (True or a tensor) the pair
+    ``(logp, entropy)`` from the same read. ``weights`` (f32 ``[rows]``): rows of
+    weight 0 are not read and give 0."""
+    dtype, rows, vocab, stride = _objective_view(logits, vocab)
+    dev = logits.device
+    labels = _labels(labels, rows, dev)
+    w = _per_row(weights, rows, dev, "weights")
+    out = _out(out, (rows,), torch.float32, dev, "out")
+    ent = None if entropy is False else _out(None if entropy is True else entropy, (rows,), torch.float32, dev,
+                                             "entropy")
+    with torch.cuda.device(dev):
+        _check("logp_rows", lib().logp_rows(logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), w,
+                                             float(temperature), out.data_ptr(), _ptr(ent), _stream(dev)))
+    return out if ent is None else (out, ent)
+
+
+def _policy(step, logits, labels, old_logp, advantages, scale, ref_logp, weights, clip_low, clip_high, kl_coef,
+            entropy_coef, temperature, vocab, entropy, grad):
+    dtype, rows, vocab, stride = _objective_view(logits, vocab)
+    dev = logits.device
+    labels = _labels(labels, rows, dev)
+    if old_logp is None or advantages is None:
+        raise ValueError("old_logp and advantages are needed")
+    old, adv = _per_row(old_logp, rows, dev, "old_logp"), _per_row(advantages, rows, dev, "advantages")
+    ref, w = _per_row(ref_logp, rows, dev, "ref_logp"), _per_row(weights, rows, dev, "weights")
+    if kl_coef != 0 and ref_logp is None:
+        raise ValueError("kl_coef needs ref_logp")
+    ent = None if entropy is False else _out(None if entropy is True else entropy, (rows,), torch.float32, dev,
+                                             "entropy")
+    loss_rows = torch.empty(rows, dtype=torch.float32, device=dev)
+    logp = torch.empty(rows, dtype=torch.float32, device=dev)
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    par = Policy(scale, temperature, clip_low, clip_high, kl_coef, entropy_coef)
+    with torch.cuda.device(dev):
+        if step:
+            grad, gs = _grad_out(grad, logits, rows, vocab)
+            _check("policy_step", lib().policy_step(
+                logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), old, adv, ref, w,
+                ctypes.byref(par), grad.data_ptr(), gs, loss_rows.data_ptr(), logp.data_ptr(), _ptr(ent),
+                loss.data_ptr(), _stream(dev)))
+            return grad, loss, loss_rows, logp, ent
+        _check("policy_loss", lib().policy_loss(
+            logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), old, adv, ref, w, ctypes.byref(par),
+            loss_rows.data_ptr(), logp.data_ptr(), _ptr(ent), loss.data_ptr(), _stream(dev)))
+    return loss, loss_rows, logp, ent
+
+
+def policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor,
+                scale: float, ref_logp: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+                clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0, entropy_coef: float = 0.0,
+                temperature: float = 1.0, vocab: int | None = None, entropy: bool | torch.Tensor = False):
+    """The clipped policy loss ``scale * sum(weights * l)`` of sampled tokens,
+    ``l = max(-A r, -A clamp(r, 1 - clip_low, 1 + clip_high)) + kl_coef (exp(d) -
+    1 - d) - entropy_coef H`` with ``r = exp(logp - old_logp)``, ``d = ref_logp -
+    logp``: returns ``(loss, loss_rows, logp, entropy)`` -- 0-d f32, f32
+    ``[rows]`` each, entropy None unless asked for."""
+    return _policy(False, logits, labels, old_logp, advantages, scale, ref_logp, weights, clip_low, clip_high, kl_coef,
+                   entropy_coef, temperature, vocab, entropy, None)
+
+
+def policy_step(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor,
+                scale: float, ref_logp: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+                clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0, entropy_coef: float = 0.0,
+                temperature: float = 1.0, vocab: int | None = None, entropy: bool | torch.Tensor = False,
+                grad: torch.Tensor | None = None):
+    """``policy_loss`` and its gradient with respect to the logits, in their
+    type, from one read: returns ``(grad, loss, loss_rows, logp, entropy)``.
+    ``grad`` may be the logits themselves (in place) or any ``[rows, >= vocab]``
+    tensor with contiguous rows (columns past vocab are left alone); dense
+    ``[rows, vocab]`` when not given."""
+    return _policy(True, logits, labels, old_logp, advantages, scale, ref_logp, weights, clip_low, clip_high, kl_coef,
+                   entropy_coef, temperature, vocab, entropy, grad)
+
+
+def _preference(step, logits, labels, offsets, scale, ref_logp, weights, kind, beta, label_smoothing, margin, average,
+                temperature, vocab, grad):
+    dtype, rows, vocab, stride = _objective_view(logits, vocab)
+    dev = logits.device
+    labels = _labels(labels, rows, dev)
+    if offsets.dtype != torch.int64 or offsets.dim() != 1 or offsets.shape[0] % 2 != 1 or offsets.device != dev or \
+            not offsets.is_contiguous():
+        raise ValueError("offsets must be a contiguous int64 tensor [2 * pairs + 1] on the logits' device")
+    if kind not in PREFERENCE_KINDS:
+        raise ValueError(f"kind must be one of {sorted(PREFERENCE_KINDS)}")
+    pairs = offsets.shape[0] // 2
+    ref, w = _per_row(ref_logp, 2 * pairs, dev, "ref_logp"), _per_row(weights, rows, dev, "weights")
+    logp = torch.empty(rows, dtype=torch.float32, device=dev)
+    seq_logp = torch.empty(2 * pairs, dtype=torch.float32, device=dev)
+    loss_pairs = torch.empty(pairs, dtype=torch.float32, device=dev)
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    work = torch.empty((rows + 1 if step else 1, 4), dtype=torch.float32, device=dev)
+    par = Preference(scale, temperature, beta, label_smoothing, margin, PREFERENCE_KINDS[kind], 1 if average else 0)
+    with torch.cuda.device(dev):
+        if step:
+            grad, gs = _grad_out(grad, logits, rows, vocab)
+            _check("preference_step", lib().preference_step(
+                logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), w, offsets.data_ptr(), pairs, ref,
+                ctypes.byref(par), grad.data_ptr(), gs, logp.data_ptr(), seq_logp.data_ptr(), loss_pairs.data_ptr(),
+                loss.data_ptr(), work.data_ptr(), _stream(dev)))
+            return grad, loss, loss_pairs, seq_logp, logp
+        _check("preference_loss", lib().preference_loss(
+            logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), w, offsets.data_ptr(), pairs, ref,
+            ctypes.byref(par), logp.data_ptr(), seq_logp.data_ptr(), loss_pairs.data_ptr(), loss.data_ptr(),
+            work.data_ptr(), _stream(dev)))
+    return loss, loss_pairs, seq_logp, logp
+
+
+def preference_loss(logits: torch.Tensor, labels: torch.Tensor, offsets: torch.Tensor, scale: float,
+                    ref_logp: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+                    kind: str = "sigmoid", beta: float = 0.1, label_smoothing: float = 0.0, margin: float = 0.0,
+                    average: bool = False, temperature: float = 1.0, vocab: int | None = None):
+    """The preference loss ``scale * sum(l)`` of pairs of sequences: rows
+    ``offsets[s]:offsets[s + 1]`` are sequence s; sequence p is the chosen and
+    ``pairs + p`` the rejected one of pair p (``offsets`` int64 ``[2 * pairs + 1]``
+    on the device). ``ref_logp`` f32 ``[2 * pairs]``: the reference model's
+    sequence log-probabilities (``seq_logp`` of its logits). Returns ``(loss,
+    loss_pairs, seq_logp, logp)``: 0-d, ``[pairs]``, ``[2 * pairs]``, ``[rows]``."""
+    return _preference(False, logits, labels, offsets, scale, ref_logp, weights, kind, beta, label_smoothing, margin,
+                       average, temperature, vocab, None)
+
+
+def preference_step(logits: torch.Tensor, labels: torch.Tensor, offsets: torch.Tensor, scale: float,
+                    ref_logp: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+                    kind: str = "sigmoid", beta: float = 0.1, label_smoothing: float = 0.0, margin: float = 0.0,
+                    average: bool = False, temperature: float = 1.0, vocab: int | None = None,
+                    grad: torch.Tensor | None = None):
+    """``preference_loss`` and its gradient with respect to the logits, in their
+    type: returns ``(grad, loss, loss_pairs, seq_logp, logp)``. ``grad`` as in
+    ``policy_step``."""
+    return _preference(True, logits, labels, offsets, scale, ref_logp, weights, kind, beta, label_smoothing, margin,
+                       average, temperature, vocab, grad)
 
 
 # -- diagnostics and tuning ---------------------------------------------------

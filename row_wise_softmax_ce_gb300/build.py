@@ -22,8 +22,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcerows.so")
 
-SOURCES = ["ce_kernels.cu", "ce_api.cu"]
-HEADERS = ["ce_device.cuh", "ce_internal.h"]
+SOURCES = ["ce_kernels.cu", "ce_objectives.cu", "ce_api.cu"]
+HEADERS = ["ce_device.cuh", "ce_objectives.cuh", "ce_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               "--expt-relaxed-constexpr", f"-I{INCLUDE}", f"-I{CSRC}"]

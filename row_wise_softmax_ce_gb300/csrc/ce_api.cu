@@ -82,6 +82,7 @@ int current_device(DeviceInfo *out) {
         }
         if (d.cc_major != 10 || d.cc_minor != 3) return CE_EDEVICE;  // built for sm_103a only
         if ((e = set_kernel_attributes(d)) != cudaSuccess) return cuda_status(e);
+        if ((e = set_objective_attributes(d)) != cudaSuccess) return cuda_status(e);
         g_dev[dev] = d;
         g_ready[dev] = true;
     }
@@ -661,10 +662,190 @@ int argmax_rows_noalloc(const float *logits, int64_t rows, int64_t vocab, int64_
     return cuda_status(launch_argmax_flat(a, static_cast<int>(ctas), keys, stream));
 }
 
+// -- the objectives over sampled answers -----------------------------------------
+
+// The checks the objectives share, and the part of ObjArgs they come to.
+static int check_objective(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,
+                           const int64_t *labels, const float *weights, double temperature, double scale,
+                           const float *logp, ObjArgs *a) {
+    if (dtype != CE_F32 && dtype != CE_BF16 && dtype != CE_F16) return CE_EINVAL;
+    if (rows < 0 || vocab < 1 || vocab > kMaxVocab || stride < vocab) return CE_EINVAL;
+    if (rows > 0 && (logits == nullptr || labels == nullptr || logp == nullptr)) return CE_EINVAL;
+    if (rows > 0 && stride > (INT64_MAX / 4) / rows) return CE_EINVAL;  // byte offsets fit int64
+    if (!(temperature >= 1e-6 && temperature <= 1e6) || !std::isfinite(scale)) return CE_EINVAL;
+    if (misaligned(logits, dtype == CE_F32 ? 4 : 2) || misaligned(labels, 8) || misaligned(weights, 4) ||
+        misaligned(logp, 4))
+        return CE_EALIGN;
+    *a = ObjArgs{};
+    a->logits = logits;
+    a->rows = rows;
+    a->vocab = static_cast<int>(vocab);
+    a->stride = stride;
+    a->labels = labels;
+    a->weights = weights;
+    a->k = static_cast<float>(1.4426950408889634 / temperature);
+    a->inv_t = static_cast<float>(1.0 / temperature);
+    a->scale = static_cast<float>(scale);
+    a->logp = const_cast<float *>(logp);
+    return CE_OK;
+}
+
+// The gradient's checks: its rows, in place or apart from the logits.
+static int check_objective_grad(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,
+                                const void *grad, int64_t grad_stride) {
+    const int64_t size = dtype == CE_F32 ? 4 : 2;
+    if (grad_stride < vocab || (rows > 0 && grad == nullptr)) return CE_EINVAL;
+    if (rows > 0 && grad_stride > (INT64_MAX / 4) / rows) return CE_EINVAL;
+    if (misaligned(grad, static_cast<uintptr_t>(size))) return CE_EALIGN;
+    if (rows == 0) return CE_OK;
+    if (grad == logits) return grad_stride == stride ? CE_OK : CE_EINVAL;
+    return ranges_overlap(grad, ((rows - 1) * grad_stride + vocab) * size, logits,
+                          ((rows - 1) * stride + vocab) * size)
+               ? CE_EINVAL
+               : CE_OK;
+}
+
+int logp_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride, const int64_t *labels,
+              const float *weights, double temperature, float *logp, float *entropy, ce_stream_t stream) {
+    ObjArgs a;
+    int st = check_objective(logits, dtype, rows, vocab, stride, labels, weights, temperature, 1.0, logp, &a);
+    if (st) return st;
+    if (misaligned(entropy, 4)) return CE_EALIGN;
+    if (rows == 0) return CE_OK;
+    DeviceInfo dev;
+    if ((st = current_device(&dev))) return st;
+    a.entropy = entropy;
+    return cuda_status(launch_obj_rows(static_cast<DType>(dtype), kObjLogp, a, dev, stream));
+}
+
+static int policy_pass(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,
+                       const int64_t *labels, const float *old_logp, const float *advantages, const float *ref_logp,
+                       const float *weights, const ce_policy *policy, bool step, void *grad, int64_t grad_stride,
+                       float *loss_rows, float *logp, float *entropy, float *loss, ce_stream_t stream) {
+    if (policy == nullptr || loss == nullptr) return CE_EINVAL;
+    ObjArgs a;
+    int st = check_objective(logits, dtype, rows, vocab, stride, labels, weights, policy->temperature, policy->scale,
+                             logp, &a);
+    if (st) return st;
+    if (!(policy->clip_low >= 0.0) || !(policy->clip_high >= 0.0)) return CE_EINVAL;
+    if (!std::isfinite(policy->kl_coef) || !std::isfinite(policy->entropy_coef)) return CE_EINVAL;
+    if (rows > 0 && (old_logp == nullptr || advantages == nullptr || loss_rows == nullptr)) return CE_EINVAL;
+    a.kl = static_cast<float>(policy->kl_coef);
+    a.bonus = static_cast<float>(policy->entropy_coef);
+    if (rows > 0 && a.kl != 0.0f && ref_logp == nullptr) return CE_EINVAL;
+    if (misaligned(old_logp, 4) || misaligned(advantages, 4) || misaligned(ref_logp, 4) || misaligned(loss_rows, 4) ||
+        misaligned(entropy, 4) || misaligned(loss, 4))
+        return CE_EALIGN;
+    if (step && (st = check_objective_grad(logits, dtype, rows, vocab, stride, grad, grad_stride))) return st;
+    DeviceInfo dev;
+    if ((st = current_device(&dev))) return st;
+    if (rows > 0) {
+        a.loss = loss_rows;
+        a.entropy = entropy;
+        a.old_logp = old_logp;
+        a.adv = advantages;
+        a.ref_logp = a.kl != 0.0f ? ref_logp : nullptr;
+        a.clip_lo = static_cast<float>(1.0 - policy->clip_low);
+        a.clip_hi = static_cast<float>(1.0 + policy->clip_high);
+        a.grad = grad;
+        a.grad_stride = grad_stride;
+        const DType t = static_cast<DType>(dtype);
+        st = cuda_status(step ? launch_policy_grad(t, a, dev, stream) : launch_obj_rows(t, kObjPolicy, a, dev, stream));
+        if (st) return st;
+    }
+    return cuda_status(launch_weighted_sum(loss_rows, weights, rows, policy->scale, loss, stream));
+}
+
+int policy_loss(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride, const int64_t *labels,
+                const float *old_logp, const float *advantages, const float *ref_logp, const float *weights,
+                const ce_policy *policy, float *loss_rows, float *logp, float *entropy, float *loss,
+                ce_stream_t stream) {
+    return policy_pass(logits, dtype, rows, vocab, stride, labels, old_logp, advantages, ref_logp, weights, policy,
+                       false, nullptr, 0, loss_rows, logp, entropy, loss, stream);
+}
+
+int policy_step(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride, const int64_t *labels,
+                const float *old_logp, const float *advantages, const float *ref_logp, const float *weights,
+                const ce_policy *policy, void *grad, int64_t grad_stride, float *loss_rows, float *logp,
+                float *entropy, float *loss, ce_stream_t stream) {
+    return policy_pass(logits, dtype, rows, vocab, stride, labels, old_logp, advantages, ref_logp, weights, policy,
+                       true, grad, grad_stride, loss_rows, logp, entropy, loss, stream);
+}
+
+static int preference_pass(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,
+                           const int64_t *labels, const float *weights, const int64_t *offsets, int64_t pairs,
+                           const float *ref_logp, const ce_preference *pref, bool step, void *grad,
+                           int64_t grad_stride, float *logp, float *seq_logp, float *loss_pairs, float *loss,
+                           void *work, ce_stream_t stream) {
+    if (pref == nullptr || loss == nullptr || offsets == nullptr || work == nullptr) return CE_EINVAL;
+    ObjArgs a;
+    int st = check_objective(logits, dtype, rows, vocab, stride, labels, weights, pref->temperature, pref->scale,
+                             logp, &a);
+    if (st) return st;
+    if (pairs < 0 || pairs > (int64_t(1) << 40)) return CE_EINVAL;
+    if (pairs > 0 && (seq_logp == nullptr || loss_pairs == nullptr)) return CE_EINVAL;
+    if (pref->kind < CE_PREF_SIGMOID || pref->kind > CE_PREF_SQUARED) return CE_EINVAL;
+    if (!(pref->beta > 0.0) || !std::isfinite(pref->beta) || !std::isfinite(pref->margin)) return CE_EINVAL;
+    if (!(pref->label_smoothing >= 0.0 && pref->label_smoothing <= 0.5)) return CE_EINVAL;
+    if (pref->label_smoothing != 0.0 && pref->kind != CE_PREF_SIGMOID) return CE_EINVAL;
+    if (misaligned(offsets, 8) || misaligned(ref_logp, 4) || misaligned(seq_logp, 4) || misaligned(loss_pairs, 4) ||
+        misaligned(loss, 4) || misaligned(work, 16))
+        return CE_EALIGN;
+    if (step && (st = check_objective_grad(logits, dtype, rows, vocab, stride, grad, grad_stride))) return st;
+    DeviceInfo dev;
+    if ((st = current_device(&dev))) return st;
+    const DType t = static_cast<DType>(dtype);
+    a.offsets = offsets;
+    a.pairs = pairs;
+    a.done = static_cast<uint32_t *>(work);
+    a.row_state = step ? static_cast<float4 *>(work) + 1 : nullptr;
+    a.grad = grad;
+    a.grad_stride = grad_stride;
+    JoinArgs j{};
+    j.logp = logp;
+    j.weights = weights;
+    j.rows = rows;
+    j.offsets = offsets;
+    j.pairs = pairs;
+    j.ref_seq = ref_logp;
+    j.kind = pref->kind;
+    j.average = pref->average != 0;
+    j.beta = pref->beta;
+    j.smoothing = pref->label_smoothing;
+    j.margin = pref->margin;
+    j.scale = pref->scale;
+    j.inv_t = 1.0 / pref->temperature;
+    j.seq_logp = seq_logp;
+    j.loss_pairs = loss_pairs;
+    j.loss = loss;
+    j.row_state = a.row_state;
+    j.done = a.done;
+    if ((st = cuda_status(launch_obj_rows(t, kObjPreference, a, dev, stream)))) return st;
+    if ((st = cuda_status(launch_join(j, dev, stream)))) return st;
+    return step ? cuda_status(launch_preference_grad(t, a, dev, stream)) : CE_OK;
+}
+
+int preference_loss(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride, const int64_t *labels,
+                    const float *weights, const int64_t *offsets, int64_t pairs, const float *ref_logp,
+                    const ce_preference *preference, float *logp, float *seq_logp, float *loss_pairs, float *loss,
+                    void *work, ce_stream_t stream) {
+    return preference_pass(logits, dtype, rows, vocab, stride, labels, weights, offsets, pairs, ref_logp, preference,
+                           false, nullptr, 0, logp, seq_logp, loss_pairs, loss, work, stream);
+}
+
+int preference_step(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride, const int64_t *labels,
+                    const float *weights, const int64_t *offsets, int64_t pairs, const float *ref_logp,
+                    const ce_preference *preference, void *grad, int64_t grad_stride, float *logp, float *seq_logp,
+                    float *loss_pairs, float *loss, void *work, ce_stream_t stream) {
+    return preference_pass(logits, dtype, rows, vocab, stride, labels, weights, offsets, pairs, ref_logp, preference,
+                           true, grad, grad_stride, logp, seq_logp, loss_pairs, loss, work, stream);
+}
+
 const char *ce_status_string(int status) {
     switch (status) {
     case CE_OK: return "ok";
-    case CE_EINVAL: return "invalid argument (null pointer, size, stride, vocab > 2^24, scale or forced plan)";
+    case CE_EINVAL:
+        return "invalid argument (null pointer, size, stride, vocab > 2^24, scale, type, constant of a loss or forced plan)";
     case CE_EALIGN: return "pointer not aligned to its element size";
     case CE_ECUDA: return "CUDA runtime error at launch (see ce_last_cuda_error)";
     case CE_EDEVICE: return "no usable sm_103 CUDA device";
@@ -744,9 +925,10 @@ static int read_counter(ce_stream_t stream, int which, int64_t *out) {
     DeviceInfo dev;
     int st = current_device(&dev);
     if (st) return st;
-    unsigned long long v[2] = {0ull, 0ull};
+    unsigned long long v[2] = {0ull, 0ull}, o[2] = {0ull, 0ull};
     if ((st = cuda_status(read_status(v, stream)))) return st;
-    *out = static_cast<int64_t>(v[which]);
+    if ((st = cuda_status(read_objective_status(o, stream)))) return st;
+    *out = static_cast<int64_t>(v[which] + o[which]);
     return CE_OK;
 }
 
@@ -758,7 +940,8 @@ int ce_device_error_reset(ce_stream_t stream) {
     DeviceInfo dev;
     int st = current_device(&dev);
     if (st) return st;
-    return cuda_status(reset_status(stream));
+    if ((st = cuda_status(reset_status(stream)))) return st;
+    return cuda_status(reset_objective_status(stream));
 }
 
 int ce_debug_force(int path, int cluster, int threads) {

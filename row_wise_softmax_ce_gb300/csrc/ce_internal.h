@@ -90,6 +90,60 @@ struct Args {
     const uint64_t *row_at;  // rows given by address (argmaxInto's indirect form), or null
 };
 
+// -- the objectives over sampled answers (ce_objectives.cu) ---------------------
+enum DType : int { kF32 = 0, kBF16 = 1, kF16 = 2 };
+// What a forward kernel writes of a row beside its log-probability.
+enum ObjMode : int { kObjLogp = 0, kObjPolicy = 1, kObjPreference = 2 };
+
+// Arguments of one launch; unused pointers are null.
+struct ObjArgs {
+    const void *logits;
+    int64_t rows;
+    int vocab;
+    int64_t stride;
+    const int64_t *labels;
+    const float *weights;  // null: every row counts 1; a row of weight 0 is not read
+    float k, inv_t;        // log2(e) / T, 1 / T
+    float scale;
+    float *loss, *logp, *entropy;  // [rows]
+    void *grad;
+    int64_t grad_stride;
+    // policy
+    const float *old_logp, *ref_logp, *adv;
+    float clip_lo, clip_hi, kl, bonus;
+    // preference: sequence s is rows offsets[s] .. offsets[s + 1] - 1
+    const int64_t *offsets;
+    int64_t pairs;
+    float4 *row_state;  // [rows] (m, 1 / s, factor, -)
+    uint32_t *done;     // join CTAs that have written their pairs
+};
+
+// The join of a preference batch's rows into sequences, pairs and the loss.
+struct JoinArgs {
+    const float *logp, *weights;  // [rows]
+    int64_t rows;
+    const int64_t *offsets;
+    int64_t pairs;
+    const float *ref_seq;  // [2 pairs] or null
+    int kind;
+    bool average;
+    double beta, smoothing, margin, scale, inv_t;
+    float *seq_logp, *loss_pairs, *loss;
+    float4 *row_state;  // null: forward only
+    uint32_t *done;
+};
+
+cudaError_t set_objective_attributes(const DeviceInfo &dev);
+cudaError_t launch_obj_rows(DType t, ObjMode mode, const ObjArgs &a, const DeviceInfo &dev, cudaStream_t s);
+cudaError_t launch_policy_grad(DType t, const ObjArgs &a, const DeviceInfo &dev, cudaStream_t s);
+cudaError_t launch_join(const JoinArgs &j, const DeviceInfo &dev, cudaStream_t s);
+cudaError_t launch_preference_grad(DType t, const ObjArgs &a, const DeviceInfo &dev, cudaStream_t s);
+// *out = scale * sum of weights[i] * loss[i] (weights null: 1), summed in f64
+cudaError_t launch_weighted_sum(const float *loss, const float *weights, int64_t rows, double scale, float *out,
+                                cudaStream_t s);
+cudaError_t read_objective_status(unsigned long long out[2], cudaStream_t s);
+cudaError_t reset_objective_status(cudaStream_t s);
+
 cudaError_t set_kernel_attributes(const DeviceInfo &dev);
 cudaError_t max_active_clusters(const Plan &p, Op op, int *n);
 

@@ -1,0 +1,580 @@
+// ce_objectives.cu -- sm_103a kernels of the objectives over sampled answers
+// and over pairs of answers, and their launchers.
+//
+//   logp_rows        logp = (x_y - m) / T - log s, H = log s - u / (T s)
+//   policy_loss      + the clipped loss of exp(logp - old), the KL term, the
+//   policy_step        entropy bonus; its gradient e (a + b (x - m)) + [y] c
+//   preference_loss  rows -> sequences -> pairs -> loss; the gradient of a
+//   preference_step    row is its pair's factor times ([y] - p)
+//
+// Kernels (all bound by HBM; none uses tensor cores):
+//   k_obj_rows       one read of each logit: log-probability, entropy and the
+//                    policy's loss of a row
+//   k_policy_stream  the policy's loss and gradient, the row read twice
+//   k_join           a preference batch's rows into sequences, pairs, the loss
+//                    and each row's gradient factor
+//   k_pair_grad      the gradient of a preference batch, the rows read again
+//   k_weighted_sum   the policy's loss, an f64 fixed-shape tree over a cluster
+#include <algorithm>
+#include <cstdint>
+
+#include "ce_internal.h"
+#include "ce_objectives.cuh"
+
+namespace cerows {
+
+namespace {
+
+// [0] rows with a bad label and pairs with a bad range; [1] bounded waits that gave up
+__device__ unsigned long long g_objective_status[2];
+
+constexpr int kRowsThreads = 256;
+constexpr int kRowsUnroll = 4;       // 16-byte loads in flight per thread
+constexpr int kRowsMinBytes = 8192;  // bytes of a row per CTA, at least, when a row is split
+
+__device__ __forceinline__ bool in_range(int64_t label, int vocab) { return label >= 0 && label < vocab; }
+
+// ---------------------------------------------------------------------------
+// k_obj_rows: one cluster of C CTAs per row (looping), each a contiguous slice
+// of `cols` columns; their states meet by pushes and CTA 0 writes the row.
+template <typename T, int kMode, bool kEnt>
+__global__ void __launch_bounds__(kRowsThreads, 4) k_obj_rows(ObjArgs a, int cols) {
+    __shared__ TokState red[32];
+    __shared__ PushXchg xg;
+    launch_dependents();
+    const uint32_t rank = cluster_rank(), C = cluster_size();
+    const int tid = threadIdx.x;
+    const int c0 = static_cast<int>(rank) * cols;
+    const int n = max(0, min(a.vocab, c0 + cols) - c0);
+    const int64_t cid = cluster_id_x(), G = cluster_count_x();
+    const int64_t K = cid < a.rows ? (a.rows - 1 - cid) / G + 1 : 0;
+    int64_t first = 0, last = a.rows;
+    if (kMode == kObjPreference) {
+        // rows before the first sequence and behind the last take no part
+        first = a.offsets[0];
+        last = a.offsets[2 * a.pairs];
+        if (blockIdx.x == 0 && tid == 0) *a.done = 0;
+    }
+    if (tid == 0) push_xchg_init(xg, K, C);
+    __syncthreads();
+    cluster_arrive();  // every CTA's slots exist before a peer pushes: the wait comes before the first push
+    bool failed = false;
+    int64_t used = 0;
+    for (int64_t row = cid; row < a.rows; row += G) {
+        const float w = a.weights ? a.weights[row] : 1.0f;
+        if (w == 0.0f || (kMode == kObjPreference && (row < first || row >= last))) {
+            if (rank == 0 && tid == 0) {
+                a.logp[row] = 0.0f;
+                if (kEnt && a.entropy) a.entropy[row] = 0.0f;
+                if (kMode == kObjPolicy) a.loss[row] = 0.0f;
+                if (kMode == kObjPreference && a.row_state) a.row_state[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            continue;
+        }
+        const T *p = static_cast<const T *>(a.logits) + row * a.stride;
+        // the row's numbers, fetched early by the thread that writes it
+        float xl = 0.0f, old = 0.0f, ref = 0.0f, adv = 0.0f;
+        bool lab_ok = true;
+        if (rank == 0 && tid == 0) {
+            const int64_t label = a.labels[row];
+            lab_ok = in_range(label, a.vocab);
+            if (lab_ok) xl = Vec<T>::to_float(p[label]);
+            if (kMode == kObjPolicy) {
+                old = a.old_logp[row];
+                adv = a.adv[row];
+                if (a.ref_logp) ref = a.ref_logp[row];
+            }
+        }
+        TokState st = n > 0 ? tok_scan<T, kEnt, kRowsUnroll>(p + c0, n, a.k, tid, kRowsThreads) : tok_empty();
+        st = tok_block_reduce_w0<kEnt>(st, red, a.k);
+        if (used == 0) cluster_wait();
+        if (tid == 0) tok_publish(xg, used, rank, C, st, 0.0f);
+        if (tid < 32) {
+            float unused;
+            const TokState g = tok_collect<kEnt>(xg, used, K, C, 0u, &unused, a.k, &failed);
+            if (rank == 0 && tid == 0) {
+                TokRow r;
+                if (kMode == kObjPolicy) {
+                    r = policy_row<kEnt>(a, g, xl, lab_ok, w, adv, old, ref);
+                    a.loss[row] = r.loss;
+                } else {
+                    float log_s;
+                    r = tok_row<kEnt>(g, xl, lab_ok, a.inv_t, &log_s);
+                }
+                a.logp[row] = r.logp;
+                if (kEnt && a.entropy) a.entropy[row] = r.entropy;
+                if (kMode == kObjPreference && a.row_state)
+                    a.row_state[row] = make_float4(g.m, 1.0f / g.s, 0.0f, 0.0f);
+                if (!lab_ok) atomicAdd(&g_objective_status[0], 1ull);
+            }
+        }
+        ++used;
+        __syncthreads();  // red is rewritten for the next row
+    }
+    if (used == 0) cluster_wait();  // the first arrive's match, for a cluster that read no row
+    cluster_arrive();               // no CTA leaves while a peer may still push to it
+    cluster_wait();
+    if (__syncthreads_or(failed) && tid == 0) atomicAdd(&g_objective_status[1], 1ull);
+}
+
+// ---------------------------------------------------------------------------
+// Writing a slice of a gradient row: columns [0, n) at g from the logits at p
+// (coherent loads: g may be p), the label's column `lab` (-1: elsewhere)
+// getting c besides. 16-byte loads and stores where the two share their phase
+// of 16 bytes, single elements otherwise.
+template <typename T, bool kB>
+__device__ __forceinline__ void write_slice(const T *p, T *g, int n, float m, float k, float a, float b, float c,
+                                            int lab, int tid, int nt) {
+    constexpr int N = Vec<T>::kN;
+    const int offp = static_cast<int>((reinterpret_cast<uintptr_t>(p) / sizeof(T)) % N);
+    const int offg = static_cast<int>((reinterpret_cast<uintptr_t>(g) / sizeof(T)) % N);
+    auto one = [&](int j) {
+        const float x = Vec<T>::to_float(p[j]);
+        g[j] = Vec<T>::from_float(j == lab ? tok_label1<kB>(x, m, k, a, b, c) : tok_grad1<kB>(x, m, k, a, b));
+    };
+    int head = n, nvec = 0;
+    if (offp == offg) {
+        head = min(n, (N - offp) % N);
+        nvec = (n - head) / N;
+    }
+    for (int j = tid; j < head; j += nt) one(j);
+    const uint4 *pv = reinterpret_cast<const uint4 *>(p + head);
+    uint4 *gv = reinterpret_cast<uint4 *>(g + head);
+    for (int q = tid; q < nvec; q += nt) {
+        const uint4 v = __ldcs(pv + q);
+        const unsigned l = static_cast<unsigned>(lab - head - N * q);
+        const uint4 o = tok_grad_vec<T, kB>(v, m, k, a, b);
+        if (l < N) {
+            T e[N];
+            *reinterpret_cast<uint4 *>(e) = o;
+            e[l] = Vec<T>::from_float(tok_label1<kB>(Vec<T>::to_float(p[head + N * q + l]), m, k, a, b, c));
+            __stcs(gv + q, *reinterpret_cast<const uint4 *>(e));
+        } else {
+            __stcs(gv + q, o);
+        }
+    }
+    for (int j = head + N * nvec + tid; j < n; j += nt) one(j);
+}
+
+template <typename T>
+__device__ __forceinline__ void zero_slice(T *g, int n, int tid, int nt) {
+    constexpr int N = Vec<T>::kN;
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(g) / sizeof(T)) % N);
+    const int head = min(n, (N - off) % N), nvec = (n - head) / N;
+    const T zero = Vec<T>::from_float(0.0f);
+    for (int j = tid; j < head; j += nt) g[j] = zero;
+    uint4 *gv = reinterpret_cast<uint4 *>(g + head);
+    for (int q = tid; q < nvec; q += nt) __stcs(gv + q, make_uint4(0u, 0u, 0u, 0u));
+    for (int j = head + N * nvec + tid; j < n; j += nt) g[j] = zero;
+}
+
+// ---------------------------------------------------------------------------
+// k_policy_stream: the policy's loss and gradient; the cluster's CTAs read
+// their slices twice (state, then gradient).
+template <typename T, bool kEnt>
+__global__ void __launch_bounds__(kRowsThreads, 4) k_policy_stream(ObjArgs a, int cols) {
+    __shared__ TokState red[32];
+    __shared__ PushXchg xg;
+    __shared__ float4 bc;
+    launch_dependents();
+    const uint32_t rank = cluster_rank(), C = cluster_size();
+    const int tid = threadIdx.x;
+    const int c0 = static_cast<int>(rank) * cols;
+    const int n = max(0, min(a.vocab, c0 + cols) - c0);
+    const int64_t cid = cluster_id_x(), G = cluster_count_x();
+    const int64_t K = cid < a.rows ? (a.rows - 1 - cid) / G + 1 : 0;
+    if (tid == 0) push_xchg_init(xg, K, C);
+    __syncthreads();
+    cluster_arrive();
+    bool failed = false;
+    int64_t used = 0;
+    for (int64_t row = cid; row < a.rows; row += G) {
+        const T *p = static_cast<const T *>(a.logits) + row * a.stride + c0;
+        T *g = static_cast<T *>(a.grad) + row * a.grad_stride + c0;
+        const float w = a.weights ? a.weights[row] : 1.0f;
+        if (w == 0.0f) {
+            zero_slice(g, n, tid, kRowsThreads);
+            if (rank == 0 && tid == 0) {
+                a.logp[row] = 0.0f;
+                a.loss[row] = 0.0f;
+                if (kEnt && a.entropy) a.entropy[row] = 0.0f;
+            }
+            continue;
+        }
+        const int64_t label = a.labels[row];
+        const bool lab_ok = in_range(label, a.vocab);
+        const int lab = lab_ok && label >= c0 && label < c0 + n ? static_cast<int>(label - c0) : -1;
+        float xl = 0.0f, old = 0.0f, ref = 0.0f, adv = 0.0f;
+        if (tid == 0) {
+            if (lab >= 0) xl = Vec<T>::to_float(p[lab]);  // before any CTA of the cluster writes (grad may be logits)
+            old = a.old_logp[row];
+            adv = a.adv[row];
+            if (a.ref_logp) ref = a.ref_logp[row];
+        }
+        TokState st = n > 0 ? tok_scan<T, kEnt, kRowsUnroll>(p, n, a.k, tid, kRowsThreads) : tok_empty();
+        st = tok_block_reduce_w0<kEnt>(st, red, a.k);
+        if (used == 0) cluster_wait();
+        if (tid == 0) tok_publish(xg, used, rank, C, st, xl);
+        if (tid < 32) {
+            const uint32_t owner = lab_ok ? static_cast<uint32_t>(label) / static_cast<uint32_t>(cols) : 0u;
+            const TokState s = tok_collect<kEnt>(xg, used, K, C, owner, &xl, a.k, &failed);
+            if (tid == 0) {
+                const TokRow r = policy_row<kEnt>(a, s, xl, lab_ok, w, adv, old, ref);
+                bc = make_float4(r.m, r.a, r.b, r.c);
+                if (rank == 0) {
+                    a.logp[row] = r.logp;
+                    a.loss[row] = r.loss;
+                    if (kEnt && a.entropy) a.entropy[row] = r.entropy;
+                    if (!lab_ok) atomicAdd(&g_objective_status[0], 1ull);
+                }
+            }
+        }
+        ++used;
+        __syncthreads();
+        const float4 f = bc;
+        write_slice<T, kEnt>(p, g, n, f.x, a.k, f.y, f.z, f.w, lab, tid, kRowsThreads);
+        __syncthreads();  // bc and red are rewritten for the next row
+    }
+    if (used == 0) cluster_wait();
+    cluster_arrive();
+    cluster_wait();
+    if (__syncthreads_or(failed) && tid == 0) atomicAdd(&g_objective_status[1], 1ull);
+}
+
+// ---------------------------------------------------------------------------
+// k_join: one CTA per pair (looping). Half of its threads sum the chosen
+// sequence's w logp (and w, for averages) in f64, half the rejected's, each in
+// a fixed order; one thread forms the pair's loss and the factors
+// dloss / dlogp of the two sequences' rows. The CTA that finishes last adds
+// the pairs' losses up, again in a fixed order.
+constexpr int kJoinThreads = 256;
+
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+    return v;
+}
+
+// log(1 + exp(x))
+__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))); }
+__device__ __forceinline__ float sigmoid(float x) {
+    const float e = expf(-fabsf(x));
+    return (x >= 0.0f ? 1.0f : e) / (1.0f + e);
+}
+
+__global__ void __launch_bounds__(kJoinThreads) k_join(JoinArgs j) {
+    __shared__ double part[2][2][kJoinThreads / 64];  // [sequence][sum, count][warp]
+    __shared__ float factor[2];
+    __shared__ bool last;
+    launch_dependents();
+    wait_prerequisites();
+    constexpr int kHalf = kJoinThreads / 2;
+    const int side = threadIdx.x / kHalf, t = threadIdx.x % kHalf, lane = t & 31, warp = t >> 5;
+    const int64_t P = j.pairs;
+    for (int64_t pair = blockIdx.x; pair < P; pair += gridDim.x) {
+        const int64_t s = side == 0 ? pair : P + pair;
+        const int64_t r0 = j.offsets[s], r1 = j.offsets[s + 1];
+        const bool ok = r0 >= 0 && r0 <= r1 && r1 <= j.rows;
+        double sum = 0.0, count = 0.0;
+        if (ok) {
+#pragma unroll 4
+            for (int64_t r = r0 + t; r < r1; r += kHalf) {
+                const float w = j.weights ? j.weights[r] : 1.0f;
+                if (w != 0.0f) sum += static_cast<double>(w) * static_cast<double>(j.logp[r]);
+                if (j.average) count += static_cast<double>(w);
+            }
+        } else {
+            sum = static_cast<double>(nan_f());
+        }
+        sum = warp_sum(sum);
+        if (j.average) count = warp_sum(count);
+        if (lane == 0) {
+            part[side][0][warp] = sum;
+            part[side][1][warp] = count;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            double L[2], per[2];
+            for (int q = 0; q < 2; ++q) {
+                double v = 0.0, c = 0.0;
+                for (int i = 0; i < kHalf / 32; ++i) v += part[q][0][i], c += part[q][1][i];
+                per[q] = j.average ? (c != 0.0 ? 1.0 / c : 0.0) : 1.0;
+                L[q] = v * per[q];
+                j.seq_logp[q == 0 ? pair : P + pair] = static_cast<float>(L[q]);
+            }
+            double h = L[0] - L[1];
+            if (j.ref_seq) h -= static_cast<double>(j.ref_seq[pair]) - static_cast<double>(j.ref_seq[P + pair]);
+            float loss, dh;
+            if (j.kind == 2) {
+                const double off = h - j.margin - 0.5 / j.beta;
+                loss = static_cast<float>(off * off);
+                dh = static_cast<float>(2.0 * off);
+            } else {
+                const float z = static_cast<float>(j.beta * h - j.margin), beta = static_cast<float>(j.beta);
+                if (j.kind == 1) {
+                    // NaN z: NaN, not the 0 of fmaxf
+                    loss = z < 1.0f ? 1.0f - z : z - z;
+                    dh = z < 1.0f ? -beta : z - z;
+                    if (z == INFINITY) loss = dh = 0.0f;
+                } else {
+                    const float eps = static_cast<float>(j.smoothing);
+                    loss = (1.0f - eps) * softplus(-z);
+                    dh = -beta * (1.0f - eps) * sigmoid(-z);
+                    if (eps != 0.0f) {
+                        loss += eps * softplus(z);
+                        dh += beta * eps * sigmoid(z);
+                    }
+                }
+            }
+            j.loss_pairs[pair] = loss;
+            const double f = static_cast<double>(dh) * j.scale * j.inv_t;
+            factor[0] = static_cast<float>(f * per[0]);
+            factor[1] = static_cast<float>(-f * per[1]);
+        }
+        __syncthreads();
+        if (!ok && t == 0) atomicAdd(&g_objective_status[0], 1ull);
+        if (j.row_state && ok) {
+            const float f = factor[side];
+            for (int64_t r = r0 + t; r < r1; r += kHalf) {
+                const float w = j.weights ? j.weights[r] : 1.0f;
+                if (w != 0.0f) j.row_state[r].z = f * w;
+            }
+        }
+    }
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(j.done, 1u) == gridDim.x - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    double sum = 0.0;
+    for (int64_t i = threadIdx.x; i < P; i += kJoinThreads) sum += static_cast<double>(__ldcg(j.loss_pairs + i));
+    sum = warp_sum(sum);
+    if (lane == 0) part[side][0][warp] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double v = 0.0;
+        for (int q = 0; q < 2; ++q)
+            for (int i = 0; i < kHalf / 32; ++i) v += part[q][0][i];
+        *j.loss = static_cast<float>(v * j.scale);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// k_pair_grad: factor ([y] - p) of every row, a CTA per part of kPartBytes of
+// a row. Rows whose factor is 0 (no weight, or in no sequence) are written as
+// zeros without being read.
+constexpr int kPartBytes = 32768;
+
+template <typename T>
+__global__ void __launch_bounds__(256) k_pair_grad(ObjArgs a, int parts) {
+    constexpr int kCols = kPartBytes / static_cast<int>(sizeof(T));
+    wait_prerequisites();
+    const int64_t unit = static_cast<int64_t>(gridDim.x) - 1 - blockIdx.x;
+    const int64_t row = unit / parts;
+    const int c0 = static_cast<int>(unit % parts) * kCols;
+    const int n = min(a.vocab - c0, kCols);
+    T *g = static_cast<T *>(a.grad) + row * a.grad_stride + c0;
+    const float4 st = a.row_state[row];
+    if (st.z == 0.0f) {
+        zero_slice(g, n, threadIdx.x, 256);
+        return;
+    }
+    const T *p = static_cast<const T *>(a.logits) + row * a.stride + c0;
+    const int64_t label = a.labels[row] - c0;
+    const int lab = label >= 0 && label < n ? static_cast<int>(label) : -1;
+    const bool bad = !isfinite(st.x);
+    write_slice<T, false>(p, g, n, st.x, a.k, bad ? nan_f() : -st.z * st.y, 0.0f, st.z, lab, threadIdx.x, 256);
+}
+
+// ---------------------------------------------------------------------------
+// k_weighted_sum: one cluster, the shape of the mean loss's kernel.
+constexpr int kSumCtas = 8;
+constexpr int kSumThreads = 256;
+
+__global__ void __launch_bounds__(kSumThreads) k_weighted_sum(const float *__restrict__ loss,
+                                                              const float *__restrict__ weights, int64_t rows,
+                                                              double scale, float *__restrict__ out) {
+    __shared__ double warp_part[kSumThreads / 32];
+    __shared__ double cta_part[kSumCtas];
+    cluster_arrive();      // every CTA has started before CTA 0's shared memory is written
+    wait_prerequisites();  // the row losses are complete and visible
+    const uint32_t rank = cluster_rank();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    double s = 0.0;
+    for (int64_t i = static_cast<int64_t>(rank) * kSumThreads + tid; i < rows; i += kSumCtas * kSumThreads) {
+        const double l = static_cast<double>(loss[i]);
+        s += weights ? static_cast<double>(weights[i]) * l : l;
+    }
+    s = warp_sum(s);
+    if (lane == 0) warp_part[warp] = s;
+    __syncthreads();
+    cluster_wait();
+    if (warp == 0) {
+        const double r = warp_sum(lane < kSumThreads / 32 ? warp_part[lane] : 0.0);
+        if (lane == 0) st_dsmem_f64(peer_smem(&cta_part[rank], 0), r);
+    }
+    cluster_arrive_release();
+    cluster_wait();
+    if (rank == 0 && warp == 0) {
+        const double r = warp_sum(lane < kSumCtas ? cta_part[lane] : 0.0);
+        if (lane == 0) *out = static_cast<float>(r * scale);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// launchers
+
+struct LaunchConfig {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    LaunchConfig(int64_t ctas, int threads, int cluster, bool dependent, cudaStream_t s, int smem = 0) {
+        cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+        cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+        cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+        cfg.stream = s;
+        int n = 0;
+        if (cluster > 0) {
+            attr[n].id = cudaLaunchAttributeClusterDimension;
+            attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+            attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+            ++n;
+        }
+        if (dependent) {
+            attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[n].val.programmaticStreamSerializationAllowed = 1;
+            ++n;
+        }
+        cfg.attrs = attr;
+        cfg.numAttrs = n;
+    }
+};
+
+template <typename T>
+const void *rows_kernel_t(ObjMode mode, bool ent) {
+    if (mode == kObjPreference) return reinterpret_cast<const void *>(&k_obj_rows<T, kObjPreference, false>);
+    if (mode == kObjPolicy)
+        return ent ? reinterpret_cast<const void *>(&k_obj_rows<T, kObjPolicy, true>)
+                   : reinterpret_cast<const void *>(&k_obj_rows<T, kObjPolicy, false>);
+    return ent ? reinterpret_cast<const void *>(&k_obj_rows<T, kObjLogp, true>)
+               : reinterpret_cast<const void *>(&k_obj_rows<T, kObjLogp, false>);
+}
+
+const void *rows_kernel(DType t, ObjMode mode, bool ent) {
+    return t == kF32    ? rows_kernel_t<float>(mode, ent)
+           : t == kBF16 ? rows_kernel_t<__nv_bfloat16>(mode, ent)
+                        : rows_kernel_t<__half>(mode, ent);
+}
+
+template <typename T>
+const void *policy_stream_t(bool ent) {
+    return ent ? reinterpret_cast<const void *>(&k_policy_stream<T, true>)
+               : reinterpret_cast<const void *>(&k_policy_stream<T, false>);
+}
+
+const void *policy_stream(DType t, bool ent) {
+    return t == kF32    ? policy_stream_t<float>(ent)
+           : t == kBF16 ? policy_stream_t<__nv_bfloat16>(ent)
+                        : policy_stream_t<__half>(ent);
+}
+
+int elem_size(DType t) { return t == kF32 ? 4 : 2; }
+
+bool wants_entropy(const ObjArgs &a) { return a.entropy != nullptr || a.bonus != 0.0f; }
+
+// CTAs per row: rows are split until there are about four and a half CTAs per
+// SM, down to kRowsMinBytes each
+int split_of(DType t, int64_t rows, int64_t vocab, const DeviceInfo &dev) {
+    if (rows >= 3 * static_cast<int64_t>(dev.sms)) return 1;
+    int64_t c = (9 * static_cast<int64_t>(dev.sms) + 2 * rows - 1) / (2 * std::max<int64_t>(1, rows));
+    c = std::min<int64_t>(c, (vocab * elem_size(t) + kRowsMinBytes - 1) / kRowsMinBytes);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(c, kMaxCluster)));
+}
+
+int cols_of(int64_t vocab, int c) { return static_cast<int>(((vocab + c - 1) / c + 7) & ~int64_t(7)); }
+
+}  // namespace
+
+cudaError_t set_objective_attributes(const DeviceInfo &) {
+    for (DType t : {kF32, kBF16, kF16})
+        for (bool ent : {false, true}) {
+            for (ObjMode m : {kObjLogp, kObjPolicy, kObjPreference}) {
+                cudaError_t e = cudaFuncSetAttribute(rows_kernel(t, m, ent), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+                if (e != cudaSuccess) return e;
+            }
+            cudaError_t e = cudaFuncSetAttribute(policy_stream(t, ent), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+        }
+    return cudaSuccess;
+}
+
+cudaError_t launch_obj_rows(DType t, ObjMode mode, const ObjArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+    const int c = split_of(t, a.rows, a.vocab, dev);
+    const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(a.rows, int64_t(1) << 20));
+    ObjArgs aa = a;
+    int cols = cols_of(a.vocab, c);
+    void *args[] = {&aa, &cols};
+    LaunchConfig l(clusters * c, kRowsThreads, c, false, s);
+    return cudaLaunchKernelExC(&l.cfg, rows_kernel(t, mode, wants_entropy(a)), args);
+}
+
+cudaError_t launch_policy_grad(DType t, const ObjArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+    const int c = split_of(t, a.rows, a.vocab, dev);
+    const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(a.rows, int64_t(1) << 20));
+    ObjArgs aa = a;
+    int cols = cols_of(a.vocab, c);
+    void *args[] = {&aa, &cols};
+    LaunchConfig l(clusters * c, kRowsThreads, c, false, s);
+    return cudaLaunchKernelExC(&l.cfg, policy_stream(t, wants_entropy(a)), args);
+}
+
+cudaError_t launch_join(const JoinArgs &j, const DeviceInfo &dev, cudaStream_t s) {
+    const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(j.pairs, 8 * static_cast<int64_t>(dev.sms)));
+    JoinArgs jj = j;
+    void *args[] = {&jj};
+    LaunchConfig l(ctas, kJoinThreads, 0, true, s);
+    return cudaLaunchKernelExC(&l.cfg, reinterpret_cast<const void *>(&k_join), args);
+}
+
+cudaError_t launch_preference_grad(DType t, const ObjArgs &a, const DeviceInfo &, cudaStream_t s) {
+    const int cols = kPartBytes / elem_size(t);
+    int parts = (a.vocab + cols - 1) / cols;
+    const void *fn = t == kF32    ? reinterpret_cast<const void *>(&k_pair_grad<float>)
+                     : t == kBF16 ? reinterpret_cast<const void *>(&k_pair_grad<__nv_bfloat16>)
+                                  : reinterpret_cast<const void *>(&k_pair_grad<__half>);
+    // at most 2^31 - 1 CTAs in one launch: more parts than that are written by further launches
+    const int64_t most = ((int64_t(1) << 31) - 1) / parts;
+    for (int64_t r0 = 0; r0 < a.rows; r0 += most) {
+        ObjArgs aa = a;
+        aa.rows = std::min(most, a.rows - r0);
+        aa.logits = static_cast<const char *>(a.logits) + r0 * a.stride * elem_size(t);
+        aa.grad = static_cast<char *>(a.grad) + r0 * a.grad_stride * elem_size(t);
+        aa.labels = a.labels + r0;
+        aa.row_state = a.row_state + r0;
+        void *args[] = {&aa, &parts};
+        LaunchConfig l(aa.rows * parts, 256, 0, r0 == 0, s);
+        cudaError_t e = cudaLaunchKernelExC(&l.cfg, fn, args);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_weighted_sum(const float *loss, const float *weights, int64_t rows, double scale, float *out,
+                                cudaStream_t s) {
+    LaunchConfig l(kSumCtas, kSumThreads, kSumCtas, true, s);
+    return cudaLaunchKernelEx(&l.cfg, k_weighted_sum, loss, weights, rows, scale, out);
+}
+
+cudaError_t read_objective_status(unsigned long long out[2], cudaStream_t s) {
+    cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_objective_status, sizeof(unsigned long long) * 2, 0,
+                                              cudaMemcpyDeviceToHost, s);
+    if (e != cudaSuccess) return e;
+    return cudaStreamSynchronize(s);
+}
+
+cudaError_t reset_objective_status(cudaStream_t s) {
+    static const unsigned long long zero[2] = {0ull, 0ull};
+    return cudaMemcpyToSymbolAsync(g_objective_status, zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
+}
+
+}  // namespace cerows
