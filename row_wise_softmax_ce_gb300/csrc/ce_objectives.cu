@@ -10,7 +10,8 @@
 // Kernels (all bound by HBM; none uses tensor cores):
 //   k_obj_rows       one read of each logit: log-probability, entropy and the
 //                    policy's loss of a row
-//   k_policy_stream  the policy's loss and gradient, the row read twice
+//   k_policy_staged  the policy's loss and gradient, rows held in shared memory
+//   k_policy_stream  the same for rows too long to hold: read three times
 //   k_join           a preference batch's rows into sequences, pairs, the loss
 //                    and each row's gradient factor
 //   k_pair_grad      the gradient of a preference batch, the rows read again
@@ -31,6 +32,7 @@ __device__ unsigned long long g_objective_status[2];
 constexpr int kRowsThreads = 256;
 constexpr int kRowsUnroll = 4;       // 16-byte loads in flight per thread
 constexpr int kRowsMinBytes = 8192;  // bytes of a row per CTA, at least, when a row is split
+constexpr int kStagedSliceBytes = 55264;  // staged slices of which four CTAs fit an SM
 
 __device__ __forceinline__ bool in_range(int64_t label, int vocab) { return label >= 0 && label < vocab; }
 
@@ -239,6 +241,222 @@ __global__ void __launch_bounds__(kRowsThreads, 4) k_policy_stream(ObjArgs a, in
     cluster_arrive();
     cluster_wait();
     if (__syncthreads_or(failed) && tid == 0) atomicAdd(&g_objective_status[1], 1ull);
+}
+
+// ---------------------------------------------------------------------------
+// k_policy_staged: the policy's loss and gradient with each logit read once
+// from HBM, rows held in shared memory, clusters persistent over rows.
+//
+// CTA `rank` of a cluster owns columns [c0, c0 + n) of the cluster's rows. A
+// slice sits in shared memory on the 16-byte grid of the logits: element i of
+// buf holds column c0 - off + i, off = the slice's start modulo 16 bytes. Its
+// aligned body arrives by one bulk copy; the at most two partial end vectors
+// are loaded by the threads that own them, with -inf outside the slice. Per
+// row: one sweep for (m, s, u); the states of the cluster's CTAs meet by
+// pushes; every CTA forms the row's factors from the same bits; the gradient
+// is written from shared memory; then the copy of the next row that counts
+// starts, its latency hidden behind the SM's other CTAs.
+struct alignas(16) PolicyHeader {
+    PushXchg xg;
+    uint64_t bar;
+    float xl;
+    float4 bc;
+    TokState red[32];
+};
+constexpr int kPolicyHeaderBytes = 1152;
+static_assert(sizeof(PolicyHeader) <= kPolicyHeaderBytes && kPolicyHeaderBytes % 128 == 0, "staged header");
+
+// A 16-byte vector of grid index q: the slice's columns, -inf elsewhere.
+template <typename T>
+__device__ __forceinline__ uint4 load_edge(const T *p, int off, int n, int q) {
+    constexpr int N = Vec<T>::kN;
+    T v[N];
+#pragma unroll
+    for (int l = 0; l < N; ++l) {
+        const int i = N * q + l - off;  // column - c0
+        v[l] = i >= 0 && i < n ? p[i] : Vec<T>::from_float(-INFINITY);
+    }
+    return *reinterpret_cast<const uint4 *>(v);
+}
+
+// The 16 bytes of elements i .. i + N - 1 of a shared-memory buffer, at any
+// phase: four words, or five shifted by half a word.
+template <typename T>
+__device__ __forceinline__ uint4 ld_shifted(const T *buf, int i) {
+    if (sizeof(T) == 4) {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(buf) + i;
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(buf) + (i >> 1);
+    if ((i & 1) == 0) return make_uint4(w[0], w[1], w[2], w[3]);
+    const uint32_t a = w[0], b = w[1], c = w[2], d = w[3], e = w[4];
+    return make_uint4(__funnelshift_r(a, b, 16), __funnelshift_r(b, c, 16), __funnelshift_r(c, d, 16),
+                      __funnelshift_r(d, e, 16));
+}
+
+template <typename T, bool kEnt>
+__global__ void __launch_bounds__(kRowsThreads, 4) k_policy_staged(ObjArgs a, int cols) {
+    constexpr int N = Vec<T>::kN, kT = kRowsThreads, kU = 4;
+    extern __shared__ __align__(128) unsigned char smem[];
+    launch_dependents();
+    PolicyHeader &h = *reinterpret_cast<PolicyHeader *>(smem);
+    T *buf = reinterpret_cast<T *>(smem + kPolicyHeaderBytes);
+    uint4 *bufv = reinterpret_cast<uint4 *>(buf);
+    const uint32_t rank = cluster_rank(), C = cluster_size();
+    const int tid = threadIdx.x;
+    const int c0 = static_cast<int>(rank) * cols;
+    const int n = max(0, min(a.vocab, c0 + cols) - c0);
+    const int64_t cid = cluster_id_x(), G = cluster_count_x();
+    const int64_t K = cid < a.rows ? (a.rows - 1 - cid) / G + 1 : 0;
+    const T *logits = static_cast<const T *>(a.logits) + c0;
+    auto phase_of = [](const T *p) {
+        return static_cast<int>((reinterpret_cast<uintptr_t>(p) / sizeof(T)) % Vec<T>::kN);
+    };
+    auto next_live = [&](int64_t row) {
+        if (a.weights)
+            while (row < a.rows && a.weights[row] == 0.0f) row += G;
+        return row;
+    };
+    // the bulk copy of the aligned body of `row`'s slice
+    uint64_t policy = 0;
+    auto issue = [&](int64_t row) {
+        const T *p = logits + row * a.stride;
+        const int off = phase_of(p);
+        const int head = min(n, (N - off) % N);
+        const int nvec = (n - head) / N;
+        const int qa = (off + head) / N;
+        const uint32_t bytes = static_cast<uint32_t>(nvec) * 16u;
+        mbar_arrive_expect_tx(&h.bar, bytes);
+        if (bytes) bulk_copy_g2s(bufv + qa, p - off + N * qa, bytes, &h.bar, policy);
+    };
+    int64_t ahead = 0;  // thread 0: the row whose copy is issued next
+    if (tid == 0) {
+        mbar_init(&h.bar, 1);
+        fence_mbar_init();
+        push_xchg_init(h.xg, K, C);
+        policy = l2_policy_evict_first();
+        ahead = next_live(cid);
+        if (ahead < a.rows) {
+            issue(ahead);
+            ahead = next_live(ahead + G);
+        }
+    }
+    __syncthreads();
+    cluster_arrive();  // every CTA's slots exist before a peer pushes: the wait comes before the first push
+    bool failed = false;
+    uint32_t parity = 0;
+    int64_t used = 0;
+    // a row's weight and label are loaded one row ahead, off its critical path
+    float w_next = K > 0 && a.weights ? a.weights[cid] : 1.0f;
+    int64_t label_next = K > 0 ? a.labels[cid] : 0;
+    for (int64_t row = cid; row < a.rows; row += G) {
+        const float w = w_next;
+        const int64_t label = label_next;
+        if (row + G < a.rows) {
+            if (a.weights) w_next = a.weights[row + G];
+            label_next = a.labels[row + G];
+        }
+        T *g = static_cast<T *>(a.grad) + row * a.grad_stride + c0;
+        if (w == 0.0f) {
+            zero_slice(g, n, tid, kT);
+            if (rank == 0 && tid == 0) {
+                a.logp[row] = 0.0f;
+                a.loss[row] = 0.0f;
+                if (kEnt && a.entropy) a.entropy[row] = 0.0f;
+            }
+            continue;
+        }
+        const T *p = logits + row * a.stride;
+        const int off = phase_of(p);
+        const int head = min(n, (N - off) % N);
+        const int nvec = (n - head) / N;    // whole body vectors
+        const int qa = (off + head) / N;    // the first of them (0 or 1)
+        const int nq = (off + n + N - 1) / N;  // vectors covering the slice
+        const int qe0 = qa == 1 ? 0 : -1, qe1 = qa + nvec < nq ? qa + nvec : -1;  // partial end vectors
+        if (qe0 >= 0 && tid == 0) bufv[qe0] = load_edge(p, off, n, qe0);
+        if (qe1 >= 0 && (qe1 & (kT - 1)) == tid) bufv[qe1] = load_edge(p, off, n, qe1);
+        float old = 0.0f, ref = 0.0f, adv = 0.0f;
+        if (tid == 0) {
+            old = a.old_logp[row];
+            adv = a.adv[row];
+            if (a.ref_logp) ref = a.ref_logp[row];
+        }
+        const bool lab_ok = in_range(label, a.vocab);
+        const int lab = lab_ok && label >= c0 && label < c0 + n ? static_cast<int>(label - c0) : -1;
+        if (!failed) failed = !mbar_wait_bounded(&h.bar, parity);
+        parity ^= 1u;
+        // the label's logit, by the owner of its vector
+        if (lab >= 0 && (((off + lab) / N) & (kT - 1)) == tid) h.xl = Vec<T>::to_float(buf[off + lab]);
+        TokState st = tok_empty();
+        int q = tid;
+        for (; q + (kU - 1) * kT < nq; q += kU * kT) {
+            uint4 v[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) v[u] = bufv[q + u * kT];
+            tok_push<T, kEnt, kU>(st, v, a.k);
+        }
+        for (; q < nq; q += kT) {
+            const uint4 v[1] = {bufv[q]};
+            tok_push<T, kEnt, 1>(st, v, a.k);
+        }
+        st = tok_block_reduce_w0<kEnt>(st, h.red, a.k);
+        if (used == 0) cluster_wait();
+        if (tid == 0) tok_publish(h.xg, used, rank, C, st, lab >= 0 ? h.xl : 0.0f);
+        if (tid < 32) {
+            float xl;
+            const uint32_t owner = lab_ok ? static_cast<uint32_t>(label) / static_cast<uint32_t>(cols) : 0u;
+            const TokState s = tok_collect<kEnt>(h.xg, used, K, C, owner, &xl, a.k, &failed);
+            if (tid == 0) {
+                const TokRow r = policy_row<kEnt>(a, s, xl, lab_ok, w, adv, old, ref);
+                h.bc = make_float4(r.m, r.a, r.b, r.c);
+                if (rank == 0) {
+                    a.logp[row] = r.logp;
+                    a.loss[row] = r.loss;
+                    if (kEnt && a.entropy) a.entropy[row] = r.entropy;
+                    if (!lab_ok) atomicAdd(&g_objective_status[0], 1ull);
+                }
+            }
+        }
+        ++used;
+        __syncthreads();
+        // the gradient, in 16-byte vectors of its own grid: the logits' own
+        // vectors where the two share their phase, shifted ones otherwise
+        const float4 f = h.bc;
+        const int offg = phase_of(g);
+        const int headg = min(n, (N - offg) % N), nvecg = (n - headg) / N, tailg = n - headg - N * nvecg;
+        uint4 *gv = reinterpret_cast<uint4 *>(g + headg);
+        const T *src = buf + off;  // column c0
+        const bool same = offg == off;
+        for (int i = tid; i < nvecg; i += kT) {
+            const int j = headg + N * i;
+            const uint4 v = same ? bufv[qa + i] : ld_shifted(buf, off + j);
+            const uint4 o = tok_grad_vec<T, kEnt>(v, f.x, a.k, f.y, f.z);
+            const unsigned l = static_cast<unsigned>(lab - j);
+            __stcs(gv + i, o);
+            // the label's element again, by the same thread
+            if (l < N) g[lab] = Vec<T>::from_float(tok_label1<kEnt>(Vec<T>::to_float(src[lab]), f.x, a.k, f.y, f.z, f.w));
+        }
+        if (tid < headg + tailg) {
+            const int j = tid < headg ? tid : N * nvecg + tid;
+            const float x = Vec<T>::to_float(src[j]);
+            g[j] = Vec<T>::from_float(j == lab ? tok_label1<kEnt>(x, f.x, a.k, f.y, f.z, f.w)
+                                               : tok_grad1<kEnt>(x, f.x, a.k, f.y, f.z));
+        }
+        __syncthreads();  // the slice, its edges and the header are free
+        if (tid == 0 && ahead < a.rows) {
+            fence_proxy_async_smem();
+            issue(ahead);
+            ahead = next_live(ahead + G);
+        }
+    }
+    if (used == 0) cluster_wait();
+    cluster_arrive();
+    cluster_wait();
+    if (__syncthreads_or(failed) && tid == 0) {
+        atomicAdd(&g_objective_status[1], 1ull);
+        // give a copy still in flight a last bounded chance to land
+        (void)mbar_wait_bounded(&h.bar, parity ^ 1u, 10000000ull);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -478,6 +696,18 @@ const void *policy_stream(DType t, bool ent) {
                         : policy_stream_t<__half>(ent);
 }
 
+template <typename T>
+const void *policy_staged_t(bool ent) {
+    return ent ? reinterpret_cast<const void *>(&k_policy_staged<T, true>)
+               : reinterpret_cast<const void *>(&k_policy_staged<T, false>);
+}
+
+const void *policy_staged(DType t, bool ent) {
+    return t == kF32    ? policy_staged_t<float>(ent)
+           : t == kBF16 ? policy_staged_t<__nv_bfloat16>(ent)
+                        : policy_staged_t<__half>(ent);
+}
+
 int elem_size(DType t) { return t == kF32 ? 4 : 2; }
 
 bool wants_entropy(const ObjArgs &a) { return a.entropy != nullptr || a.bonus != 0.0f; }
@@ -495,14 +725,19 @@ int cols_of(int64_t vocab, int c) { return static_cast<int>(((vocab + c - 1) / c
 
 }  // namespace
 
-cudaError_t set_objective_attributes(const DeviceInfo &) {
+cudaError_t set_objective_attributes(const DeviceInfo &dev) {
     for (DType t : {kF32, kBF16, kF16})
         for (bool ent : {false, true}) {
             for (ObjMode m : {kObjLogp, kObjPolicy, kObjPreference}) {
                 cudaError_t e = cudaFuncSetAttribute(rows_kernel(t, m, ent), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
                 if (e != cudaSuccess) return e;
             }
-            cudaError_t e = cudaFuncSetAttribute(policy_stream(t, ent), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            for (const void *f : {policy_stream(t, ent), policy_staged(t, ent)}) {
+                cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+                if (e != cudaSuccess) return e;
+            }
+            cudaError_t e = cudaFuncSetAttribute(policy_staged(t, ent), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 dev.max_smem_optin);
             if (e != cudaSuccess) return e;
         }
     return cudaSuccess;
@@ -518,14 +753,41 @@ cudaError_t launch_obj_rows(DType t, ObjMode mode, const ObjArgs &a, const Devic
     return cudaLaunchKernelExC(&l.cfg, rows_kernel(t, mode, wants_entropy(a)), args);
 }
 
+// The staged kernel's shape for c CTAs per row: columns and shared memory per
+// CTA, and the clusters resident at once (0: it does not fit).
+static int staged_active(DType t, bool ent, int64_t vocab, int c, const DeviceInfo &dev, int *cols, int *smem) {
+    const int N = 16 / elem_size(t);
+    *cols = cols_of(vocab, c);
+    *smem = kPolicyHeaderBytes + 16 * ((*cols + 2 * N) / N + 1);
+    if (*smem > dev.max_smem_optin) return 0;
+    LaunchConfig l(c, kRowsThreads, c, false, nullptr, *smem);
+    int active = 0;
+    if (cudaOccupancyMaxActiveClusters(&active, policy_staged(t, ent), &l.cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    return active;
+}
+
 cudaError_t launch_policy_grad(DType t, const ObjArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-    const int c = split_of(t, a.rows, a.vocab, dev);
-    const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(a.rows, int64_t(1) << 20));
+    const bool ent = wants_entropy(a);
     ObjArgs aa = a;
-    int cols = cols_of(a.vocab, c);
+    int cols = 0, smem = 0;
     void *args[] = {&aa, &cols};
-    LaunchConfig l(clusters * c, kRowsThreads, c, false, s);
-    return cudaLaunchKernelExC(&l.cfg, policy_stream(t, wants_entropy(a)), args);
+    const int64_t bytes = static_cast<int64_t>(a.vocab) * elem_size(t);
+    int64_t c = std::max<int64_t>((bytes + kStagedSliceBytes - 1) / kStagedSliceBytes, split_of(t, a.rows, a.vocab, dev));
+    c = std::min<int64_t>(c, kMaxCluster);
+    const int active = staged_active(t, ent, a.vocab, static_cast<int>(c), dev, &cols, &smem);
+    if (active > 0) {
+        const int64_t clusters = a.rows < 32 * static_cast<int64_t>(active) ? a.rows : active;
+        LaunchConfig l(std::min<int64_t>(clusters, int64_t(1) << 20) * c, kRowsThreads, static_cast<int>(c), false, s, smem);
+        return cudaLaunchKernelExC(&l.cfg, policy_staged(t, ent), args);
+    }
+    // rows too long for the shared memory of a cluster
+    c = kMaxCluster;
+    cols = cols_of(a.vocab, static_cast<int>(c));
+    LaunchConfig l(std::min<int64_t>(a.rows, int64_t(1) << 20) * c, kRowsThreads, static_cast<int>(c), false, s);
+    return cudaLaunchKernelExC(&l.cfg, policy_stream(t, ent), args);
 }
 
 cudaError_t launch_join(const JoinArgs &j, const DeviceInfo &dev, cudaStream_t s) {
