@@ -29,10 +29,17 @@ namespace {
 // [0] rows with a bad label and pairs with a bad range; [1] bounded waits that gave up
 __device__ unsigned long long g_objective_status[2];
 
+// Of a forward scan: 128 threads, eight 16-byte loads in flight each, eight
+// CTAs per SM. Measured (us; logp 8192 x 128256 bf16 with entropies, 4096 x
+// 50257 f32): 64 threads x 8 loads 294, 100; 128 x 4 277, 98; 128 x 6 264, 94;
+// 128 x 8 263, 93; 256 x 4 287, 104; 256 x 6 278, 97; the next group loaded
+// before the current one is pushed, 128 x 4 271, 94, 256 x 4 274, 96.
+constexpr int kScanThreads = 128;
+constexpr int kScanUnroll = 8;
 constexpr int kRowsThreads = 256;
 constexpr int kRowsUnroll = 4;       // 16-byte loads in flight per thread
 constexpr int kRowsMinBytes = 8192;  // bytes of a row per CTA, at least, when a row is split
-constexpr int kStagedSliceBytes = 55264;  // staged slices of which four CTAs fit an SM
+constexpr int kStagedThreads = 128;
 
 __device__ __forceinline__ bool in_range(int64_t label, int vocab) { return label >= 0 && label < vocab; }
 
@@ -40,7 +47,7 @@ __device__ __forceinline__ bool in_range(int64_t label, int vocab) { return labe
 // k_obj_rows: one cluster of C CTAs per row (looping), each a contiguous slice
 // of `cols` columns; their states meet by pushes and CTA 0 writes the row.
 template <typename T, int kMode, bool kEnt>
-__global__ void __launch_bounds__(kRowsThreads, 4) k_obj_rows(ObjArgs a, int cols) {
+__global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows(ObjArgs a, int cols) {
     __shared__ TokState red[32];
     __shared__ PushXchg xg;
     launch_dependents();
@@ -57,9 +64,11 @@ __global__ void __launch_bounds__(kRowsThreads, 4) k_obj_rows(ObjArgs a, int col
         last = a.offsets[2 * a.pairs];
         if (blockIdx.x == 0 && tid == 0) *a.done = 0;
     }
-    if (tid == 0) push_xchg_init(xg, K, C);
-    __syncthreads();
-    cluster_arrive();  // every CTA's slots exist before a peer pushes: the wait comes before the first push
+    if (C > 1) {
+        if (tid == 0) push_xchg_init(xg, K, C);
+        __syncthreads();
+        cluster_arrive();  // every CTA's slots exist before a peer pushes: the wait comes before the first push
+    }
     bool failed = false;
     int64_t used = 0;
     for (int64_t row = cid; row < a.rows; row += G) {
@@ -74,49 +83,54 @@ __global__ void __launch_bounds__(kRowsThreads, 4) k_obj_rows(ObjArgs a, int col
             continue;
         }
         const T *p = static_cast<const T *>(a.logits) + row * a.stride;
-        // the row's numbers, fetched early by the thread that writes it
         float xl = 0.0f, old = 0.0f, ref = 0.0f, adv = 0.0f;
         bool lab_ok = true;
-        if (rank == 0 && tid == 0) {
+        // the row's numbers, by the thread that writes it. Not before the scan's
+        // first loads: its warp would wait for the label before it asked for
+        // logits, and the CTA for its warp (8192 x 128256: 300 -> 439 us)
+        auto numbers = [&] {
+            if (rank != 0 || tid != 0) return;
             const int64_t label = a.labels[row];
-            lab_ok = in_range(label, a.vocab);
-            if (lab_ok) xl = Vec<T>::to_float(p[label]);
             if (kMode == kObjPolicy) {
                 old = a.old_logp[row];
                 adv = a.adv[row];
                 if (a.ref_logp) ref = a.ref_logp[row];
             }
-        }
-        TokState st = n > 0 ? tok_scan<T, kEnt, kRowsUnroll>(p + c0, n, a.k, tid, kRowsThreads) : tok_empty();
+            lab_ok = in_range(label, a.vocab);
+            if (lab_ok) xl = Vec<T>::to_float(p[label]);
+        };
+        TokState st = tok_scan<T, kEnt, kScanUnroll, kScanThreads>(p + c0, n, a.k, tid, numbers);
         st = tok_block_reduce_w0<kEnt>(st, red, a.k);
-        if (used == 0) cluster_wait();
-        if (tid == 0) tok_publish(xg, used, rank, C, st, 0.0f);
-        if (tid < 32) {
+        if (C > 1) {
+            if (used == 0) cluster_wait();
+            if (tid == 0) tok_publish(xg, used, rank, C, st, 0.0f);
             float unused;
-            const TokState g = tok_collect<kEnt>(xg, used, K, C, 0u, &unused, a.k, &failed);
-            if (rank == 0 && tid == 0) {
-                TokRow r;
-                if (kMode == kObjPolicy) {
-                    r = policy_row<kEnt>(a, g, xl, lab_ok, w, adv, old, ref);
-                    a.loss[row] = r.loss;
-                } else {
-                    float log_s;
-                    r = tok_row<kEnt>(g, xl, lab_ok, a.inv_t, &log_s);
-                }
-                a.logp[row] = r.logp;
-                if (kEnt && a.entropy) a.entropy[row] = r.entropy;
-                if (kMode == kObjPreference && a.row_state)
-                    a.row_state[row] = make_float4(g.m, 1.0f / g.s, 0.0f, 0.0f);
-                if (!lab_ok) atomicAdd(&g_objective_status[0], 1ull);
+            if (tid < 32) st = tok_collect<kEnt>(xg, used, K, C, 0u, &unused, a.k, &failed);
+        }
+        if (rank == 0 && tid == 0) {
+            TokRow r;
+            if (kMode == kObjPolicy) {
+                r = policy_row<kEnt>(a, st, xl, lab_ok, w, adv, old, ref);
+                a.loss[row] = r.loss;
+            } else {
+                float log_s;
+                r = tok_row<kEnt>(st, xl, lab_ok, a.inv_t, &log_s);
             }
+            a.logp[row] = r.logp;
+            if (kEnt && a.entropy) a.entropy[row] = r.entropy;
+            if (kMode == kObjPreference && a.row_state)
+                a.row_state[row] = make_float4(st.m, 1.0f / st.s, 0.0f, 0.0f);
+            if (!lab_ok) atomicAdd(&g_objective_status[0], 1ull);
         }
         ++used;
         __syncthreads();  // red is rewritten for the next row
     }
-    if (used == 0) cluster_wait();  // the first arrive's match, for a cluster that read no row
-    cluster_arrive();               // no CTA leaves while a peer may still push to it
-    cluster_wait();
-    if (__syncthreads_or(failed) && tid == 0) atomicAdd(&g_objective_status[1], 1ull);
+    if (C > 1) {
+        if (used == 0) cluster_wait();  // the first arrive's match, for a cluster that read no row
+        cluster_arrive();               // no CTA leaves while a peer may still push to it
+        cluster_wait();
+        if (__syncthreads_or(failed) && tid == 0) atomicAdd(&g_objective_status[1], 1ull);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -213,7 +227,7 @@ __global__ void __launch_bounds__(kRowsThreads, 4) k_policy_stream(ObjArgs a, in
             adv = a.adv[row];
             if (a.ref_logp) ref = a.ref_logp[row];
         }
-        TokState st = n > 0 ? tok_scan<T, kEnt, kRowsUnroll>(p, n, a.k, tid, kRowsThreads) : tok_empty();
+        TokState st = tok_scan<T, kEnt, kRowsUnroll, kRowsThreads>(p, n, a.k, tid, [] {});
         st = tok_block_reduce_w0<kEnt>(st, red, a.k);
         if (used == 0) cluster_wait();
         if (tid == 0) tok_publish(xg, used, rank, C, st, xl);
@@ -245,7 +259,7 @@ __global__ void __launch_bounds__(kRowsThreads, 4) k_policy_stream(ObjArgs a, in
 
 // ---------------------------------------------------------------------------
 // k_policy_staged: the policy's loss and gradient with each logit read once
-// from HBM, rows held in shared memory, clusters persistent over rows.
+// from HBM, rows held in shared memory.
 //
 // CTA `rank` of a cluster owns columns [c0, c0 + n) of the cluster's rows. A
 // slice sits in shared memory on the 16-byte grid of the logits: element i of
@@ -295,8 +309,8 @@ __device__ __forceinline__ uint4 ld_shifted(const T *buf, int i) {
 }
 
 template <typename T, bool kEnt>
-__global__ void __launch_bounds__(kRowsThreads, 4) k_policy_staged(ObjArgs a, int cols) {
-    constexpr int N = Vec<T>::kN, kT = kRowsThreads, kU = 4;
+__global__ void __launch_bounds__(kStagedThreads, 8) k_policy_staged(ObjArgs a, int cols) {
+    constexpr int N = Vec<T>::kN, kU = 4, kT = kStagedThreads;
     extern __shared__ __align__(128) unsigned char smem[];
     launch_dependents();
     PolicyHeader &h = *reinterpret_cast<PolicyHeader *>(smem);
@@ -426,15 +440,20 @@ __global__ void __launch_bounds__(kRowsThreads, 4) k_policy_staged(ObjArgs a, in
         const int headg = min(n, (N - offg) % N), nvecg = (n - headg) / N, tailg = n - headg - N * nvecg;
         uint4 *gv = reinterpret_cast<uint4 *>(g + headg);
         const T *src = buf + off;  // column c0
-        const bool same = offg == off;
-        for (int i = tid; i < nvecg; i += kT) {
-            const int j = headg + N * i;
-            const uint4 v = same ? bufv[qa + i] : ld_shifted(buf, off + j);
-            const uint4 o = tok_grad_vec<T, kEnt>(v, f.x, a.k, f.y, f.z);
-            const unsigned l = static_cast<unsigned>(lab - j);
-            __stcs(gv + i, o);
-            // the label's element again, by the same thread
-            if (l < N) g[lab] = Vec<T>::from_float(tok_label1<kEnt>(Vec<T>::to_float(src[lab]), f.x, a.k, f.y, f.z, f.w));
+        if (offg == off) {
+            const uint4 *bv = bufv + qa;
+            int i = tid;
+            for (; i + (kU - 1) * kT < nvecg; i += kU * kT) {
+                uint4 v[kU];
+#pragma unroll
+                for (int u = 0; u < kU; ++u) v[u] = bv[i + u * kT];
+#pragma unroll
+                for (int u = 0; u < kU; ++u) __stcs(gv + i + u * kT, tok_grad_vec<T, kEnt>(v[u], f.x, a.k, f.y, f.z));
+            }
+            for (; i < nvecg; i += kT) __stcs(gv + i, tok_grad_vec<T, kEnt>(bv[i], f.x, a.k, f.y, f.z));
+        } else {
+            for (int i = tid; i < nvecg; i += kT)
+                __stcs(gv + i, tok_grad_vec<T, kEnt>(ld_shifted(buf, off + headg + N * i), f.x, a.k, f.y, f.z));
         }
         if (tid < headg + tailg) {
             const int j = tid < headg ? tid : N * nvecg + tid;
@@ -442,6 +461,10 @@ __global__ void __launch_bounds__(kRowsThreads, 4) k_policy_staged(ObjArgs a, in
             g[j] = Vec<T>::from_float(j == lab ? tok_label1<kEnt>(x, f.x, a.k, f.y, f.z, f.w)
                                                : tok_grad1<kEnt>(x, f.x, a.k, f.y, f.z));
         }
+        // the label's element of a vector, again, by the thread that wrote it
+        const unsigned li = static_cast<unsigned>(lab - headg);
+        if (li < static_cast<unsigned>(N * nvecg) && (static_cast<int>(li / N) & (kT - 1)) == tid)
+            g[lab] = Vec<T>::from_float(tok_label1<kEnt>(Vec<T>::to_float(src[lab]), f.x, a.k, f.y, f.z, f.w));
         __syncthreads();  // the slice, its edges and the header are free
         if (tid == 0 && ahead < a.rows) {
             fence_proxy_async_smem();
@@ -749,45 +772,54 @@ cudaError_t launch_obj_rows(DType t, ObjMode mode, const ObjArgs &a, const Devic
     ObjArgs aa = a;
     int cols = cols_of(a.vocab, c);
     void *args[] = {&aa, &cols};
-    LaunchConfig l(clusters * c, kRowsThreads, c, false, s);
+    LaunchConfig l(clusters * c, kScanThreads, c, false, s);
     return cudaLaunchKernelExC(&l.cfg, rows_kernel(t, mode, wants_entropy(a)), args);
 }
 
-// The staged kernel's shape for c CTAs per row: columns and shared memory per
-// CTA, and the clusters resident at once (0: it does not fit).
-static int staged_active(DType t, bool ent, int64_t vocab, int c, const DeviceInfo &dev, int *cols, int *smem) {
+// Shared memory of a staged CTA that holds `cols` columns at any phase.
+static int64_t staged_smem(DType t, int cols) {
     const int N = 16 / elem_size(t);
-    *cols = cols_of(vocab, c);
-    *smem = kPolicyHeaderBytes + 16 * ((*cols + 2 * N) / N + 1);
-    if (*smem > dev.max_smem_optin) return 0;
-    LaunchConfig l(c, kRowsThreads, c, false, nullptr, *smem);
-    int active = 0;
-    if (cudaOccupancyMaxActiveClusters(&active, policy_staged(t, ent), &l.cfg) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return 0;
+    return kPolicyHeaderBytes + 16 * static_cast<int64_t>((cols + 2 * N) / N + 1);
+}
+
+// CTAs per row of the staged kernel; 0: the row does not fit a cluster. What
+// hides a row's latencies (copy, exchange, write) is the bytes an SM holds, so
+// the split that holds most of them, in at most six CTAs. Measured (us, 128
+// threads per CTA, CTAs per row: time; CTAs per SM x KB): 4096 x 128256 f32
+// 8: 766; 3 x 64, 10: 651; 4 x 51, 11: 707; 4 x 47, 12: 626; 5 x 43; 8192 x
+// 50257 bf16 2: 256.0; 4 x 50, 3: 256.6; 6 x 34, 4: 276; 8 x 25; 4096 x 32000
+// bf16 1: 80.3; 3 x 64, 2: 77.9; 6 x 32, 3: 86.6; 8 x 21. 256 threads: 640 at
+// 10, 259 at 2, 79.9 at 1. Clusters persistent over rows, each row's copy
+// issued behind the last one's write: 651 -> 675 at 10 CTAs, 256 -> 276 at 2,
+// 78 -> 91 at 2 -- the hardware's own scheduling balances better.
+// With few rows a row is split further, like a forward row.
+static int staged_split(DType t, int64_t rows, int64_t vocab, const DeviceInfo &dev) {
+    constexpr int64_t kPerSm = 228 * 1024, kReserved = 1024;
+    int best = 0;
+    int64_t most = 0;
+    for (int c = 1; c <= kMaxCluster; ++c) {
+        const int64_t smem = staged_smem(t, cols_of(vocab, c));
+        if (smem > dev.max_smem_optin) continue;
+        const int64_t held = std::min<int64_t>(6, kPerSm / (smem + kReserved)) * (smem - kPolicyHeaderBytes);
+        // a tie (within 1/32) goes to the larger split while an SM holds fewer than four CTAs
+        const bool few = best != 0 && kPerSm / (staged_smem(t, cols_of(vocab, best)) + kReserved) < 4;
+        if (held > most + most / 32 || (few && held >= most - most / 32)) best = c, most = held;
     }
-    return active;
+    return best == 0 ? 0 : std::max(best, split_of(t, rows, vocab, dev));
 }
 
 cudaError_t launch_policy_grad(DType t, const ObjArgs &a, const DeviceInfo &dev, cudaStream_t s) {
     const bool ent = wants_entropy(a);
+    const int64_t clusters = std::min<int64_t>(a.rows, int64_t(1) << 20);
     ObjArgs aa = a;
-    int cols = 0, smem = 0;
+    int c = staged_split(t, a.rows, a.vocab, dev);
+    const bool staged = c > 0;
+    if (!staged) c = kMaxCluster;  // rows too long for the shared memory of a cluster
+    int cols = cols_of(a.vocab, c);
     void *args[] = {&aa, &cols};
-    const int64_t bytes = static_cast<int64_t>(a.vocab) * elem_size(t);
-    int64_t c = std::max<int64_t>((bytes + kStagedSliceBytes - 1) / kStagedSliceBytes, split_of(t, a.rows, a.vocab, dev));
-    c = std::min<int64_t>(c, kMaxCluster);
-    const int active = staged_active(t, ent, a.vocab, static_cast<int>(c), dev, &cols, &smem);
-    if (active > 0) {
-        const int64_t clusters = a.rows < 32 * static_cast<int64_t>(active) ? a.rows : active;
-        LaunchConfig l(std::min<int64_t>(clusters, int64_t(1) << 20) * c, kRowsThreads, static_cast<int>(c), false, s, smem);
-        return cudaLaunchKernelExC(&l.cfg, policy_staged(t, ent), args);
-    }
-    // rows too long for the shared memory of a cluster
-    c = kMaxCluster;
-    cols = cols_of(a.vocab, static_cast<int>(c));
-    LaunchConfig l(std::min<int64_t>(a.rows, int64_t(1) << 20) * c, kRowsThreads, static_cast<int>(c), false, s);
-    return cudaLaunchKernelExC(&l.cfg, policy_stream(t, ent), args);
+    const int threads = staged ? kStagedThreads : kRowsThreads;
+    LaunchConfig l(clusters * c, threads, c, false, s, staged ? static_cast<int>(staged_smem(t, cols)) : 0);
+    return cudaLaunchKernelExC(&l.cfg, staged ? policy_staged(t, ent) : policy_stream(t, ent), args);
 }
 
 cudaError_t launch_join(const JoinArgs &j, const DeviceInfo &dev, cudaStream_t s) {

@@ -32,6 +32,7 @@ struct Vec<float> {
         else
             v.z = __float_as_uint(p.x), v.w = __float_as_uint(p.y);
     }
+    __device__ static uint4 lowest() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
     // the larger of the two, lane by lane; a NaN gives way to a number
     __device__ static uint4 vmax(const uint4 &a, const uint4 &b) {
         return make_uint4(m(a.x, b.x), m(a.y, b.y), m(a.z, b.z), m(a.w, b.w));
@@ -64,6 +65,7 @@ struct Vec<__nv_bfloat16> {
         const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
         word(v, i) = *reinterpret_cast<const uint32_t *>(&b);
     }
+    __device__ static uint4 lowest() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
     __device__ static uint4 vmax(const uint4 &a, const uint4 &b) {
         return make_uint4(m(a.x, b.x), m(a.y, b.y), m(a.z, b.z), m(a.w, b.w));
     }
@@ -93,6 +95,7 @@ struct Vec<__half> {
         const __half2 b = __floats2half2_rn(p.x, p.y);
         word(v, i) = *reinterpret_cast<const uint32_t *>(&b);
     }
+    __device__ static uint4 lowest() { return make_uint4(0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u); }
     __device__ static uint4 vmax(const uint4 &a, const uint4 &b) {
         return make_uint4(m(a.x, b.x), m(a.y, b.y), m(a.z, b.z), m(a.w, b.w));
     }
@@ -260,29 +263,44 @@ __device__ __forceinline__ TokState tok_collect(PushXchg &x, int64_t n, int64_t 
 }
 
 // Push the columns [0, n) at p: a scalar head up to the first 16-byte
-// boundary, 16-byte vectors kU at a time, a scalar tail.
-template <typename T, bool kEnt, int kU>
-__device__ __forceinline__ TokState tok_scan(const T *__restrict__ p, int n, float k, int tid, int nt) {
+// boundary, 16-byte vectors kU at a time per thread, a scalar tail. A partial
+// group is filled up with -inf (which adds nothing) rather than read vector by
+// vector, so a thread's loads never wait for one another. `early` runs once
+// the first group's loads are on their way: a load that it waits for costs no
+// more than they do.
+template <typename T, bool kEnt, int kU, int kT, typename Early>
+__device__ __forceinline__ TokState tok_scan(const T *__restrict__ p, int n, float k, int tid, Early early) {
     TokState st = tok_empty();
-    constexpr int N = Vec<T>::kN;
+    constexpr int N = Vec<T>::kN, kStep = kU * kT;
     const int off = static_cast<int>((reinterpret_cast<uintptr_t>(p) / sizeof(T)) % N);
     const int head = min(n, (N - off) % N);
     const int nvec = (n - head) / N;
     const int tail = n - head - N * nvec;
     const uint4 *pv = reinterpret_cast<const uint4 *>(p + head);
-    int q = tid;
-    for (; q + (kU - 1) * nt < nvec; q += kU * nt) {
-        uint4 v[kU];
+    uint4 v[kU];
+    auto load = [&](int q0) {
 #pragma unroll
-        for (int u = 0; u < kU; ++u) v[u] = ld_stream_u4(pv + q + u * nt);
+        for (int u = 0; u < kU; ++u)
+            v[u] = q0 + u * kT < nvec ? ld_stream_u4(pv + q0 + u * kT) : Vec<T>::lowest();
+    };
+    T ends[2];
+    load(tid);
+    if (tid < head) ends[0] = p[tid];
+    if (tid < tail) ends[1] = p[head + N * nvec + tid];
+    early();
+    tok_push<T, kEnt, kU>(st, v, k);
+    int q = tid + kStep;
+    for (; q + (kU - 1) * kT < nvec; q += kStep) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) v[u] = ld_stream_u4(pv + q + u * kT);
         tok_push<T, kEnt, kU>(st, v, k);
     }
-    for (; q < nvec; q += nt) {
-        const uint4 v[1] = {ld_stream_u4(pv + q)};
-        tok_push<T, kEnt, 1>(st, v, k);
+    if (q < nvec) {
+        load(q);
+        tok_push<T, kEnt, kU>(st, v, k);
     }
-    if (tid < head) tok_push1<kEnt>(st, Vec<T>::to_float(p[tid]), k);
-    if (tid < tail) tok_push1<kEnt>(st, Vec<T>::to_float(p[head + N * nvec + tid]), k);
+    if (tid < head) tok_push1<kEnt>(st, Vec<T>::to_float(ends[0]), k);
+    if (tid < tail) tok_push1<kEnt>(st, Vec<T>::to_float(ends[1]), k);
     return st;
 }
 

@@ -253,13 +253,23 @@ def test_bad_offsets_read_nothing_out_of_range():
 # -- the formulas' corners ------------------------------------------------------------
 
 def test_policy_on_policy_and_at_the_border():
-    """old = the same call's log-probabilities: the ratio is exactly 1, and with
-    no room to either side the two terms are equal, which counts as unclipped."""
+    """old = logp_rows' log-probabilities: the ratio is 1 to within the bounds of
+    two log-probabilities t (one per call: the calls add up in their own orders),
+    so the loss is -A to within |A| (2 t + 4 U), U = 2^-24 for each of expf's
+    result (2), the product and its clamp. old = the same call's: the ratio is
+    exactly 1, and with no room to either side the two terms are equal, which
+    counts as unclipped."""
     rows, vocab = 64, 3000
     x, g = logits_at(rows, vocab, vocab, torch.bfloat16, seed=1)
     y = torch.randint(0, vocab, (rows,), generator=g, device=DEV)
     adv = torch.randn(rows, generator=g, device=DEV)
     old = ce.logp_rows(x, y)
+    bound = adv.double().abs() * (2 * R.logp64(x, y)["logp"][1] + 4 * R.U)
+    free = ce.policy_step(x, y, old, adv, 1.0 / rows, clip_low=math.inf, clip_high=math.inf)
+    tight = ce.policy_step(x, y, old, adv, 1.0 / rows, clip_low=0.0, clip_high=0.0)
+    R.assert_near(free[2], (-adv.double(), bound), "free")
+    R.assert_near(tight[2], (-adv.double(), bound), "tight")
+    old = free[3]
     free = ce.policy_step(x, y, old, adv, 1.0 / rows, clip_low=math.inf, clip_high=math.inf)
     tight = ce.policy_step(x, y, old, adv, 1.0 / rows, clip_low=0.0, clip_high=0.0)
     assert torch.equal(free[2], -adv) and torch.equal(tight[2], -adv)
@@ -374,7 +384,9 @@ def test_a_round_of_training():
     adv = torch.randn(T, generator=g, device=DEV)
     # one step away from the sampling policy
     grad, loss, rows, logp, _ = ce.policy_step(x, y, old, adv, 1.0 / T, ref_logp=ref, kl_coef=0.05)
-    assert torch.equal(logp, old)
+    exact, bound = R.logp64(x, y)["logp"]
+    R.assert_near(logp, (exact, bound), "logp of the step")
+    R.assert_near(logp, (old.double(), 2 * bound), "the step's against the rollout's")
     W2 = W - 0.5 * (grad.t() @ hid)
     x2 = hid @ W2.t()
     want = R.policy64(x2, y, old, adv, 1.0 / T, ref=ref, kl_coef=0.05)
