@@ -539,46 +539,78 @@ def ce_grad_from_stats(shard: torch.Tensor, labels: torch.Tensor, col0: int, com
 
 # -- objectives over sampled answers and over pairs of answers ---------------------
 
+# The current stream's handle: torch's own accessor without the Stream object
+# around it where there is one (2 us less on calls that take 10 to 20 in all).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(name: str, device: torch.device, *args) -> None:
+    """The C entry point `name` on `device` and its current stream."""
+    fn, index = getattr(_lib or lib(), name), device.index
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _raw_stream(index))
+    if status != CE_OK:
+        _check(name, status)
+
+
 def _objective_view(logits: torch.Tensor, vocab: int | None):
     """(dtype, rows, vocab, stride) of f32, bf16 or f16 logits with contiguous rows."""
-    if not isinstance(logits, torch.Tensor) or logits.dtype not in DTYPES:
+    dtype = DTYPES.get(logits.dtype) if isinstance(logits, torch.Tensor) else None
+    if dtype is None:
         raise TypeError("logits must be a float32, bfloat16 or float16 torch.Tensor")
     if not logits.is_cuda:
         raise ValueError("logits must be on a CUDA device")
     if logits.dim() != 2:
         raise ValueError("logits must be 2-D [rows, cols]")
     rows, cols = logits.shape
-    if rows > 0 and cols > 1 and logits.stride(1) != 1:
+    stride, inner = logits.stride()
+    if inner != 1 and rows > 0 and cols > 1:
         raise ValueError("each row of logits must be contiguous (stride(1) == 1)")
-    stride = logits.stride(0) if rows > 1 else max(cols, 1)
     vocab = cols if vocab is None else int(vocab)
     if not 1 <= vocab <= cols:
         raise ValueError(f"need 1 <= vocab <= logits.shape[1] (vocab={vocab}, cols={cols})")
-    if rows > 1 and stride < vocab:
-        raise ValueError("rows of logits overlap (stride(0) < vocab)")
-    return DTYPES[logits.dtype], rows, vocab, max(stride, vocab)
+    if rows > 1:
+        if stride < vocab:
+            raise ValueError("rows of logits overlap (stride(0) < vocab)")
+    else:
+        stride = cols
+    return dtype, rows, vocab, stride
 
 
 def _per_row(t, n, device, name):
     """A contiguous f32 [n] input's pointer (None for None)."""
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n or t.device != device or not t.is_contiguous():
+    if t.dtype != torch.float32 or t.shape != (n,) or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor [{n}] on {device}")
     return t.data_ptr()
+
+
+def _f32(n, device):
+    return torch.empty(n, dtype=torch.float32, device=device)
+
+
+def _entropy_out(entropy, rows, device):
+    if entropy is False:
+        return None
+    return _f32(rows, device) if entropy is True else _out(entropy, (rows,), torch.float32, device, "entropy")
 
 
 def _grad_out(grad, logits, rows, vocab):
     """The gradient's tensor and row stride: allocated dense, or the caller's
     [rows, >= vocab] tensor of the logits' type with contiguous rows."""
     if grad is None:
-        grad = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
-    elif grad.dtype != logits.dtype or grad.device != logits.device or grad.dim() != 2 or grad.shape[0] != rows or \
+        return torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device), vocab
+    if grad.dtype != logits.dtype or grad.device != logits.device or grad.dim() != 2 or grad.shape[0] != rows or \
             grad.shape[1] < vocab or (rows > 0 and grad.shape[1] > 1 and grad.stride(1) != 1):
         raise ValueError(f"grad must be a {logits.dtype} [rows={rows}, >= {vocab}] tensor with contiguous rows on "
                          f"{logits.device}")
     stride = grad.stride(0) if rows > 1 else vocab
-    if rows > 1 and stride < vocab:
+    if stride < vocab:
         raise ValueError("rows of grad overlap (stride(0) < vocab)")
     return grad, stride
 
@@ -598,12 +630,10 @@ def logp_rows(logits: torch.Tensor, labels: torch.Tensor, weights: torch.Tensor 
     dev = logits.device
     labels = _labels(labels, rows, dev)
     w = _per_row(weights, rows, dev, "weights")
-    out = _out(out, (rows,), torch.float32, dev, "out")
-    ent = None if entropy is False else _out(None if entropy is True else entropy, (rows,), torch.float32, dev,
-                                             "entropy")
-    with torch.cuda.device(dev):
-        _check("logp_rows", lib().logp_rows(logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), w,
-                                             float(temperature), out.data_ptr(), _ptr(ent), _stream(dev)))
+    out = _f32(rows, dev) if out is None else _out(out, (rows,), torch.float32, dev, "out")
+    ent = _entropy_out(entropy, rows, dev)
+    _call("logp_rows", dev, logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), w, float(temperature),
+          out.data_ptr(), _ptr(ent))
     return out if ent is None else (out, ent)
 
 
@@ -618,24 +648,17 @@ def _policy(step, logits, labels, old_logp, advantages, scale, ref_logp, weights
     ref, w = _per_row(ref_logp, rows, dev, "ref_logp"), _per_row(weights, rows, dev, "weights")
     if kl_coef != 0 and ref_logp is None:
         raise ValueError("kl_coef needs ref_logp")
-    ent = None if entropy is False else _out(None if entropy is True else entropy, (rows,), torch.float32, dev,
-                                             "entropy")
-    loss_rows = torch.empty(rows, dtype=torch.float32, device=dev)
-    logp = torch.empty(rows, dtype=torch.float32, device=dev)
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    par = Policy(scale, temperature, clip_low, clip_high, kl_coef, entropy_coef)
-    with torch.cuda.device(dev):
-        if step:
-            grad, gs = _grad_out(grad, logits, rows, vocab)
-            _check("policy_step", lib().policy_step(
-                logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), old, adv, ref, w,
-                ctypes.byref(par), grad.data_ptr(), gs, loss_rows.data_ptr(), logp.data_ptr(), _ptr(ent),
-                loss.data_ptr(), _stream(dev)))
-            return grad, loss, loss_rows, logp, ent
-        _check("policy_loss", lib().policy_loss(
-            logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), old, adv, ref, w, ctypes.byref(par),
-            loss_rows.data_ptr(), logp.data_ptr(), _ptr(ent), loss.data_ptr(), _stream(dev)))
-    return loss, loss_rows, logp, ent
+    ent = _entropy_out(entropy, rows, dev)
+    loss_rows, logp, loss = _f32(rows, dev), _f32(rows, dev), _f32((), dev)
+    par = ctypes.byref(Policy(scale, temperature, clip_low, clip_high, kl_coef, entropy_coef))
+    if not step:
+        _call("policy_loss", dev, logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), old, adv, ref, w,
+              par, loss_rows.data_ptr(), logp.data_ptr(), _ptr(ent), loss.data_ptr())
+        return loss, loss_rows, logp, ent
+    grad, grad_stride = _grad_out(grad, logits, rows, vocab)
+    _call("policy_step", dev, logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), old, adv, ref, w, par,
+          grad.data_ptr(), grad_stride, loss_rows.data_ptr(), logp.data_ptr(), _ptr(ent), loss.data_ptr())
+    return grad, loss, loss_rows, logp, ent
 
 
 def policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor,
@@ -677,25 +700,20 @@ def _preference(step, logits, labels, offsets, scale, ref_logp, weights, kind, b
         raise ValueError(f"kind must be one of {sorted(PREFERENCE_KINDS)}")
     pairs = offsets.shape[0] // 2
     ref, w = _per_row(ref_logp, 2 * pairs, dev, "ref_logp"), _per_row(weights, rows, dev, "weights")
-    logp = torch.empty(rows, dtype=torch.float32, device=dev)
-    seq_logp = torch.empty(2 * pairs, dtype=torch.float32, device=dev)
-    loss_pairs = torch.empty(pairs, dtype=torch.float32, device=dev)
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    work = torch.empty((rows + 1 if step else 1, 4), dtype=torch.float32, device=dev)
-    par = Preference(scale, temperature, beta, label_smoothing, margin, PREFERENCE_KINDS[kind], 1 if average else 0)
-    with torch.cuda.device(dev):
-        if step:
-            grad, gs = _grad_out(grad, logits, rows, vocab)
-            _check("preference_step", lib().preference_step(
-                logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), w, offsets.data_ptr(), pairs, ref,
-                ctypes.byref(par), grad.data_ptr(), gs, logp.data_ptr(), seq_logp.data_ptr(), loss_pairs.data_ptr(),
-                loss.data_ptr(), work.data_ptr(), _stream(dev)))
-            return grad, loss, loss_pairs, seq_logp, logp
-        _check("preference_loss", lib().preference_loss(
-            logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), w, offsets.data_ptr(), pairs, ref,
-            ctypes.byref(par), logp.data_ptr(), seq_logp.data_ptr(), loss_pairs.data_ptr(), loss.data_ptr(),
-            work.data_ptr(), _stream(dev)))
-    return loss, loss_pairs, seq_logp, logp
+    logp, seq_logp, loss_pairs, loss = _f32(rows, dev), _f32(2 * pairs, dev), _f32(pairs, dev), _f32((), dev)
+    work = _f32(4 * (rows + 1) if step else 4, dev)
+    par = ctypes.byref(Preference(scale, temperature, beta, label_smoothing, margin, PREFERENCE_KINDS[kind],
+                                  1 if average else 0))
+    if not step:
+        _call("preference_loss", dev, logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), w,
+              offsets.data_ptr(), pairs, ref, par, logp.data_ptr(), seq_logp.data_ptr(), loss_pairs.data_ptr(),
+              loss.data_ptr(), work.data_ptr())
+        return loss, loss_pairs, seq_logp, logp
+    grad, grad_stride = _grad_out(grad, logits, rows, vocab)
+    _call("preference_step", dev, logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), w,
+          offsets.data_ptr(), pairs, ref, par, grad.data_ptr(), grad_stride, logp.data_ptr(), seq_logp.data_ptr(),
+          loss_pairs.data_ptr(), loss.data_ptr(), work.data_ptr())
+    return grad, loss, loss_pairs, seq_logp, logp
 
 
 def preference_loss(logits: torch.Tensor, labels: torch.Tensor, offsets: torch.Tensor, scale: float,
