@@ -138,9 +138,23 @@ __global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows(ObjArgs a, int col
 // (coherent loads: g may be p), the label's column `lab` (-1: elsewhere)
 // getting c besides. 16-byte loads and stores where the two share their phase
 // of 16 bytes, single elements otherwise.
-template <typename T, bool kB>
+// Elements r .. r + N - 1 of the 2 N of two neighbouring vectors.
+template <typename T>
+__device__ __forceinline__ uint4 shift_pair(const uint4 &a, const uint4 &b, int r) {
+    const int bytes = r * static_cast<int>(sizeof(T));
+    const bool two = bytes & 8, one = bytes & 4;
+    const uint32_t w0 = two ? a.z : a.x, w1 = two ? a.w : a.y, w2 = two ? b.x : a.z, w3 = two ? b.y : a.w,
+                   w4 = two ? b.z : b.x, w5 = two ? b.w : b.y;
+    const uint32_t v0 = one ? w1 : w0, v1 = one ? w2 : w1, v2 = one ? w3 : w2, v3 = one ? w4 : w3, v4 = one ? w5 : w4;
+    if (sizeof(T) == 4) return make_uint4(v0, v1, v2, v3);
+    const int half = (bytes & 2) * 8;
+    return make_uint4(__funnelshift_r(v0, v1, half), __funnelshift_r(v1, v2, half), __funnelshift_r(v2, v3, half),
+                      __funnelshift_r(v3, v4, half));
+}
+
+template <typename T, bool kB, int kU, int kT>
 __device__ __forceinline__ void write_slice(const T *p, T *g, int n, float m, float k, float a, float b, float c,
-                                            int lab, int tid, int nt) {
+                                            int lab, int tid) {
     constexpr int N = Vec<T>::kN;
     const int offp = static_cast<int>((reinterpret_cast<uintptr_t>(p) / sizeof(T)) % N);
     const int offg = static_cast<int>((reinterpret_cast<uintptr_t>(g) / sizeof(T)) % N);
@@ -148,28 +162,44 @@ __device__ __forceinline__ void write_slice(const T *p, T *g, int n, float m, fl
         const float x = Vec<T>::to_float(p[j]);
         g[j] = Vec<T>::from_float(j == lab ? tok_label1<kB>(x, m, k, a, b, c) : tok_grad1<kB>(x, m, k, a, b));
     };
-    int head = n, nvec = 0;
-    if (offp == offg) {
-        head = min(n, (N - offp) % N);
-        nvec = (n - head) / N;
+    if (offp != offg) {
+        // vectors i0 .. i1 - 1 of the gradient's grid, whose logits lie in two
+        // whole vectors of the logits' grid inside the slice; the rest, at most
+        // three vectors' worth, one by one
+        const int headg = (N - offg) % N, lead = offp + headg, r = lead % N;  // r > 0
+        const uint4 *pa = reinterpret_cast<const uint4 *>(p - offp) + lead / N;
+        const int i0 = lead < N && offp > 0 ? 1 : 0;
+        const int i1 = max(i0, (offp + n) / N - lead / N - 1);
+        const int first = min(n, headg + N * i0), rest = max(first, min(n, headg + N * i1));
+        uint4 *gv = reinterpret_cast<uint4 *>(g + headg);
+        for (int i = i0 + tid; i < i1; i += kT) {
+            const int j = headg + N * i;
+            const uint4 o = tok_grad_vec<T, kB>(shift_pair<T>(__ldcs(pa + i), __ldcs(pa + i + 1), r), m, k, a, b);
+            __stcs(gv + i, o);
+            if (static_cast<unsigned>(lab - j) < N) one(lab);
+        }
+        for (int j = tid; j < first + n - rest; j += kT) one(j < first ? j : rest + j - first);
+        return;
     }
-    for (int j = tid; j < head; j += nt) one(j);
+    const int head = min(n, (N - offp) % N), nvec = (n - head) / N, tail = n - head - N * nvec;
+    // the label's logit, read before its vector is written (g may be p), by the
+    // thread that owns the vector and so writes both
+    const unsigned li = static_cast<unsigned>(lab - head);
+    const bool owns = li < static_cast<unsigned>(N * nvec) && static_cast<int>(li / N) % kT == tid;
+    const float xl = owns ? Vec<T>::to_float(p[lab]) : 0.0f;
+    if (tid < head + tail) one(tid < head ? tid : N * nvec + tid);
     const uint4 *pv = reinterpret_cast<const uint4 *>(p + head);
     uint4 *gv = reinterpret_cast<uint4 *>(g + head);
-    for (int q = tid; q < nvec; q += nt) {
-        const uint4 v = __ldcs(pv + q);
-        const unsigned l = static_cast<unsigned>(lab - head - N * q);
-        const uint4 o = tok_grad_vec<T, kB>(v, m, k, a, b);
-        if (l < N) {
-            T e[N];
-            *reinterpret_cast<uint4 *>(e) = o;
-            e[l] = Vec<T>::from_float(tok_label1<kB>(Vec<T>::to_float(p[head + N * q + l]), m, k, a, b, c));
-            __stcs(gv + q, *reinterpret_cast<const uint4 *>(e));
-        } else {
-            __stcs(gv + q, o);
-        }
+    int q = tid;
+    for (; q + (kU - 1) * kT < nvec; q += kU * kT) {
+        uint4 v[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) v[u] = __ldcs(pv + q + u * kT);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) __stcs(gv + q + u * kT, tok_grad_vec<T, kB>(v[u], m, k, a, b));
     }
-    for (int j = head + N * nvec + tid; j < n; j += nt) one(j);
+    for (; q < nvec; q += kT) __stcs(gv + q, tok_grad_vec<T, kB>(__ldcs(pv + q), m, k, a, b));
+    if (owns) g[lab] = Vec<T>::from_float(tok_label1<kB>(xl, m, k, a, b, c));
 }
 
 template <typename T>
@@ -248,7 +278,7 @@ __global__ void __launch_bounds__(kRowsThreads, 4) k_policy_stream(ObjArgs a, in
         ++used;
         __syncthreads();
         const float4 f = bc;
-        write_slice<T, kEnt>(p, g, n, f.x, a.k, f.y, f.z, f.w, lab, tid, kRowsThreads);
+        write_slice<T, kEnt, 4, kRowsThreads>(p, g, n, f.x, a.k, f.y, f.z, f.w, lab, tid);
         __syncthreads();  // bc and red are rewritten for the next row
     }
     if (used == 0) cluster_wait();
@@ -291,21 +321,6 @@ __device__ __forceinline__ uint4 load_edge(const T *p, int off, int n, int q) {
         v[l] = i >= 0 && i < n ? p[i] : Vec<T>::from_float(-INFINITY);
     }
     return *reinterpret_cast<const uint4 *>(v);
-}
-
-// The 16 bytes of elements i .. i + N - 1 of a shared-memory buffer, at any
-// phase: four words, or five shifted by half a word.
-template <typename T>
-__device__ __forceinline__ uint4 ld_shifted(const T *buf, int i) {
-    if (sizeof(T) == 4) {
-        const uint32_t *w = reinterpret_cast<const uint32_t *>(buf) + i;
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(buf) + (i >> 1);
-    if ((i & 1) == 0) return make_uint4(w[0], w[1], w[2], w[3]);
-    const uint32_t a = w[0], b = w[1], c = w[2], d = w[3], e = w[4];
-    return make_uint4(__funnelshift_r(a, b, 16), __funnelshift_r(b, c, 16), __funnelshift_r(c, d, 16),
-                      __funnelshift_r(d, e, 16));
 }
 
 template <typename T, bool kEnt>
@@ -452,8 +467,11 @@ __global__ void __launch_bounds__(kStagedThreads, 8) k_policy_staged(ObjArgs a, 
             }
             for (; i < nvecg; i += kT) __stcs(gv + i, tok_grad_vec<T, kEnt>(bv[i], f.x, a.k, f.y, f.z));
         } else {
+            const int lead = off + headg, r = lead % N;
+            const uint4 *bv = bufv + lead / N;
+#pragma unroll 2
             for (int i = tid; i < nvecg; i += kT)
-                __stcs(gv + i, tok_grad_vec<T, kEnt>(ld_shifted(buf, off + headg + N * i), f.x, a.k, f.y, f.z));
+                __stcs(gv + i, tok_grad_vec<T, kEnt>(shift_pair<T>(bv[i], bv[i + 1], r), f.x, a.k, f.y, f.z));
         }
         if (tid < headg + tailg) {
             const int j = tid < headg ? tid : N * nvecg + tid;
@@ -606,9 +624,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(JoinArgs j) {
 // a row. Rows whose factor is 0 (no weight, or in no sequence) are written as
 // zeros without being read.
 constexpr int kPartBytes = 32768;
+constexpr int kPairThreads = 256;
+constexpr int kPairUnroll = 4;
 
 template <typename T>
-__global__ void __launch_bounds__(256) k_pair_grad(ObjArgs a, int parts) {
+__global__ void __launch_bounds__(kPairThreads) k_pair_grad(ObjArgs a, int parts) {
     constexpr int kCols = kPartBytes / static_cast<int>(sizeof(T));
     wait_prerequisites();
     const int64_t unit = static_cast<int64_t>(gridDim.x) - 1 - blockIdx.x;
@@ -618,14 +638,15 @@ __global__ void __launch_bounds__(256) k_pair_grad(ObjArgs a, int parts) {
     T *g = static_cast<T *>(a.grad) + row * a.grad_stride + c0;
     const float4 st = a.row_state[row];
     if (st.z == 0.0f) {
-        zero_slice(g, n, threadIdx.x, 256);
+        zero_slice(g, n, threadIdx.x, kPairThreads);
         return;
     }
     const T *p = static_cast<const T *>(a.logits) + row * a.stride + c0;
     const int64_t label = a.labels[row] - c0;
     const int lab = label >= 0 && label < n ? static_cast<int>(label) : -1;
     const bool bad = !isfinite(st.x);
-    write_slice<T, false>(p, g, n, st.x, a.k, bad ? nan_f() : -st.z * st.y, 0.0f, st.z, lab, threadIdx.x, 256);
+    write_slice<T, false, kPairUnroll, kPairThreads>(p, g, n, st.x, a.k, bad ? nan_f() : -st.z * st.y, 0.0f, st.z, lab,
+                                                     threadIdx.x);
 }
 
 // ---------------------------------------------------------------------------
@@ -846,7 +867,7 @@ cudaError_t launch_preference_grad(DType t, const ObjArgs &a, const DeviceInfo &
         aa.labels = a.labels + r0;
         aa.row_state = a.row_state + r0;
         void *args[] = {&aa, &parts};
-        LaunchConfig l(aa.rows * parts, 256, 0, r0 == 0, s);
+        LaunchConfig l(aa.rows * parts, kPairThreads, 0, r0 == 0, s);
         cudaError_t e = cudaLaunchKernelExC(&l.cfg, fn, args);
         if (e != cudaSuccess) return e;
     }
