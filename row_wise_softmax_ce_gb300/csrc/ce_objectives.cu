@@ -301,13 +301,10 @@ __global__ void __launch_bounds__(kRowsThreads, 4) k_policy_stream(ObjArgs a, in
 // is written from shared memory; then the copy of the next row that counts
 // starts, its latency hidden behind the SM's other CTAs.
 struct alignas(16) PolicyHeader {
-    PushXchg xg;
+    WarpXchg<kStagedThreads / 32> xg;
     uint64_t bar;
-    float xl;
-    float4 bc;
-    TokState red[32];
 };
-constexpr int kPolicyHeaderBytes = 1152;
+constexpr int kPolicyHeaderBytes = 2176;
 static_assert(sizeof(PolicyHeader) <= kPolicyHeaderBytes && kPolicyHeaderBytes % 128 == 0, "staged header");
 
 // A 16-byte vector of grid index q: the slice's columns, -inf elsewhere.
@@ -362,7 +359,7 @@ __global__ void __launch_bounds__(kStagedThreads, 8) k_policy_staged(ObjArgs a, 
     if (tid == 0) {
         mbar_init(&h.bar, 1);
         fence_mbar_init();
-        push_xchg_init(h.xg, K, C);
+        warp_xchg_init(h.xg, K, C);
         policy = l2_policy_evict_first();
         ahead = next_live(cid);
         if (ahead < a.rows) {
@@ -372,7 +369,7 @@ __global__ void __launch_bounds__(kStagedThreads, 8) k_policy_staged(ObjArgs a, 
     }
     __syncthreads();
     cluster_arrive();  // every CTA's slots exist before a peer pushes: the wait comes before the first push
-    bool failed = false;
+    bool failed = false, left = false;
     uint32_t parity = 0;
     int64_t used = 0;
     // a row's weight and label are loaded one row ahead, off its critical path
@@ -404,18 +401,11 @@ __global__ void __launch_bounds__(kStagedThreads, 8) k_policy_staged(ObjArgs a, 
         const int qe0 = qa == 1 ? 0 : -1, qe1 = qa + nvec < nq ? qa + nvec : -1;  // partial end vectors
         if (qe0 >= 0 && tid == 0) bufv[qe0] = load_edge(p, off, n, qe0);
         if (qe1 >= 0 && (qe1 & (kT - 1)) == tid) bufv[qe1] = load_edge(p, off, n, qe1);
-        float old = 0.0f, ref = 0.0f, adv = 0.0f;
-        if (tid == 0) {
-            old = a.old_logp[row];
-            adv = a.adv[row];
-            if (a.ref_logp) ref = a.ref_logp[row];
-        }
+        const float old = a.old_logp[row], adv = a.adv[row], ref = a.ref_logp ? a.ref_logp[row] : 0.0f;
         const bool lab_ok = in_range(label, a.vocab);
         const int lab = lab_ok && label >= c0 && label < c0 + n ? static_cast<int>(label - c0) : -1;
         if (!failed) failed = !mbar_wait_bounded(&h.bar, parity);
         parity ^= 1u;
-        // the label's logit, by the owner of its vector
-        if (lab >= 0 && (((off + lab) / N) & (kT - 1)) == tid) h.xl = Vec<T>::to_float(buf[off + lab]);
         TokState st = tok_empty();
         int q = tid;
         for (; q + (kU - 1) * kT < nq; q += kU * kT) {
@@ -428,29 +418,31 @@ __global__ void __launch_bounds__(kStagedThreads, 8) k_policy_staged(ObjArgs a, 
             const uint4 v[1] = {bufv[q]};
             tok_push<T, kEnt, 1>(st, v, a.k);
         }
-        st = tok_block_reduce_w0<kEnt>(st, h.red, a.k);
+        st = tok_warp_reduce<kEnt>(st, a.k);
+        // the label's logit goes with the warp that owns its vector
+        const int owner = lab >= 0 ? (off + lab) / N & (kT - 1) : -32;
+        float xl = owner == tid ? Vec<T>::to_float(buf[off + lab]) : 0.0f;
+        xl = __shfl_sync(kFullMask, xl, owner & 31);
+        if (owner / 32 != tid / 32) xl = 0.0f;
         if (used == 0) cluster_wait();
-        if (tid == 0) tok_publish(h.xg, used, rank, C, st, lab >= 0 ? h.xl : 0.0f);
-        if (tid < 32) {
-            float xl;
-            const uint32_t owner = lab_ok ? static_cast<uint32_t>(label) / static_cast<uint32_t>(cols) : 0u;
-            const TokState s = tok_collect<kEnt>(h.xg, used, K, C, owner, &xl, a.k, &failed);
-            if (tid == 0) {
-                const TokRow r = policy_row<kEnt>(a, s, xl, lab_ok, w, adv, old, ref);
-                h.bc = make_float4(r.m, r.a, r.b, r.c);
-                if (rank == 0) {
-                    a.logp[row] = r.logp;
-                    a.loss[row] = r.loss;
-                    if (kEnt && a.entropy) a.entropy[row] = r.entropy;
-                    if (!lab_ok) atomicAdd(&g_objective_status[0], 1ull);
-                }
-            }
+        warp_xchg_push(h.xg, used, rank, C, st, xl);
+        st = warp_xchg_collect<kT / 32, kEnt>(h.xg, used, K, C, &xl, a.k, &failed);
+        const TokRow r = policy_row<kEnt>(a, st, xl, lab_ok, w, adv, old, ref);
+        if (rank == 0 && tid == 0) {
+            a.logp[row] = r.logp;
+            a.loss[row] = r.loss;
+            if (kEnt && a.entropy) a.entropy[row] = r.entropy;
+            if (!lab_ok) atomicAdd(&g_objective_status[0], 1ull);
         }
         ++used;
-        __syncthreads();
+        if (row + G >= a.rows) {
+            cluster_arrive();  // nothing more is pushed to or by this CTA
+            left = true;
+        }
+        if (qe0 >= 0 || qe1 >= 0) __syncthreads();  // the edges are read by other threads than their owners
         // the gradient, in 16-byte vectors of its own grid: the logits' own
         // vectors where the two share their phase, shifted ones otherwise
-        const float4 f = h.bc;
+        const float4 f = make_float4(r.m, r.a, r.b, r.c);
         const int offg = phase_of(g);
         const int headg = min(n, (N - offg) % N), nvecg = (n - headg) / N, tailg = n - headg - N * nvecg;
         uint4 *gv = reinterpret_cast<uint4 *>(g + headg);
@@ -491,8 +483,8 @@ __global__ void __launch_bounds__(kStagedThreads, 8) k_policy_staged(ObjArgs a, 
         }
     }
     if (used == 0) cluster_wait();
-    cluster_arrive();
-    cluster_wait();
+    if (!left) cluster_arrive();
+    cluster_wait();  // no CTA leaves while a peer may still push to it
     if (__syncthreads_or(failed) && tid == 0) {
         atomicAdd(&g_objective_status[1], 1ull);
         // give a copy still in flight a last bounded chance to land

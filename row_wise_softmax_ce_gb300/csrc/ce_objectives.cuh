@@ -191,8 +191,7 @@ __device__ __forceinline__ void tok_push1(TokState &st, float x, float k) {
     if (kEnt) st.u = fmaf(e, finite_below(d), st.u);
 }
 
-// merge two states; symmetric but for the order of two additions, which f32
-// addition does not see: a butterfly gives every lane the same bits
+// merge two states
 template <bool kEnt>
 __device__ __forceinline__ TokState tok_merge(TokState a, TokState b, float k) {
     const float m = fmaxf(a.m, b.m);
@@ -203,15 +202,23 @@ __device__ __forceinline__ TokState tok_merge(TokState a, TokState b, float k) {
     return TokState{m, a.s + b.s, kEnt ? a.u + b.u : 0.0f};
 }
 
+// the warp's largest value (no lane holds a NaN)
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Every lane gets the warp's state: the max first, each lane raised to it
+// once, then a butterfly of plain sums.
 template <bool kEnt>
 __device__ __forceinline__ TokState tok_warp_reduce(TokState st, float k) {
+    const float m = warp_max(st.m);
+    if (m != -INFINITY) tok_raise<kEnt>(st, m, k);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        TokState q;
-        q.m = __shfl_xor_sync(kFullMask, st.m, o);
-        q.s = __shfl_xor_sync(kFullMask, st.s, o);
-        q.u = kEnt ? __shfl_xor_sync(kFullMask, st.u, o) : 0.0f;
-        st = tok_merge<kEnt>(st, q, k);
+        st.s += __shfl_xor_sync(kFullMask, st.s, o);
+        if (kEnt) st.u += __shfl_xor_sync(kFullMask, st.u, o);
     }
     return st;
 }
@@ -260,6 +267,57 @@ __device__ __forceinline__ TokState tok_collect(PushXchg &x, int64_t n, int64_t 
     const TokState g = tok_warp_reduce<kEnt>(q, k);
     if (lane == 0 && n + 2 < N) mbar_arrive_expect_tx(&x.bar[xs], 16u * C);
     return g;
+}
+
+// The same exchange warp by warp, without a reduction over the CTA first: each
+// of the kW warps of the cluster's C CTAs pushes its state into slot n % 2 of
+// every CTA (lane r into CTA r), and every warp waits for the kW C states of
+// its own CTA's slot and merges them: the same bits in every warp, and no CTA
+// barrier. Two slots suffice as for PushXchg: a warp pushes exchange n + 2 only
+// after all warps have pushed n + 1, which each does only after it has read
+// slot n % 2. x[label] comes with the one warp that owns it, 0 with the others.
+template <int kW>
+struct WarpXchg {
+    float4 slot[2][16 * kW];
+    uint64_t bar[2];
+};
+
+template <int kW>
+__device__ __forceinline__ void warp_xchg_init(WarpXchg<kW> &x, int64_t N, uint32_t C) {
+    for (int i = 0; i < 2; ++i) mbar_init(&x.bar[i], 1);
+    fence_mbar_init();
+    for (int i = 0; i < 2; ++i)
+        if (i < N) mbar_arrive_expect_tx(&x.bar[i], 16u * kW * C);
+}
+
+template <int kW>
+__device__ __forceinline__ void warp_xchg_push(WarpXchg<kW> &x, int64_t n, uint32_t rank, uint32_t C,
+                                               const TokState &st, float xl) {
+    const int xs = static_cast<int>(n & 1), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane < static_cast<int>(C))
+        st_async_peer(peer_smem(&x.slot[xs][rank * kW + warp], lane), make_float4(st.m, st.s, st.u, xl),
+                      peer_smem(&x.bar[xs], lane));
+}
+
+template <int kW, bool kEnt>
+__device__ __forceinline__ TokState warp_xchg_collect(WarpXchg<kW> &x, int64_t n, int64_t N, uint32_t C, float *xl,
+                                                      float k, bool *failed) {
+    const int xs = static_cast<int>(n & 1), lane = threadIdx.x & 31, E = kW * static_cast<int>(C);
+    if (!*failed) *failed = !mbar_wait_bounded(&x.bar[xs], static_cast<uint32_t>(n >> 1) & 1u);
+    TokState st = tok_empty();
+    float v = 0.0f;
+#pragma unroll
+    for (int i = lane; i < 16 * kW; i += 32) {
+        if (i >= E) break;
+        const float4 e = x.slot[xs][i];
+        st = tok_merge<kEnt>(st, TokState{e.x, e.y, e.z}, k);
+        v += e.w;
+    }
+    if (threadIdx.x == 0 && n + 2 < N) mbar_arrive_expect_tx(&x.bar[xs], 16u * kW * C);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+    *xl = v;
+    return tok_warp_reduce<kEnt>(st, k);
 }
 
 // Push the columns [0, n) at p: a scalar head up to the first 16-byte
