@@ -15,7 +15,7 @@
 //   k_join           a preference batch's rows into sequences, pairs, the loss
 //                    and each row's gradient factor
 //   k_pair_grad      the gradient of a preference batch, the rows read again
-//   k_weighted_sum   the policy's loss, an f64 fixed-shape tree over a cluster
+//   k_weighted_sum   the policy's loss, a fixed-shape tree of f32 pairs
 #include <algorithm>
 #include <cstdint>
 
@@ -494,15 +494,37 @@ __global__ void __launch_bounds__(kStagedThreads, 8) k_policy_staged(ObjArgs a, 
 
 // ---------------------------------------------------------------------------
 // k_join: one CTA per pair (looping). Half of its threads sum the chosen
-// sequence's w logp (and w, for averages) in f64, half the rejected's, each in
-// a fixed order; one thread forms the pair's loss and the factors
+// sequence's w logp (and w, for averages), half the rejected's, each in a fixed
+// order; one thread forms the pair's loss and the factors
 // dloss / dlogp of the two sequences' rows. The CTA that finishes last adds
 // the pairs' losses up, again in a fixed order.
 constexpr int kJoinThreads = 256;
 
-__device__ __forceinline__ double warp_sum(double v) {
+// A sum over rows as an unevaluated pair hi + lo of f32: hi the rounded sum,
+// lo the sum of the rounding errors, each exact (two-sum), so the pair carries
+// about 48 bits. GB300 adds f64 at about two lanes per clock and SM; an f64
+// butterfly over 8 warps alone takes longer than all the rest of such a sum.
+// lo is NaN once hi overflows or an infinity was added: hi alone is the sum.
+struct Sum2 {
+    float hi, lo;
+};
+__device__ __forceinline__ Sum2 sum2_add(Sum2 a, Sum2 b) {
+    const float s = a.hi + b.hi, bb = s - a.hi;
+    return Sum2{s, ((a.hi - (s - bb)) + (b.hi - bb)) + (a.lo + b.lo)};
+}
+__device__ __forceinline__ Sum2 sum2_mul(float w, float x) {
+    const float p = __fmul_rn(w, x);
+    return Sum2{p, __fmaf_rn(w, x, -p)};
+}
+__device__ __forceinline__ double sum2_value(Sum2 v) {
+    return isnan(v.lo) ? static_cast<double>(v.hi) : static_cast<double>(v.hi) + static_cast<double>(v.lo);
+}
+// over aligned groups of kLanes lanes; every lane gets its group's sum
+template <int kLanes = 32>
+__device__ __forceinline__ Sum2 sum2_warp(Sum2 v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+    for (int o = kLanes / 2; o > 0; o >>= 1)
+        v = sum2_add(v, Sum2{__shfl_xor_sync(kFullMask, v.hi, o), __shfl_xor_sync(kFullMask, v.lo, o)});
     return v;
 }
 
@@ -514,7 +536,7 @@ __device__ __forceinline__ float sigmoid(float x) {
 }
 
 __global__ void __launch_bounds__(kJoinThreads) k_join(JoinArgs j) {
-    __shared__ double part[2][2][kJoinThreads / 64];  // [sequence][sum, count][warp]
+    __shared__ Sum2 part[2][2][kJoinThreads / 64];  // [sequence][sum, count][warp]
     __shared__ float factor[2];
     __shared__ bool last;
     launch_dependents();
@@ -526,19 +548,17 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(JoinArgs j) {
         const int64_t s = side == 0 ? pair : P + pair;
         const int64_t r0 = j.offsets[s], r1 = j.offsets[s + 1];
         const bool ok = r0 >= 0 && r0 <= r1 && r1 <= j.rows;
-        double sum = 0.0, count = 0.0;
+        Sum2 sum{ok ? 0.0f : nan_f(), 0.0f}, count{0.0f, 0.0f};
         if (ok) {
 #pragma unroll 4
             for (int64_t r = r0 + t; r < r1; r += kHalf) {
                 const float w = j.weights ? j.weights[r] : 1.0f;
-                if (w != 0.0f) sum += static_cast<double>(w) * static_cast<double>(j.logp[r]);
-                if (j.average) count += static_cast<double>(w);
+                if (w != 0.0f) sum = sum2_add(sum, sum2_mul(w, j.logp[r]));
+                if (j.average) count = sum2_add(count, Sum2{w, 0.0f});
             }
-        } else {
-            sum = static_cast<double>(nan_f());
         }
-        sum = warp_sum(sum);
-        if (j.average) count = warp_sum(count);
+        sum = sum2_warp(sum);
+        if (j.average) count = sum2_warp(count);
         if (lane == 0) {
             part[side][0][warp] = sum;
             part[side][1][warp] = count;
@@ -547,10 +567,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(JoinArgs j) {
         if (threadIdx.x == 0) {
             double L[2], per[2];
             for (int q = 0; q < 2; ++q) {
-                double v = 0.0, c = 0.0;
-                for (int i = 0; i < kHalf / 32; ++i) v += part[q][0][i], c += part[q][1][i];
-                per[q] = j.average ? (c != 0.0 ? 1.0 / c : 0.0) : 1.0;
-                L[q] = v * per[q];
+                Sum2 v = part[q][0][0], c = part[q][1][0];
+                for (int i = 1; i < kHalf / 32; ++i) v = sum2_add(v, part[q][0][i]), c = sum2_add(c, part[q][1][i]);
+                const double n = sum2_value(c);
+                per[q] = j.average ? (n != 0.0 ? 1.0 / n : 0.0) : 1.0;
+                L[q] = sum2_value(v) * per[q];
                 j.seq_logp[q == 0 ? pair : P + pair] = static_cast<float>(L[q]);
             }
             double h = L[0] - L[1];
@@ -598,16 +619,15 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(JoinArgs j) {
     __syncthreads();
     if (!last) return;
     __threadfence();
-    double sum = 0.0;
-    for (int64_t i = threadIdx.x; i < P; i += kJoinThreads) sum += static_cast<double>(__ldcg(j.loss_pairs + i));
-    sum = warp_sum(sum);
+    Sum2 sum{0.0f, 0.0f};
+    for (int64_t i = threadIdx.x; i < P; i += kJoinThreads) sum = sum2_add(sum, Sum2{__ldcg(j.loss_pairs + i), 0.0f});
+    sum = sum2_warp(sum);
     if (lane == 0) part[side][0][warp] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
-        double v = 0.0;
-        for (int q = 0; q < 2; ++q)
-            for (int i = 0; i < kHalf / 32; ++i) v += part[q][0][i];
-        *j.loss = static_cast<float>(v * j.scale);
+        Sum2 v = part[0][0][0];
+        for (int i = 1; i < kJoinThreads / 32; ++i) v = sum2_add(v, part[i / (kHalf / 32)][0][i % (kHalf / 32)]);
+        *j.loss = static_cast<float>(sum2_value(v) * j.scale);
     }
 }
 
@@ -642,37 +662,48 @@ __global__ void __launch_bounds__(kPairThreads) k_pair_grad(ObjArgs a, int parts
 }
 
 // ---------------------------------------------------------------------------
-// k_weighted_sum: one cluster, the shape of the mean loss's kernel.
+// k_weighted_sum: one CTA, or for many rows one cluster, launched as a
+// programmatic dependent of the row kernel. Thread g of all sums rows g, g +
+// all, ... as f32 pairs; a butterfly over each warp, then over the CTA's warps;
+// a cluster's CTAs meet in CTA 0's shared memory. A fixed shape for a number
+// of rows: the same bits every run.
 constexpr int kSumCtas = 8;
-constexpr int kSumThreads = 256;
+constexpr int kSumThreads = 512;
+constexpr int64_t kSumOneCta = 8192;  // rows up to here: one CTA
 
 __global__ void __launch_bounds__(kSumThreads) k_weighted_sum(const float *__restrict__ loss,
                                                               const float *__restrict__ weights, int64_t rows,
                                                               double scale, float *__restrict__ out) {
-    __shared__ double warp_part[kSumThreads / 32];
+    __shared__ Sum2 warp_part[kSumThreads / 32];
     __shared__ double cta_part[kSumCtas];
-    cluster_arrive();      // every CTA has started before CTA 0's shared memory is written
-    wait_prerequisites();  // the row losses are complete and visible
-    const uint32_t rank = cluster_rank();
+    const uint32_t rank = cluster_rank(), C = cluster_size();
+    if (C > 1) cluster_arrive();  // every CTA has started before CTA 0's shared memory is written
+    wait_prerequisites();         // the row losses are complete and visible
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    double s = 0.0;
-    for (int64_t i = static_cast<int64_t>(rank) * kSumThreads + tid; i < rows; i += kSumCtas * kSumThreads) {
-        const double l = static_cast<double>(loss[i]);
-        s += weights ? static_cast<double>(weights[i]) * l : l;
-    }
-    s = warp_sum(s);
+    const int64_t all = static_cast<int64_t>(C) * kSumThreads;
+    Sum2 s{0.0f, 0.0f};
+#pragma unroll 4
+    for (int64_t i = static_cast<int64_t>(rank) * kSumThreads + tid; i < rows; i += all)
+        s = sum2_add(s, weights ? sum2_mul(weights[i], loss[i]) : Sum2{loss[i], 0.0f});
+    s = sum2_warp(s);
     if (lane == 0) warp_part[warp] = s;
     __syncthreads();
-    cluster_wait();
+    if (C > 1) cluster_wait();
     if (warp == 0) {
-        const double r = warp_sum(lane < kSumThreads / 32 ? warp_part[lane] : 0.0);
-        if (lane == 0) st_dsmem_f64(peer_smem(&cta_part[rank], 0), r);
+        const Sum2 r = sum2_warp<kSumThreads / 32>(warp_part[lane % (kSumThreads / 32)]);
+        if (C == 1) {
+            if (lane == 0) *out = static_cast<float>(sum2_value(r) * scale);
+            return;
+        }
+        if (lane == 0) st_dsmem_f64(peer_smem(&cta_part[rank], 0), sum2_value(r));
     }
+    if (C == 1) return;
     cluster_arrive_release();
     cluster_wait();
-    if (rank == 0 && warp == 0) {
-        const double r = warp_sum(lane < kSumCtas ? cta_part[lane] : 0.0);
-        if (lane == 0) *out = static_cast<float>(r * scale);
+    if (rank == 0 && tid == 0) {
+        double v = 0.0;
+        for (int i = 0; i < kSumCtas; ++i) v += cta_part[i];
+        *out = static_cast<float>(v * scale);
     }
 }
 
@@ -868,7 +899,8 @@ cudaError_t launch_preference_grad(DType t, const ObjArgs &a, const DeviceInfo &
 
 cudaError_t launch_weighted_sum(const float *loss, const float *weights, int64_t rows, double scale, float *out,
                                 cudaStream_t s) {
-    LaunchConfig l(kSumCtas, kSumThreads, kSumCtas, true, s);
+    const int ctas = rows > kSumOneCta ? kSumCtas : 1;
+    LaunchConfig l(ctas, kSumThreads, ctas > 1 ? ctas : 0, true, s);
     return cudaLaunchKernelEx(&l.cfg, k_weighted_sum, loss, weights, rows, scale, out);
 }
 
