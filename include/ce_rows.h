@@ -355,7 +355,7 @@ CE_API int ce_grad_from_stats(const float *logits, int64_t rows, int64_t vocab, 
  *  - dtype: CE_F32, CE_BF16 or CE_F16, the type of the logits and of their
  *    gradient. Everything else of a row is f32; row statistics, losses and
  *    the gradient are computed in f32 and a gradient is rounded once, at the
- *    end. Sums over rows are f64, rounded once to the f32 they are given as.
+ *    end. Sums over rows carry at least 48 bits and are rounded once to f32.
  *  - temperature T > 0 (1e-6 <= T <= 1e6): the distribution of a row is
  *    softmax(x / T); gradients are with respect to x.
  *  - weights: [rows] f32, or NULL (every row counts 1). A row of weight 0 (a

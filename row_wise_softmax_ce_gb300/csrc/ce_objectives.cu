@@ -44,19 +44,25 @@ constexpr int kStagedThreads = 128;
 __device__ __forceinline__ bool in_range(int64_t label, int vocab) { return label >= 0 && label < vocab; }
 
 // ---------------------------------------------------------------------------
-// k_obj_rows: one cluster of C CTAs per row (looping), each a contiguous slice
-// of `cols` columns; their states meet by pushes and CTA 0 writes the row.
+// k_obj_rows: one CTA per row (looping), or few rows over clusters of C CTAs,
+// a row each: every warp scans its part of a contiguous slice of `cols`
+// columns and pushes its state into CTA 0's shared memory, whose first warp
+// merges them and writes the row.
+struct RowsXchg {
+    float4 slot[kMaxCluster * (kScanThreads / 32)];
+    uint64_t bar;
+};
+
 template <typename T, int kMode, bool kEnt>
 __global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows(ObjArgs a, int cols) {
-    __shared__ TokState red[32];
-    __shared__ PushXchg xg;
+    constexpr int kW = kScanThreads / 32;
+    __shared__ RowsXchg x;
     launch_dependents();
     const uint32_t rank = cluster_rank(), C = cluster_size();
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int c0 = static_cast<int>(rank) * cols;
     const int n = max(0, min(a.vocab, c0 + cols) - c0);
-    const int64_t cid = cluster_id_x(), G = cluster_count_x();
-    const int64_t K = cid < a.rows ? (a.rows - 1 - cid) / G + 1 : 0;
+    const int64_t G = cluster_count_x();
     int64_t first = 0, last = a.rows;
     if (kMode == kObjPreference) {
         // rows before the first sequence and behind the last take no part
@@ -65,13 +71,15 @@ __global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows(ObjArgs a, int col
         if (blockIdx.x == 0 && tid == 0) *a.done = 0;
     }
     if (C > 1) {
-        if (tid == 0) push_xchg_init(xg, K, C);
-        __syncthreads();
-        cluster_arrive();  // every CTA's slots exist before a peer pushes: the wait comes before the first push
+        if (rank == 0 && tid == 0) {
+            mbar_init(&x.bar, 1);
+            fence_mbar_init();
+            mbar_arrive_expect_tx(&x.bar, 16u * kW * C);
+        }
+        cluster_arrive_release();  // CTA 0's barrier exists before a peer pushes: the wait comes before the push
     }
     bool failed = false;
-    int64_t used = 0;
-    for (int64_t row = cid; row < a.rows; row += G) {
+    for (int64_t row = cluster_id_x(); row < a.rows; row += G) {
         const float w = a.weights ? a.weights[row] : 1.0f;
         if (w == 0.0f || (kMode == kObjPreference && (row < first || row >= last))) {
             if (rank == 0 && tid == 0) {
@@ -80,6 +88,7 @@ __global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows(ObjArgs a, int col
                 if (kMode == kObjPolicy) a.loss[row] = 0.0f;
                 if (kMode == kObjPreference && a.row_state) a.row_state[row] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
+            if (C > 1) cluster_wait();
             continue;
         }
         const T *p = static_cast<const T *>(a.logits) + row * a.stride;
@@ -100,36 +109,45 @@ __global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows(ObjArgs a, int col
             if (lab_ok) xl = Vec<T>::to_float(p[label]);
         };
         TokState st = tok_scan<T, kEnt, kScanUnroll, kScanThreads>(p + c0, n, a.k, tid, numbers);
-        st = tok_block_reduce_w0<kEnt>(st, red, a.k);
+        st = tok_warp_reduce<kEnt>(st, a.k);
+        const float4 mine = make_float4(st.m, st.s, st.u, 0.0f);
         if (C > 1) {
-            if (used == 0) cluster_wait();
-            if (tid == 0) tok_publish(xg, used, rank, C, st, 0.0f);
-            float unused;
-            if (tid < 32) st = tok_collect<kEnt>(xg, used, K, C, 0u, &unused, a.k, &failed);
+            cluster_wait();  // a cluster has one row
+            if (lane == 0) st_async_peer(peer_smem(&x.slot[rank * kW + warp], 0), mine, peer_smem(&x.bar, 0));
+            if (rank != 0) return;
+            if (warp == 0) failed = !mbar_wait_bounded(&x.bar, 0);
+        } else {
+            if (lane == 0) x.slot[warp] = mine;
+            __syncthreads();
         }
-        if (rank == 0 && tid == 0) {
-            TokRow r;
-            if (kMode == kObjPolicy) {
-                r = policy_row<kEnt>(a, st, xl, lab_ok, w, adv, old, ref);
-                a.loss[row] = r.loss;
-            } else {
-                float log_s;
-                r = tok_row<kEnt>(st, xl, lab_ok, a.inv_t, &log_s);
+        if (warp == 0) {
+            st = tok_empty();
+            for (int i = lane; i < kW * static_cast<int>(C); i += 32)
+                st = tok_merge<kEnt>(st, TokState{x.slot[i].x, x.slot[i].y, x.slot[i].z}, a.k);
+            st = tok_warp_reduce<kEnt>(st, a.k);
+            if (tid == 0) {
+                TokRow r;
+                if (kMode == kObjPolicy) {
+                    r = policy_row<kEnt>(a, st, xl, lab_ok, w, adv, old, ref);
+                    a.loss[row] = r.loss;
+                } else {
+                    float log_s;
+                    r = tok_row<kEnt>(st, xl, lab_ok, a.inv_t, &log_s);
+                }
+                a.logp[row] = r.logp;
+                if (kEnt && a.entropy) a.entropy[row] = r.entropy;
+                if (kMode == kObjPreference && a.row_state)
+                    a.row_state[row] = make_float4(st.m, 1.0f / st.s, 0.0f, 0.0f);
+                if (!lab_ok) atomicAdd(&g_objective_status[0], 1ull);
             }
-            a.logp[row] = r.logp;
-            if (kEnt && a.entropy) a.entropy[row] = r.entropy;
-            if (kMode == kObjPreference && a.row_state)
-                a.row_state[row] = make_float4(st.m, 1.0f / st.s, 0.0f, 0.0f);
-            if (!lab_ok) atomicAdd(&g_objective_status[0], 1ull);
         }
-        ++used;
-        __syncthreads();  // red is rewritten for the next row
+        if (row + G < a.rows) __syncthreads();  // the slots are rewritten for the next row
     }
     if (C > 1) {
-        if (used == 0) cluster_wait();  // the first arrive's match, for a cluster that read no row
-        cluster_arrive();               // no CTA leaves while a peer may still push to it
+        // CTA 0 stays while a peer that has not left may still push to it
+        if (failed && tid == 0) atomicAdd(&g_objective_status[1], 1ull);
+        cluster_arrive();
         cluster_wait();
-        if (__syncthreads_or(failed) && tid == 0) atomicAdd(&g_objective_status[1], 1ull);
     }
 }
 
@@ -779,13 +797,29 @@ int elem_size(DType t) { return t == kF32 ? 4 : 2; }
 
 bool wants_entropy(const ObjArgs &a) { return a.entropy != nullptr || a.bonus != 0.0f; }
 
-// CTAs per row: rows are split until there are about four and a half CTAs per
-// SM, down to kRowsMinBytes each
+// CTAs per row of few rows: as many as make at most six CTAs per SM, of at
+// least kRowsMinBytes each. Measured (us, rows of 151936 bf16, by CTAs per row
+// 1 / 2 / 3 / 4 / 6 / 8 / 12 / 16): 16 rows - / 9.2 / - / 7.6 / 6.3 / 6.3 /
+// 6.2 / 6.2; 64 rows - / 14.4 / - / 10.4 / 10.3 / 9.8 / 9.3 / 10.4; 128 rows
+// - / 14.9 / - / 12.4 / 12.4 / 12.4 / 14.4 / 14.7; 300 rows 26.5 / 22.7 / 21.0
+// / 23.7 / 23.9 / 24.0; 456 rows 30.8 / 28.9 / 32.3 / 29.3 / 31.0 / 31.1; 700
+// rows 39.1 / 45.6 / 39.7 / 40.9 / 41.6 / 42.2.
 int split_of(DType t, int64_t rows, int64_t vocab, const DeviceInfo &dev) {
-    if (rows >= 3 * static_cast<int64_t>(dev.sms)) return 1;
-    int64_t c = (9 * static_cast<int64_t>(dev.sms) + 2 * rows - 1) / (2 * std::max<int64_t>(1, rows));
-    c = std::min<int64_t>(c, (vocab * elem_size(t) + kRowsMinBytes - 1) / kRowsMinBytes);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(c, kMaxCluster)));
+    const int64_t fill = 6 * static_cast<int64_t>(dev.sms) / std::max<int64_t>(1, rows);
+    const int64_t parts = (vocab * elem_size(t) + kRowsMinBytes - 1) / kRowsMinBytes;
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fill, parts), kMaxCluster)));
+}
+
+// The same for a forward pass, whose CTAs hold eight to an SM: between one and
+// four waves of whole rows the last wave leaves the GPU half empty, and rows
+// in up to four parts of at least 64 KB end closer together. Measured (us,
+// rows of 151936 bf16, 1 against 4 CTAs per row): 1024 rows (one wave) 52.0,
+// 53.9; 1500 81.8, 74.2; 2000 94.2, 93.7; 3000 137.3, 134.8; 7168 rows of
+// 128256 256, 277; rows of 64 KB (2048 x 32000) 26.9, 34.9 (32.2 in two).
+int forward_split(DType t, int64_t rows, int64_t vocab, const DeviceInfo &dev) {
+    const int64_t wave = 8 * static_cast<int64_t>(dev.sms);
+    if (rows <= wave || rows >= 4 * wave) return split_of(t, rows, vocab, dev);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, vocab * elem_size(t) / 65536)));
 }
 
 int cols_of(int64_t vocab, int c) { return static_cast<int>(((vocab + c - 1) / c + 7) & ~int64_t(7)); }
@@ -811,7 +845,8 @@ cudaError_t set_objective_attributes(const DeviceInfo &dev) {
 }
 
 cudaError_t launch_obj_rows(DType t, ObjMode mode, const ObjArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-    const int c = split_of(t, a.rows, a.vocab, dev);
+    const int c = forward_split(t, a.rows, a.vocab, dev);
+    // a cluster of several CTAs takes one row: they are few then
     const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(a.rows, int64_t(1) << 20));
     ObjArgs aa = a;
     int cols = cols_of(a.vocab, c);
