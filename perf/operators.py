@@ -309,7 +309,8 @@ def _own(st):
         got = ce.policy_loss(*args, **more) if op == "policy_loss" else ce.policy_step(*args, **more)
     else:
         more = dict(ref_logp=st["ref"], weights=st["weights"], kind=c["kind"], beta=c["beta"],
-                    label_smoothing=c["smoothing"], margin=c["margin"], average=c["average"],
+                    label_smoothing=c["smoothing"] if c["kind"] == "sigmoid" else 0.0, margin=c["margin"],
+                    average=c["average"],
                     temperature=c["temperature"])
         args = (st["logits"], st["labels"], st["offsets"], st["scale"])
         names = ("loss", "loss_pairs", "seq_logp", "logp")
