@@ -9,8 +9,10 @@
 //
 // Kernels (all bound by HBM; none uses tensor cores):
 //   k_obj_rows       one read of each logit: log-probability, entropy and the
-//                    policy's loss of a row
+//                    policy's loss of a row, a CTA or a cluster per row
+//   k_obj_rows_warp  the same for many short rows, a warp per row
 //   k_policy_staged  the policy's loss and gradient, rows held in shared memory
+//   k_policy_warp    the same for short rows, held in a warp's registers
 //   k_policy_stream  the same for rows too long to hold: read three times
 //   k_join           a preference batch's rows into sequences, pairs, the loss
 //                    and each row's gradient factor
@@ -53,6 +55,52 @@ struct RowsXchg {
     uint64_t bar;
 };
 
+// A row that takes no part.
+template <int kMode, bool kEnt>
+__device__ __forceinline__ void write_dead_row(const ObjArgs &a, int64_t row) {
+    a.logp[row] = 0.0f;
+    if (kEnt && a.entropy) a.entropy[row] = 0.0f;
+    if (kMode == kObjPolicy) a.loss[row] = 0.0f;
+    if (kMode == kObjPreference && a.row_state) a.row_state[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+}
+
+// A row's numbers beside its logits, and its outputs: one thread's work.
+struct RowNumbers {
+    float xl = 0.0f, old = 0.0f, ref = 0.0f, adv = 0.0f;
+    bool lab_ok = true;
+};
+
+template <typename T, int kMode>
+__device__ __forceinline__ RowNumbers load_numbers(const ObjArgs &a, int64_t row, const T *p) {
+    RowNumbers r;
+    const int64_t label = a.labels[row];
+    if (kMode == kObjPolicy) {
+        r.old = a.old_logp[row];
+        r.adv = a.adv[row];
+        if (a.ref_logp) r.ref = a.ref_logp[row];
+    }
+    r.lab_ok = in_range(label, a.vocab);
+    if (r.lab_ok) r.xl = Vec<T>::to_float(p[label]);
+    return r;
+}
+
+template <int kMode, bool kEnt>
+__device__ __forceinline__ void write_row(const ObjArgs &a, int64_t row, const TokState &st, const RowNumbers &x,
+                                          float w) {
+    TokRow r;
+    if (kMode == kObjPolicy) {
+        r = policy_row<kEnt>(a, st, x.xl, x.lab_ok, w, x.adv, x.old, x.ref);
+        a.loss[row] = r.loss;
+    } else {
+        float log_s;
+        r = tok_row<kEnt>(st, x.xl, x.lab_ok, a.inv_t, &log_s);
+    }
+    a.logp[row] = r.logp;
+    if (kEnt && a.entropy) a.entropy[row] = r.entropy;
+    if (kMode == kObjPreference && a.row_state) a.row_state[row] = make_float4(st.m, 1.0f / st.s, 0.0f, 0.0f);
+    if (!x.lab_ok) atomicAdd(&g_objective_status[0], 1ull);
+}
+
 template <typename T, int kMode, bool kEnt>
 __global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows(ObjArgs a, int cols) {
     constexpr int kW = kScanThreads / 32;
@@ -82,33 +130,19 @@ __global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows(ObjArgs a, int col
     for (int64_t row = cluster_id_x(); row < a.rows; row += G) {
         const float w = a.weights ? a.weights[row] : 1.0f;
         if (w == 0.0f || (kMode == kObjPreference && (row < first || row >= last))) {
-            if (rank == 0 && tid == 0) {
-                a.logp[row] = 0.0f;
-                if (kEnt && a.entropy) a.entropy[row] = 0.0f;
-                if (kMode == kObjPolicy) a.loss[row] = 0.0f;
-                if (kMode == kObjPreference && a.row_state) a.row_state[row] = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
+            if (rank == 0 && tid == 0) write_dead_row<kMode, kEnt>(a, row);
             if (C > 1) cluster_wait();
             continue;
         }
         const T *p = static_cast<const T *>(a.logits) + row * a.stride;
-        float xl = 0.0f, old = 0.0f, ref = 0.0f, adv = 0.0f;
-        bool lab_ok = true;
         // the row's numbers, by the thread that writes it. Not before the scan's
         // first loads: its warp would wait for the label before it asked for
         // logits, and the CTA for its warp (8192 x 128256: 300 -> 439 us)
-        auto numbers = [&] {
-            if (rank != 0 || tid != 0) return;
-            const int64_t label = a.labels[row];
-            if (kMode == kObjPolicy) {
-                old = a.old_logp[row];
-                adv = a.adv[row];
-                if (a.ref_logp) ref = a.ref_logp[row];
-            }
-            lab_ok = in_range(label, a.vocab);
-            if (lab_ok) xl = Vec<T>::to_float(p[label]);
+        RowNumbers numbers;
+        auto early = [&] {
+            if (rank == 0 && tid == 0) numbers = load_numbers<T, kMode>(a, row, p);
         };
-        TokState st = tok_scan<T, kEnt, kScanUnroll, kScanThreads>(p + c0, n, a.k, tid, numbers);
+        TokState st = tok_scan<T, kEnt, kScanUnroll, kScanThreads>(p + c0, n, a.k, tid, early);
         st = tok_warp_reduce<kEnt>(st, a.k);
         const float4 mine = make_float4(st.m, st.s, st.u, 0.0f);
         if (C > 1) {
@@ -125,21 +159,7 @@ __global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows(ObjArgs a, int col
             for (int i = lane; i < kW * static_cast<int>(C); i += 32)
                 st = tok_merge<kEnt>(st, TokState{x.slot[i].x, x.slot[i].y, x.slot[i].z}, a.k);
             st = tok_warp_reduce<kEnt>(st, a.k);
-            if (tid == 0) {
-                TokRow r;
-                if (kMode == kObjPolicy) {
-                    r = policy_row<kEnt>(a, st, xl, lab_ok, w, adv, old, ref);
-                    a.loss[row] = r.loss;
-                } else {
-                    float log_s;
-                    r = tok_row<kEnt>(st, xl, lab_ok, a.inv_t, &log_s);
-                }
-                a.logp[row] = r.logp;
-                if (kEnt && a.entropy) a.entropy[row] = r.entropy;
-                if (kMode == kObjPreference && a.row_state)
-                    a.row_state[row] = make_float4(st.m, 1.0f / st.s, 0.0f, 0.0f);
-                if (!lab_ok) atomicAdd(&g_objective_status[0], 1ull);
-            }
+            if (tid == 0) write_row<kMode, kEnt>(a, row, st, numbers, w);
         }
         if (row + G < a.rows) __syncthreads();  // the slots are rewritten for the next row
     }
@@ -148,6 +168,36 @@ __global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows(ObjArgs a, int col
         if (failed && tid == 0) atomicAdd(&g_objective_status[1], 1ull);
         cluster_arrive();
         cluster_wait();
+    }
+}
+
+// k_obj_rows_warp: the same for many short rows, a warp per row: no barrier, no
+// exchange, four rows per CTA.
+template <typename T, int kMode, bool kEnt>
+__global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows_warp(ObjArgs a) {
+    launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kScanThreads / 32);
+    int64_t first = 0, last = a.rows;
+    if (kMode == kObjPreference) {
+        first = a.offsets[0];
+        last = a.offsets[2 * a.pairs];
+        if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
+    }
+    for (int64_t row = blockIdx.x * int64_t(kScanThreads / 32) + (threadIdx.x >> 5); row < a.rows; row += warps) {
+        const float w = a.weights ? a.weights[row] : 1.0f;
+        if (w == 0.0f || (kMode == kObjPreference && (row < first || row >= last))) {
+            if (lane == 0) write_dead_row<kMode, kEnt>(a, row);
+            continue;
+        }
+        const T *p = static_cast<const T *>(a.logits) + row * a.stride;
+        RowNumbers numbers;
+        auto early = [&] {
+            if (lane == 0) numbers = load_numbers<T, kMode>(a, row, p);
+        };
+        TokState st = tok_scan<T, kEnt, kScanUnroll, 32>(p, a.vocab, a.k, lane, early);
+        st = tok_warp_reduce<kEnt>(st, a.k);
+        if (lane == 0) write_row<kMode, kEnt>(a, row, st, numbers, w);
     }
 }
 
@@ -511,6 +561,95 @@ __global__ void __launch_bounds__(kStagedThreads, 8) k_policy_staged(ObjArgs a, 
 }
 
 // ---------------------------------------------------------------------------
+// k_policy_warp: the policy's loss and gradient of short rows, a warp per row
+// that it holds in registers (at most kV vectors per lane, and a partial vector
+// at either end by single elements).
+template <typename T, bool kEnt, int kV>
+__global__ void __launch_bounds__(kScanThreads, kV > 8 ? 3 : kV > 4 ? 6 : 8) k_policy_warp(ObjArgs a) {
+    constexpr int N = Vec<T>::kN;
+    launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kScanThreads / 32);
+    for (int64_t row = blockIdx.x * int64_t(kScanThreads / 32) + (threadIdx.x >> 5); row < a.rows; row += warps) {
+        const float w = a.weights ? a.weights[row] : 1.0f;
+        T *g = static_cast<T *>(a.grad) + row * a.grad_stride;
+        if (w == 0.0f) {
+            zero_slice(g, a.vocab, lane, 32);
+            if (lane == 0) write_dead_row<kObjPolicy, kEnt>(a, row);
+            continue;
+        }
+        const T *p = static_cast<const T *>(a.logits) + row * a.stride;
+        const int off = static_cast<int>((reinterpret_cast<uintptr_t>(p) / sizeof(T)) % N);
+        const int head = min(a.vocab, (N - off) % N), nvec = (a.vocab - head) / N, tail = a.vocab - head - N * nvec;
+        const uint4 *pv = reinterpret_cast<const uint4 *>(p + head);
+        uint4 v[kV];
+#pragma unroll
+        for (int u = 0; u < kV; ++u) v[u] = lane + 32 * u < nvec ? __ldcs(pv + lane + 32 * u) : Vec<T>::lowest();
+        const int je = lane < head ? lane : lane < head + tail ? N * nvec + lane : -1;  // a single element's column
+        float xe = je >= 0 ? Vec<T>::to_float(p[je]) : -INFINITY;
+        const RowNumbers x = load_numbers<T, kObjPolicy>(a, row, p);
+        TokState st = tok_empty();
+#pragma unroll
+        for (int u = 0; u < kV; u += 4) {
+            const uint4 four[4] = {v[u], v[u + 1], v[u + 2], v[u + 3]};
+            tok_push<T, kEnt, 4>(st, four, a.k);
+        }
+        if (je >= 0) tok_push1<kEnt>(st, xe, a.k);
+        st = tok_warp_reduce<kEnt>(st, a.k);
+        const TokRow r = policy_row<kEnt>(a, st, x.xl, x.lab_ok, w, x.adv, x.old, x.ref);
+        if (lane == 0) {
+            a.logp[row] = r.logp;
+            a.loss[row] = r.loss;
+            if (kEnt && a.entropy) a.entropy[row] = r.entropy;
+            if (!x.lab_ok) atomicAdd(&g_objective_status[0], 1ull);
+        }
+        const int lab = x.lab_ok ? static_cast<int>(a.labels[row]) : -1;
+        auto one = [&](int j, float xj) {
+            g[j] = Vec<T>::from_float(j == lab ? tok_label1<kEnt>(xj, r.m, a.k, r.a, r.b, r.c)
+                                               : tok_grad1<kEnt>(xj, r.m, a.k, r.a, r.b));
+        };
+        const int headg = static_cast<int>((N - (reinterpret_cast<uintptr_t>(g) / sizeof(T)) % N) % N);
+        const int by = (headg - (N - off) % N + N) % N;  // the gradient's grid against the logits'
+        if (by == 0) {
+            uint4 *gv = reinterpret_cast<uint4 *>(g + head);
+#pragma unroll
+            for (int u = 0; u < kV; ++u)
+                if (lane + 32 * u < nvec) __stcs(gv + lane + 32 * u, tok_grad_vec<T, kEnt>(v[u], r.m, a.k, r.a, r.b));
+            if (je >= 0) one(je, xe);
+            // the label's element of a vector, again, by the lane that wrote it
+            const unsigned li = static_cast<unsigned>(lab - head);
+            if (li < static_cast<unsigned>(N * nvec) && static_cast<int>(li / N) % 32 == lane) one(lab, x.xl);
+        } else {
+            // vector q of the gradient's grid from vectors q and q + 1 of the
+            // logits', the second the next lane's; what lies before the first
+            // and behind the last one by one
+            uint4 *gv = reinterpret_cast<uint4 *>(g + head + by);
+#pragma unroll
+            for (int u = 0; u < kV; ++u) v[u] = tok_grad_vec<T, kEnt>(v[u], r.m, a.k, r.a, r.b);
+#pragma unroll
+            for (int u = 0; u < kV; ++u) {
+                uint4 next = v[u];
+                if (lane == 0 && u + 1 < kV) next = v[u + 1 < kV ? u + 1 : u];
+                next.x = __shfl_sync(kFullMask, next.x, (lane + 1) & 31);
+                next.y = __shfl_sync(kFullMask, next.y, (lane + 1) & 31);
+                next.z = __shfl_sync(kFullMask, next.z, (lane + 1) & 31);
+                next.w = __shfl_sync(kFullMask, next.w, (lane + 1) & 31);
+                if (lane + 32 * u + 1 < nvec) __stcs(gv + lane + 32 * u, shift_pair<T>(v[u], next, by));
+            }
+            const int whole = max(0, nvec - 1);
+            const int before = whole > 0 ? head + by : a.vocab, behind = head + by + N * whole;
+            const int singles = whole > 0 ? before + a.vocab - behind : a.vocab;
+            for (int i = lane; i < singles; i += 32) {
+                const int j = i < before ? i : behind + i - before;
+                one(j, Vec<T>::to_float(p[j]));
+            }
+            const unsigned li = static_cast<unsigned>(lab - head - by);
+            if (li < static_cast<unsigned>(N * whole) && static_cast<int>(li / N) % 32 == lane) one(lab, x.xl);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
 // k_join: one CTA per pair (looping). Half of its threads sum the chosen
 // sequence's w logp (and w, for averages), half the rejected's, each in a fixed
 // order; one thread forms the pair's loss and the factors
@@ -753,20 +892,24 @@ struct LaunchConfig {
     }
 };
 
-template <typename T>
-const void *rows_kernel_t(ObjMode mode, bool ent) {
-    if (mode == kObjPreference) return reinterpret_cast<const void *>(&k_obj_rows<T, kObjPreference, false>);
-    if (mode == kObjPolicy)
-        return ent ? reinterpret_cast<const void *>(&k_obj_rows<T, kObjPolicy, true>)
-                   : reinterpret_cast<const void *>(&k_obj_rows<T, kObjPolicy, false>);
-    return ent ? reinterpret_cast<const void *>(&k_obj_rows<T, kObjLogp, true>)
-               : reinterpret_cast<const void *>(&k_obj_rows<T, kObjLogp, false>);
+template <typename T, int kMode, bool kEnt>
+const void *rows_kernel_m(bool warp) {
+    return warp ? reinterpret_cast<const void *>(&k_obj_rows_warp<T, kMode, kEnt>)
+                : reinterpret_cast<const void *>(&k_obj_rows<T, kMode, kEnt>);
 }
 
-const void *rows_kernel(DType t, ObjMode mode, bool ent) {
-    return t == kF32    ? rows_kernel_t<float>(mode, ent)
-           : t == kBF16 ? rows_kernel_t<__nv_bfloat16>(mode, ent)
-                        : rows_kernel_t<__half>(mode, ent);
+template <typename T>
+const void *rows_kernel_t(ObjMode mode, bool ent, bool warp) {
+    if (mode == kObjPreference) return rows_kernel_m<T, kObjPreference, false>(warp);
+    if (mode == kObjPolicy)
+        return ent ? rows_kernel_m<T, kObjPolicy, true>(warp) : rows_kernel_m<T, kObjPolicy, false>(warp);
+    return ent ? rows_kernel_m<T, kObjLogp, true>(warp) : rows_kernel_m<T, kObjLogp, false>(warp);
+}
+
+const void *rows_kernel(DType t, ObjMode mode, bool ent, bool warp) {
+    return t == kF32    ? rows_kernel_t<float>(mode, ent, warp)
+           : t == kBF16 ? rows_kernel_t<__nv_bfloat16>(mode, ent, warp)
+                        : rows_kernel_t<__half>(mode, ent, warp);
 }
 
 template <typename T>
@@ -791,6 +934,19 @@ const void *policy_staged(DType t, bool ent) {
     return t == kF32    ? policy_staged_t<float>(ent)
            : t == kBF16 ? policy_staged_t<__nv_bfloat16>(ent)
                         : policy_staged_t<__half>(ent);
+}
+
+template <typename T, int kV>
+const void *policy_warp_t(bool ent) {
+    return ent ? reinterpret_cast<const void *>(&k_policy_warp<T, true, kV>)
+               : reinterpret_cast<const void *>(&k_policy_warp<T, false, kV>);
+}
+
+template <int kV>
+const void *policy_warp_v(DType t, bool ent) {
+    return t == kF32    ? policy_warp_t<float, kV>(ent)
+           : t == kBF16 ? policy_warp_t<__nv_bfloat16, kV>(ent)
+                        : policy_warp_t<__half, kV>(ent);
 }
 
 int elem_size(DType t) { return t == kF32 ? 4 : 2; }
@@ -822,6 +978,27 @@ int forward_split(DType t, int64_t rows, int64_t vocab, const DeviceInfo &dev) {
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, vocab * elem_size(t) / 65536)));
 }
 
+// Where a warp per row beats a CTA per row. Measured (us, f16 policy losses,
+// warp against CTA, rows of 2000 / 4000 / 8000 / 16000 / 32000 / 50257): 300
+// rows 6.3, 7.8 / 8.0, 8.1 / 8.3, 8.3 / 14.2, 10.3 / 20.9, 12.4 / 30, 14; 1200
+// rows 8.2, 10.3 / 10.3, 10.3 / 12.4, 11.5 / 16.4, 15.0 / 24.7, 19.0; 2400 rows
+// 8.3, 14.4 / 12.3, 14.4 / 14.5, 16.1 / 20.5, 21.8 / 31.3, 30.8; 8192 rows
+// 14.5, 31.0 / 22.6, 32.6 / 31.3, 33.0 / 46.2, 51.2 / 82.8, 78.4 / 126, 123.
+bool forward_warp(DType t, int64_t rows, int64_t vocab, const DeviceInfo &dev) {
+    const int64_t bytes = vocab * elem_size(t);
+    return bytes <= 8192 || (bytes <= 32768 && rows >= 12 * static_cast<int64_t>(dev.sms));
+}
+
+// Rows a warp holds in its registers. Measured (us, policy steps, warp against
+// staged CTA): 8192 rows of 1000 bf16 12.4, 32.9, of 2000 19.2, 36.0, of 4000
+// 31.1, 43.7, of 2000 f32 27.1, 40.6; 300 rows of 2000 bf16 6.2, 8.2.
+constexpr int64_t kWarpStepBytes = 8192;
+
+int64_t warp_ctas(int64_t rows) {
+    constexpr int kPer = kScanThreads / 32;
+    return std::max<int64_t>(1, std::min<int64_t>((rows + kPer - 1) / kPer, int64_t(1) << 20));
+}
+
 int cols_of(int64_t vocab, int c) { return static_cast<int>(((vocab + c - 1) / c + 7) & ~int64_t(7)); }
 
 }  // namespace
@@ -830,7 +1007,7 @@ cudaError_t set_objective_attributes(const DeviceInfo &dev) {
     for (DType t : {kF32, kBF16, kF16})
         for (bool ent : {false, true}) {
             for (ObjMode m : {kObjLogp, kObjPolicy, kObjPreference}) {
-                cudaError_t e = cudaFuncSetAttribute(rows_kernel(t, m, ent), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+                cudaError_t e = cudaFuncSetAttribute(rows_kernel(t, m, ent, false), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
                 if (e != cudaSuccess) return e;
             }
             for (const void *f : {policy_stream(t, ent), policy_staged(t, ent)}) {
@@ -845,6 +1022,12 @@ cudaError_t set_objective_attributes(const DeviceInfo &dev) {
 }
 
 cudaError_t launch_obj_rows(DType t, ObjMode mode, const ObjArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+    if (forward_warp(t, a.rows, a.vocab, dev)) {
+        ObjArgs aa = a;
+        void *args[] = {&aa};
+        LaunchConfig l(warp_ctas(a.rows), kScanThreads, 0, false, s);
+        return cudaLaunchKernelExC(&l.cfg, rows_kernel(t, mode, wants_entropy(a), true), args);
+    }
     const int c = forward_split(t, a.rows, a.vocab, dev);
     // a cluster of several CTAs takes one row: they are few then
     const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(a.rows, int64_t(1) << 20));
@@ -852,7 +1035,7 @@ cudaError_t launch_obj_rows(DType t, ObjMode mode, const ObjArgs &a, const Devic
     int cols = cols_of(a.vocab, c);
     void *args[] = {&aa, &cols};
     LaunchConfig l(clusters * c, kScanThreads, c, false, s);
-    return cudaLaunchKernelExC(&l.cfg, rows_kernel(t, mode, wants_entropy(a)), args);
+    return cudaLaunchKernelExC(&l.cfg, rows_kernel(t, mode, wants_entropy(a), false), args);
 }
 
 // Shared memory of a staged CTA that holds `cols` columns at any phase.
@@ -891,6 +1074,14 @@ cudaError_t launch_policy_grad(DType t, const ObjArgs &a, const DeviceInfo &dev,
     const bool ent = wants_entropy(a);
     const int64_t clusters = std::min<int64_t>(a.rows, int64_t(1) << 20);
     ObjArgs aa = a;
+    const int64_t bytes = static_cast<int64_t>(a.vocab) * elem_size(t);
+    if (bytes <= kWarpStepBytes) {
+        void *args[] = {&aa};
+        LaunchConfig l(warp_ctas(a.rows), kScanThreads, 0, false, s);
+        return cudaLaunchKernelExC(&l.cfg, bytes <= 2048   ? policy_warp_v<4>(t, ent)
+                                           : bytes <= 4096 ? policy_warp_v<8>(t, ent)
+                                                           : policy_warp_v<16>(t, ent), args);
+    }
     int c = staged_split(t, a.rows, a.vocab, dev);
     const bool staged = c > 0;
     if (!staged) c = kMaxCluster;  // rows too long for the shared memory of a cluster
