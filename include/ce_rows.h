@@ -420,8 +420,8 @@ CE_API int policy_loss(const void *logits, int dtype, int64_t rows, int64_t voca
  * policy_step: policy_loss and its gradient, with
  *     g = [-A r where -A r is the larger term, or the terms are equal] + kl_coef (1 - exp(d)):
  *     grad[i, j] = scale weights_i / T (g ([j == label] - p_j) + entropy_coef p_j (log p_j + H)).
- * Each logit is read once from HBM and each gradient written once (rows of
- * more than about 3.5 MB are read three times).
+ * Each logit is read once from HBM and each gradient written once (rows that
+ * do not fit the shared memory of 16 CTAs, about 3.5 MB, are read twice).
  */
 CE_API int policy_step(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,
                        const int64_t *labels, const float *old_logp, const float *advantages, const float *ref_logp,
@@ -509,7 +509,8 @@ CE_API int ce_device_wait_timeouts(ce_stream_t stream, int64_t *out);
 CE_API int ce_device_error_reset(ce_stream_t stream);
 
 /*
- * Launch-plan override, for tests and tuning: forces the kernel family
+ * Launch-plan override, for tests and tuning (not of the objectives, whose
+ * kernels follow from sizes and types alone): forces the kernel family
  * (path: 0 automatic, 1 shared-memory-staged (persistent), 2 streaming from
  * global, 3 refused (formerly a ring-of-copies kernel), 4
  * shared-memory-staged with one row per cluster, 5 refused (the argmax split

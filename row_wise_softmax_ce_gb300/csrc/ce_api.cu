@@ -687,6 +687,8 @@ static int check_objective(const void *logits, int dtype, int64_t rows, int64_t 
     a->inv_t = static_cast<float>(1.0 / temperature);
     a->scale = static_cast<float>(scale);
     a->logp = const_cast<float *>(logp);
+    std::lock_guard<std::mutex> lock(g_mu);
+    a->grid_cap = g_force.grid_cap;
     return CE_OK;
 }
 

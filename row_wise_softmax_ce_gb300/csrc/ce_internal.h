@@ -116,6 +116,7 @@ struct ObjArgs {
     int64_t pairs;
     float4 *row_state;  // [rows] (m, 1 / s, factor, -)
     uint32_t *done;     // join CTAs that have written their pairs
+    int64_t grid_cap;   // at most this many clusters (0: no cap)
 };
 
 // The join of a preference batch's rows into sequences, pairs and the loss.

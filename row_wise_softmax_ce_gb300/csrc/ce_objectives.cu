@@ -13,7 +13,7 @@
 //   k_obj_rows_warp  the same for many short rows, a warp per row
 //   k_policy_staged  the policy's loss and gradient, rows held in shared memory
 //   k_policy_warp    the same for short rows, held in a warp's registers
-//   k_policy_stream  the same for rows too long to hold: read three times
+//   k_policy_stream  the same for rows too long to hold: read twice
 //   k_join           a preference batch's rows into sequences, pairs, the loss
 //                    and each row's gradient factor
 //   k_pair_grad      the gradient of a preference batch, the rows read again
@@ -47,7 +47,7 @@ __device__ __forceinline__ bool in_range(int64_t label, int vocab) { return labe
 
 // ---------------------------------------------------------------------------
 // k_obj_rows: one CTA per row (looping), or few rows over clusters of C CTAs,
-// a row each: every warp scans its part of a contiguous slice of `cols`
+// exactly one row each: every warp scans its part of a contiguous slice of `cols`
 // columns and pushes its state into CTA 0's shared memory, whose first warp
 // merges them and writes the row.
 struct RowsXchg {
@@ -994,9 +994,15 @@ bool forward_warp(DType t, int64_t rows, int64_t vocab, const DeviceInfo &dev) {
 // 31.1, 43.7, of 2000 f32 27.1, 40.6; 300 rows of 2000 bf16 6.2, 8.2.
 constexpr int64_t kWarpStepBytes = 8192;
 
-int64_t warp_ctas(int64_t rows) {
+// Every row kernel loops over rows, so fewer clusters (or CTAs of a warp per
+// row) only take more rows each.
+int64_t capped(int64_t clusters, const ObjArgs &a) {
+    clusters = std::min<int64_t>(clusters, int64_t(1) << 20);
+    return std::max<int64_t>(1, a.grid_cap > 0 ? std::min(clusters, a.grid_cap) : clusters);
+}
+int64_t warp_ctas(const ObjArgs &a) {
     constexpr int kPer = kScanThreads / 32;
-    return std::max<int64_t>(1, std::min<int64_t>((rows + kPer - 1) / kPer, int64_t(1) << 20));
+    return capped((a.rows + kPer - 1) / kPer, a);
 }
 
 int cols_of(int64_t vocab, int c) { return static_cast<int>(((vocab + c - 1) / c + 7) & ~int64_t(7)); }
@@ -1025,12 +1031,12 @@ cudaError_t launch_obj_rows(DType t, ObjMode mode, const ObjArgs &a, const Devic
     if (forward_warp(t, a.rows, a.vocab, dev)) {
         ObjArgs aa = a;
         void *args[] = {&aa};
-        LaunchConfig l(warp_ctas(a.rows), kScanThreads, 0, false, s);
+        LaunchConfig l(warp_ctas(a), kScanThreads, 0, false, s);
         return cudaLaunchKernelExC(&l.cfg, rows_kernel(t, mode, wants_entropy(a), true), args);
     }
-    const int c = forward_split(t, a.rows, a.vocab, dev);
-    // a cluster of several CTAs takes one row: they are few then
-    const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(a.rows, int64_t(1) << 20));
+    // a cluster of several CTAs takes one row, no more and no fewer
+    const int64_t clusters = capped(a.rows, a);
+    const int c = clusters == a.rows ? forward_split(t, a.rows, a.vocab, dev) : 1;
     ObjArgs aa = a;
     int cols = cols_of(a.vocab, c);
     void *args[] = {&aa, &cols};
@@ -1072,12 +1078,12 @@ static int staged_split(DType t, int64_t rows, int64_t vocab, const DeviceInfo &
 
 cudaError_t launch_policy_grad(DType t, const ObjArgs &a, const DeviceInfo &dev, cudaStream_t s) {
     const bool ent = wants_entropy(a);
-    const int64_t clusters = std::min<int64_t>(a.rows, int64_t(1) << 20);
+    const int64_t clusters = capped(a.rows, a);
     ObjArgs aa = a;
     const int64_t bytes = static_cast<int64_t>(a.vocab) * elem_size(t);
     if (bytes <= kWarpStepBytes) {
         void *args[] = {&aa};
-        LaunchConfig l(warp_ctas(a.rows), kScanThreads, 0, false, s);
+        LaunchConfig l(warp_ctas(a), kScanThreads, 0, false, s);
         return cudaLaunchKernelExC(&l.cfg, bytes <= 2048   ? policy_warp_v<4>(t, ent)
                                            : bytes <= 4096 ? policy_warp_v<8>(t, ent)
                                                            : policy_warp_v<16>(t, ent), args);
