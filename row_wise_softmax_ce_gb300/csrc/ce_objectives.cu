@@ -64,6 +64,15 @@ __device__ __forceinline__ void write_dead_row(const ObjArgs &a, int64_t row) {
     if (kMode == kObjPreference && a.row_state) a.row_state[row] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
+// A row's label, asked for beside its weight and first used once the row's
+// first logits are on their way: not one more latency in a row of few logits.
+// volatile keeps the load where it is written.
+__device__ __forceinline__ int64_t ld_label(const int64_t *p) {
+    int64_t v;
+    asm volatile("ld.global.nc.s64 %0, [%1];" : "=l"(v) : "l"(p));
+    return v;
+}
+
 // A row's numbers beside its logits, and its outputs: one thread's work.
 struct RowNumbers {
     float xl = 0.0f, old = 0.0f, ref = 0.0f, adv = 0.0f;
@@ -71,9 +80,8 @@ struct RowNumbers {
 };
 
 template <typename T, int kMode>
-__device__ __forceinline__ RowNumbers load_numbers(const ObjArgs &a, int64_t row, const T *p) {
+__device__ __forceinline__ RowNumbers load_numbers(const ObjArgs &a, int64_t row, const T *p, int64_t label) {
     RowNumbers r;
-    const int64_t label = a.labels[row];
     if (kMode == kObjPolicy) {
         r.old = a.old_logp[row];
         r.adv = a.adv[row];
@@ -128,6 +136,8 @@ __global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows(ObjArgs a, int col
     }
     bool failed = false;
     for (int64_t row = cluster_id_x(); row < a.rows; row += G) {
+        int64_t label = 0;
+        if (rank == 0 && tid == 0) label = ld_label(a.labels + row);
         const float w = a.weights ? a.weights[row] : 1.0f;
         if (w == 0.0f || (kMode == kObjPreference && (row < first || row >= last))) {
             if (rank == 0 && tid == 0) write_dead_row<kMode, kEnt>(a, row);
@@ -140,7 +150,7 @@ __global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows(ObjArgs a, int col
         // logits, and the CTA for its warp (8192 x 128256: 300 -> 439 us)
         RowNumbers numbers;
         auto early = [&] {
-            if (rank == 0 && tid == 0) numbers = load_numbers<T, kMode>(a, row, p);
+            if (rank == 0 && tid == 0) numbers = load_numbers<T, kMode>(a, row, p, label);
         };
         TokState st = tok_scan<T, kEnt, kScanUnroll, kScanThreads>(p + c0, n, a.k, tid, early);
         st = tok_warp_reduce<kEnt>(st, a.k);
@@ -185,6 +195,8 @@ __global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows_warp(ObjArgs a) {
         if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
     }
     for (int64_t row = blockIdx.x * int64_t(kScanThreads / 32) + (threadIdx.x >> 5); row < a.rows; row += warps) {
+        int64_t label = 0;
+        if (lane == 0) label = ld_label(a.labels + row);
         const float w = a.weights ? a.weights[row] : 1.0f;
         if (w == 0.0f || (kMode == kObjPreference && (row < first || row >= last))) {
             if (lane == 0) write_dead_row<kMode, kEnt>(a, row);
@@ -193,7 +205,7 @@ __global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows_warp(ObjArgs a) {
         const T *p = static_cast<const T *>(a.logits) + row * a.stride;
         RowNumbers numbers;
         auto early = [&] {
-            if (lane == 0) numbers = load_numbers<T, kMode>(a, row, p);
+            if (lane == 0) numbers = load_numbers<T, kMode>(a, row, p, label);
         };
         TokState st = tok_scan<T, kEnt, kScanUnroll, 32>(p, a.vocab, a.k, lane, early);
         st = tok_warp_reduce<kEnt>(st, a.k);
@@ -571,6 +583,7 @@ __global__ void __launch_bounds__(kScanThreads, kV > 8 ? 3 : kV > 4 ? 6 : 8) k_p
     const int lane = threadIdx.x & 31;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * (kScanThreads / 32);
     for (int64_t row = blockIdx.x * int64_t(kScanThreads / 32) + (threadIdx.x >> 5); row < a.rows; row += warps) {
+        const int64_t label = ld_label(a.labels + row);
         const float w = a.weights ? a.weights[row] : 1.0f;
         T *g = static_cast<T *>(a.grad) + row * a.grad_stride;
         if (w == 0.0f) {
@@ -587,7 +600,7 @@ __global__ void __launch_bounds__(kScanThreads, kV > 8 ? 3 : kV > 4 ? 6 : 8) k_p
         for (int u = 0; u < kV; ++u) v[u] = lane + 32 * u < nvec ? __ldcs(pv + lane + 32 * u) : Vec<T>::lowest();
         const int je = lane < head ? lane : lane < head + tail ? N * nvec + lane : -1;  // a single element's column
         float xe = je >= 0 ? Vec<T>::to_float(p[je]) : -INFINITY;
-        const RowNumbers x = load_numbers<T, kObjPolicy>(a, row, p);
+        const RowNumbers x = load_numbers<T, kObjPolicy>(a, row, p, label);
         TokState st = tok_empty();
 #pragma unroll
         for (int u = 0; u < kV; u += 4) {
@@ -603,7 +616,7 @@ __global__ void __launch_bounds__(kScanThreads, kV > 8 ? 3 : kV > 4 ? 6 : 8) k_p
             if (kEnt && a.entropy) a.entropy[row] = r.entropy;
             if (!x.lab_ok) atomicAdd(&g_objective_status[0], 1ull);
         }
-        const int lab = x.lab_ok ? static_cast<int>(a.labels[row]) : -1;
+        const int lab = x.lab_ok ? static_cast<int>(label) : -1;
         auto one = [&](int j, float xj) {
             g[j] = Vec<T>::from_float(j == lab ? tok_label1<kEnt>(xj, r.m, a.k, r.a, r.b, r.c)
                                                : tok_grad1<kEnt>(xj, r.m, a.k, r.a, r.b));
@@ -697,13 +710,20 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(JoinArgs j) {
     __shared__ float factor[2];
     __shared__ bool last;
     launch_dependents();
-    wait_prerequisites();
     constexpr int kHalf = kJoinThreads / 2;
     const int side = threadIdx.x / kHalf, t = threadIdx.x % kHalf, lane = t & 31, warp = t >> 5;
     const int64_t P = j.pairs;
-    for (int64_t pair = blockIdx.x; pair < P; pair += gridDim.x) {
+    // the first pair's range is an input: read while the rows are still being read
+    int64_t r0 = 0, r1 = 0;
+    auto range = [&](int64_t pair) {
         const int64_t s = side == 0 ? pair : P + pair;
-        const int64_t r0 = j.offsets[s], r1 = j.offsets[s + 1];
+        r0 = j.offsets[s];
+        r1 = j.offsets[s + 1];
+    };
+    if (blockIdx.x < P) range(blockIdx.x);
+    wait_prerequisites();
+    for (int64_t pair = blockIdx.x; pair < P; pair += gridDim.x) {
+        if (pair != blockIdx.x) range(pair);
         const bool ok = r0 >= 0 && r0 <= r1 && r1 <= j.rows;
         Sum2 sum{ok ? 0.0f : nan_f(), 0.0f}, count{0.0f, 0.0f};
         if (ok) {
@@ -800,9 +820,8 @@ template <typename T>
 __global__ void __launch_bounds__(kPairThreads) k_pair_grad(ObjArgs a, int parts) {
     constexpr int kCols = kPartBytes / static_cast<int>(sizeof(T));
     wait_prerequisites();
-    const int64_t unit = static_cast<int64_t>(gridDim.x) - 1 - blockIdx.x;
-    const int64_t row = unit / parts;
-    const int c0 = static_cast<int>(unit % parts) * kCols;
+    const int64_t row = blockIdx.x / parts;
+    const int c0 = static_cast<int>(blockIdx.x % parts) * kCols;
     const int n = min(a.vocab - c0, kCols);
     T *g = static_cast<T *>(a.grad) + row * a.grad_stride + c0;
     const float4 st = a.row_state[row];
