@@ -700,7 +700,7 @@ static int check_objective_grad(const void *logits, int dtype, int64_t rows, int
     if (rows > 0 && grad_stride > (INT64_MAX / 4) / rows) return CE_EINVAL;
     if (misaligned(grad, static_cast<uintptr_t>(size))) return CE_EALIGN;
     if (rows == 0) return CE_OK;
-    if (grad == logits) return grad_stride == stride ? CE_OK : CE_EINVAL;
+    if (grad == logits) return grad_stride == stride || rows == 1 ? CE_OK : CE_EINVAL;
     return ranges_overlap(grad, ((rows - 1) * grad_stride + vocab) * size, logits,
                           ((rows - 1) * stride + vocab) * size)
                ? CE_EINVAL

@@ -214,10 +214,6 @@ __global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows_warp(ObjArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Writing a slice of a gradient row: columns [0, n) at g from the logits at p
-// (coherent loads: g may be p), the label's column `lab` (-1: elsewhere)
-// getting c besides. 16-byte loads and stores where the two share their phase
-// of 16 bytes, single elements otherwise.
 // Elements r .. r + N - 1 of the 2 N of two neighbouring vectors.
 template <typename T>
 __device__ __forceinline__ uint4 shift_pair(const uint4 &a, const uint4 &b, int r) {
@@ -232,6 +228,10 @@ __device__ __forceinline__ uint4 shift_pair(const uint4 &a, const uint4 &b, int 
                       __funnelshift_r(v3, v4, half));
 }
 
+// Writing a slice of a gradient row: columns [0, n) at g from the logits at p
+// (coherent loads: g may be p), the label's column `lab` (-1: elsewhere)
+// getting c besides, by 16-byte stores: from the same vectors of the logits
+// where the two share their phase of 16 bytes, from pairs of vectors otherwise.
 template <typename T, bool kB, int kU, int kT>
 __device__ __forceinline__ void write_slice(const T *p, T *g, int n, float m, float k, float a, float b, float c,
                                             int lab, int tid) {
@@ -674,7 +674,7 @@ constexpr int kJoinThreads = 256;
 // lo the sum of the rounding errors, each exact (two-sum), so the pair carries
 // about 48 bits. GB300 adds f64 at about two lanes per clock and SM; an f64
 // butterfly over 8 warps alone takes longer than all the rest of such a sum.
-// lo is NaN once hi overflows or an infinity was added: hi alone is the sum.
+// lo means nothing once hi has overflowed or an infinity was added.
 struct Sum2 {
     float hi, lo;
 };
@@ -687,7 +687,7 @@ __device__ __forceinline__ Sum2 sum2_mul(float w, float x) {
     return Sum2{p, __fmaf_rn(w, x, -p)};
 }
 __device__ __forceinline__ double sum2_value(Sum2 v) {
-    return isnan(v.lo) ? static_cast<double>(v.hi) : static_cast<double>(v.hi) + static_cast<double>(v.lo);
+    return isfinite(v.hi) ? static_cast<double>(v.hi) + static_cast<double>(v.lo) : static_cast<double>(v.hi);
 }
 // over aligned groups of kLanes lanes; every lane gets its group's sum
 template <int kLanes = 32>

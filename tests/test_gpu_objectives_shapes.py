@@ -165,6 +165,33 @@ def test_one_row_of_any_stride():
         check(dict(zip(("grad", "loss", "loss_rows", "logp"), got)), want, "one row")
 
 
+def test_one_row_in_place_of_a_wider_one():
+    """The first columns of a single wider row, in place: the rest of it is left alone."""
+    for dtype in TYPES:
+        x = torch.randn(1, 900, device=DEV).to(dtype)
+        y, f = torch.tensor([3], device=DEV), torch.zeros(1, device=DEV)
+        want, pref = R.policy64(x[:, :700], y, f, f + 1, 1.0), R.preference64(x[:, :700], y, [0, 1, 1], 1.0)
+        z = x.clone()
+        ce.policy_step(z, y, f, f + 1, 1.0, vocab=700, grad=z)
+        R.assert_near(z[:, :700], want["grad"], "policy")
+        assert torch.equal(z[:, 700:], x[:, 700:])
+        z = x.clone()
+        ce.preference_step(z, y, torch.tensor([0, 1, 1], device=DEV), 1.0, vocab=700, grad=z)
+        R.assert_near(z[:, :700], pref["grad"], "preference")
+        assert torch.equal(z[:, 700:], x[:, 700:])
+
+
+def test_sums_that_overflow():
+    """A weighted loss beyond f32 is infinite, not NaN; beyond f32 before the scale only, likewise."""
+    x, y, f = torch.zeros(3, 8, device=DEV), torch.zeros(3, dtype=torch.int64, device=DEV), torch.zeros(3, device=DEV)
+    w = torch.full((3,), 3e38, device=DEV)
+    old = torch.full((3,), -math.log(8) - 10, device=DEV)  # a ratio of e^10, unclipped at a negative advantage
+    loss = ce.policy_loss(x, y, old, f - 1, 1.0, weights=w)[0]
+    assert float(loss) == math.inf
+    seq = ce.preference_loss(x, y, torch.tensor([0, 2, 3], device=DEV), 1.0, weights=w)[2]
+    assert float(seq[0]) == -math.inf and float(seq[1]) == -math.inf
+
+
 def test_large_weights_and_long_sums():
     """A loss summed over more rows than one CTA takes, of both signs."""
     rows = 20011
