@@ -4,7 +4,8 @@ GB300 (sm_103a).
 A thin binding over the C ABI of ``libcerows.so`` (declared in
 ``include/ce_rows.h``): each function checks the tensors it is given,
 passes their device pointers and the current CUDA stream to the entry point
-of the same name, and returns. Every step of the computation runs in the
+of the same name (the objectives' functions from C++, ``_binding.so``), and
+returns. Every step of the computation runs in the
 library's CUDA kernels; there is no other implementation to fall back to, so
 a missing library is an error.
 
@@ -62,14 +63,14 @@ HEADER = os.path.join(os.path.dirname(_PKG), "include", "ce_rows.h")
 CE_OK, CE_EINVAL, CE_EALIGN, CE_ECUDA, CE_EDEVICE, CE_ERANGE = 0, -1, -2, -3, -4, -5
 PATH_AUTO, PATH_STAGED, PATH_STREAM, PATH_STAGED_PER_ROW, PATH_FLAT, PATH_WARP, PATH_RING = 0, 1, 2, 4, 5, 6, 7
 OP_ROWS, OP_GRAD, OP_ARGMAX, OP_SOFTMAX, OP_LOG_SOFTMAX, OP_CANDIDATES = 0, 1, 2, 3, 4, 5
-# logits of the objectives (enum ce_dtype) and kinds of preference loss (enum ce_preference_kind)
-DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+# kinds of preference loss (enum ce_preference_kind)
 PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "squared": 2}
 # candidatesInto's workgroup, TOP_EACH and CANDIDATE_ROW (gizml:netops, Constants)
 CANDIDATE_THREADS, TOP_EACH, CANDIDATE_ROW = 256, 4, 2048
 
 _lock = threading.Lock()
 _lib = None
+_objectives = None
 
 
 class Policy(ctypes.Structure):
@@ -539,84 +540,26 @@ def ce_grad_from_stats(shard: torch.Tensor, labels: torch.Tensor, col0: int, com
 
 # -- objectives over sampled answers and over pairs of answers ---------------------
 
-# The current stream's handle: torch's own accessor without the Stream object
-# around it where there is one (2 us less on calls that take 10 to 20 in all).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+def _bound():
+    """The module of csrc/binding.cpp, with libcerows.so loaded; raises if it has not been built."""
+    global _objectives
+    lib()
+    with _lock:
+        if _objectives is None:
+            try:
+                from . import _binding as module  # an extension module beside this file
+            except ImportError as e:
+                raise RuntimeError("the objectives' binding _binding.so is missing or does not fit this PyTorch: build it "
+                                   "with `python -m row_wise_softmax_ce_gb300.build` (or __graft_entry__.build())") from e
+            _objectives = module
+        return _objectives
 
 
-def _call(name: str, device: torch.device, *args) -> None:
-    """The C entry point `name` on `device` and its current stream."""
-    fn, index = getattr(_lib or lib(), name), device.index
-    if torch.cuda.current_device() == index:
-        status = fn(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, _raw_stream(index))
-    if status != CE_OK:
-        _check(name, status)
-
-
-def _objective_view(logits: torch.Tensor, vocab: int | None):
-    """(dtype, rows, vocab, stride) of f32, bf16 or f16 logits with contiguous rows."""
-    dtype = DTYPES.get(logits.dtype) if isinstance(logits, torch.Tensor) else None
-    if dtype is None:
-        raise TypeError("logits must be a float32, bfloat16 or float16 torch.Tensor")
-    if not logits.is_cuda:
-        raise ValueError("logits must be on a CUDA device")
-    if logits.dim() != 2:
-        raise ValueError("logits must be 2-D [rows, cols]")
-    rows, cols = logits.shape
-    stride, inner = logits.stride()
-    if inner != 1 and rows > 0 and cols > 1:
-        raise ValueError("each row of logits must be contiguous (stride(1) == 1)")
-    vocab = cols if vocab is None else int(vocab)
-    if not 1 <= vocab <= cols:
-        raise ValueError(f"need 1 <= vocab <= logits.shape[1] (vocab={vocab}, cols={cols})")
-    if rows > 1:
-        if stride < vocab:
-            raise ValueError("rows of logits overlap (stride(0) < vocab)")
-    else:
-        stride = cols
-    return dtype, rows, vocab, stride
-
-
-def _per_row(t, n, device, name):
-    """A contiguous f32 [n] input's pointer (None for None)."""
-    if t is None:
-        return None
-    if t.dtype != torch.float32 or t.shape != (n,) or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 tensor [{n}] on {device}")
-    return t.data_ptr()
-
-
-def _f32(n, device):
-    return torch.empty(n, dtype=torch.float32, device=device)
-
-
-def _entropy_out(entropy, rows, device):
-    if entropy is False:
-        return None
-    return _f32(rows, device) if entropy is True else _out(entropy, (rows,), torch.float32, device, "entropy")
-
-
-def _grad_out(grad, logits, rows, vocab):
-    """The gradient's tensor and row stride: allocated dense, or the caller's
-    [rows, >= vocab] tensor of the logits' type with contiguous rows."""
-    if grad is None:
-        return torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device), vocab
-    if grad.dtype != logits.dtype or grad.device != logits.device or grad.dim() != 2 or grad.shape[0] != rows or \
-            grad.shape[1] < vocab or (rows > 0 and grad.shape[1] > 1 and grad.stride(1) != 1):
-        raise ValueError(f"grad must be a {logits.dtype} [rows={rows}, >= {vocab}] tensor with contiguous rows on "
-                         f"{logits.device}")
-    stride = grad.stride(0) if rows > 1 else vocab
-    if stride < vocab:
-        raise ValueError("rows of grad overlap (stride(0) < vocab)")
-    return grad, stride
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _done(fn: str, result):
+    """The tensors of a call, or its status as an error."""
+    if result.__class__ is int:
+        _check(fn, result)
+    return result
 
 
 def logp_rows(logits: torch.Tensor, labels: torch.Tensor, weights: torch.Tensor | None = None,
@@ -626,39 +569,8 @@ def logp_rows(logits: torch.Tensor, labels: torch.Tensor, weights: torch.Tensor 
     temperature), f32 ``[rows]``; with ``entropy`` (True or a tensor) the pair
     ``(logp, entropy)`` from the same read. ``weights`` (f32 ``[rows]``): rows of
     weight 0 are not read and give 0."""
-    dtype, rows, vocab, stride = _objective_view(logits, vocab)
-    dev = logits.device
-    labels = _labels(labels, rows, dev)
-    w = _per_row(weights, rows, dev, "weights")
-    out = _f32(rows, dev) if out is None else _out(out, (rows,), torch.float32, dev, "out")
-    ent = _entropy_out(entropy, rows, dev)
-    _call("logp_rows", dev, logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), w, float(temperature),
-          out.data_ptr(), _ptr(ent))
-    return out if ent is None else (out, ent)
-
-
-def _policy(step, logits, labels, old_logp, advantages, scale, ref_logp, weights, clip_low, clip_high, kl_coef,
-            entropy_coef, temperature, vocab, entropy, grad):
-    dtype, rows, vocab, stride = _objective_view(logits, vocab)
-    dev = logits.device
-    labels = _labels(labels, rows, dev)
-    if old_logp is None or advantages is None:
-        raise ValueError("old_logp and advantages are needed")
-    old, adv = _per_row(old_logp, rows, dev, "old_logp"), _per_row(advantages, rows, dev, "advantages")
-    ref, w = _per_row(ref_logp, rows, dev, "ref_logp"), _per_row(weights, rows, dev, "weights")
-    if kl_coef != 0 and ref_logp is None:
-        raise ValueError("kl_coef needs ref_logp")
-    ent = _entropy_out(entropy, rows, dev)
-    loss_rows, logp, loss = _f32(rows, dev), _f32(rows, dev), _f32((), dev)
-    par = ctypes.byref(Policy(scale, temperature, clip_low, clip_high, kl_coef, entropy_coef))
-    if not step:
-        _call("policy_loss", dev, logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), old, adv, ref, w,
-              par, loss_rows.data_ptr(), logp.data_ptr(), _ptr(ent), loss.data_ptr())
-        return loss, loss_rows, logp, ent
-    grad, grad_stride = _grad_out(grad, logits, rows, vocab)
-    _call("policy_step", dev, logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), old, adv, ref, w, par,
-          grad.data_ptr(), grad_stride, loss_rows.data_ptr(), logp.data_ptr(), _ptr(ent), loss.data_ptr())
-    return grad, loss, loss_rows, logp, ent
+    got = _done("logp_rows", (_objectives or _bound()).logp_rows(logits, labels, weights, temperature, vocab, entropy, out))
+    return got[0] if entropy is False else got
 
 
 def policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor,
@@ -670,8 +582,9 @@ def policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch.Tens
     1 - d) - entropy_coef H`` with ``r = exp(logp - old_logp)``, ``d = ref_logp -
     logp``: returns ``(loss, loss_rows, logp, entropy)`` -- 0-d f32, f32
     ``[rows]`` each, entropy None unless asked for."""
-    return _policy(False, logits, labels, old_logp, advantages, scale, ref_logp, weights, clip_low, clip_high, kl_coef,
-                   entropy_coef, temperature, vocab, entropy, None)
+    return _done("policy_loss", (_objectives or _bound()).policy(
+        False, logits, labels, old_logp, advantages, scale, ref_logp, weights, clip_low, clip_high, kl_coef,
+        entropy_coef, temperature, vocab, entropy, None))
 
 
 def policy_step(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor,
@@ -684,36 +597,15 @@ def policy_step(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch.Tens
     ``grad`` may be the logits themselves (in place) or any ``[rows, >= vocab]``
     tensor with contiguous rows (columns past vocab are left alone); dense
     ``[rows, vocab]`` when not given."""
-    return _policy(True, logits, labels, old_logp, advantages, scale, ref_logp, weights, clip_low, clip_high, kl_coef,
-                   entropy_coef, temperature, vocab, entropy, grad)
+    return _done("policy_step", (_objectives or _bound()).policy(
+        True, logits, labels, old_logp, advantages, scale, ref_logp, weights, clip_low, clip_high, kl_coef,
+        entropy_coef, temperature, vocab, entropy, grad))
 
 
-def _preference(step, logits, labels, offsets, scale, ref_logp, weights, kind, beta, label_smoothing, margin, average,
-                temperature, vocab, grad):
-    dtype, rows, vocab, stride = _objective_view(logits, vocab)
-    dev = logits.device
-    labels = _labels(labels, rows, dev)
-    if offsets.dtype != torch.int64 or offsets.dim() != 1 or offsets.shape[0] % 2 != 1 or offsets.device != dev or \
-            not offsets.is_contiguous():
-        raise ValueError("offsets must be a contiguous int64 tensor [2 * pairs + 1] on the logits' device")
+def _kind(kind: str) -> int:
     if kind not in PREFERENCE_KINDS:
         raise ValueError(f"kind must be one of {sorted(PREFERENCE_KINDS)}")
-    pairs = offsets.shape[0] // 2
-    ref, w = _per_row(ref_logp, 2 * pairs, dev, "ref_logp"), _per_row(weights, rows, dev, "weights")
-    logp, seq_logp, loss_pairs, loss = _f32(rows, dev), _f32(2 * pairs, dev), _f32(pairs, dev), _f32((), dev)
-    work = _f32(4 * (rows + 1) if step else 4, dev)
-    par = ctypes.byref(Preference(scale, temperature, beta, label_smoothing, margin, PREFERENCE_KINDS[kind],
-                                  1 if average else 0))
-    if not step:
-        _call("preference_loss", dev, logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), w,
-              offsets.data_ptr(), pairs, ref, par, logp.data_ptr(), seq_logp.data_ptr(), loss_pairs.data_ptr(),
-              loss.data_ptr(), work.data_ptr())
-        return loss, loss_pairs, seq_logp, logp
-    grad, grad_stride = _grad_out(grad, logits, rows, vocab)
-    _call("preference_step", dev, logits.data_ptr(), dtype, rows, vocab, stride, labels.data_ptr(), w,
-          offsets.data_ptr(), pairs, ref, par, grad.data_ptr(), grad_stride, logp.data_ptr(), seq_logp.data_ptr(),
-          loss_pairs.data_ptr(), loss.data_ptr(), work.data_ptr())
-    return grad, loss, loss_pairs, seq_logp, logp
+    return PREFERENCE_KINDS[kind]
 
 
 def preference_loss(logits: torch.Tensor, labels: torch.Tensor, offsets: torch.Tensor, scale: float,
@@ -726,8 +618,9 @@ def preference_loss(logits: torch.Tensor, labels: torch.Tensor, offsets: torch.T
     on the device). ``ref_logp`` f32 ``[2 * pairs]``: the reference model's
     sequence log-probabilities (``seq_logp`` of its logits). Returns ``(loss,
     loss_pairs, seq_logp, logp)``: 0-d, ``[pairs]``, ``[2 * pairs]``, ``[rows]``."""
-    return _preference(False, logits, labels, offsets, scale, ref_logp, weights, kind, beta, label_smoothing, margin,
-                       average, temperature, vocab, None)
+    return _done("preference_loss", (_objectives or _bound()).preference(
+        False, logits, labels, offsets, scale, ref_logp, weights, _kind(kind), beta, label_smoothing, margin, average,
+        temperature, vocab, None))
 
 
 def preference_step(logits: torch.Tensor, labels: torch.Tensor, offsets: torch.Tensor, scale: float,
@@ -738,8 +631,9 @@ def preference_step(logits: torch.Tensor, labels: torch.Tensor, offsets: torch.T
     """``preference_loss`` and its gradient with respect to the logits, in their
     type: returns ``(grad, loss, loss_pairs, seq_logp, logp)``. ``grad`` as in
     ``policy_step``."""
-    return _preference(True, logits, labels, offsets, scale, ref_logp, weights, kind, beta, label_smoothing, margin,
-                       average, temperature, vocab, grad)
+    return _done("preference_step", (_objectives or _bound()).preference(
+        True, logits, labels, offsets, scale, ref_logp, weights, _kind(kind), beta, label_smoothing, margin, average,
+        temperature, vocab, grad))
 
 
 # -- diagnostics and tuning ---------------------------------------------------
