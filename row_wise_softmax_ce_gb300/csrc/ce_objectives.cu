@@ -49,7 +49,8 @@ __device__ __forceinline__ bool in_range(int64_t label, int vocab) { return labe
 // k_obj_rows: one CTA per row (looping), or few rows over clusters of C CTAs,
 // exactly one row each: every warp scans its part of a contiguous slice of `cols`
 // columns and pushes its state into CTA 0's shared memory, whose first warp
-// merges them and writes the row.
+// merges them and writes the row. HBM-bound: 7168 rows of 128256 bf16 with
+// entropies 256-260 us, 7.1 TB/s; 3072 of 50257 f32 91 us, 6.8 TB/s.
 struct RowsXchg {
     float4 slot[kMaxCluster * (kScanThreads / 32)];
     uint64_t bar;
@@ -182,7 +183,8 @@ __global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows(ObjArgs a, int col
 }
 
 // k_obj_rows_warp: the same for many short rows, a warp per row: no barrier, no
-// exchange, four rows per CTA.
+// exchange, four rows per CTA. Bound by a row's latencies over the warps
+// resident: 8192 x 2000 f16 policy losses 14.5 us (a CTA per row 31.0).
 template <typename T, int kMode, bool kEnt>
 __global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows_warp(ObjArgs a) {
     launch_dependents();
@@ -376,10 +378,14 @@ __global__ void __launch_bounds__(kRowsThreads, 4) k_policy_stream(ObjArgs a, in
 // buf holds column c0 - off + i, off = the slice's start modulo 16 bytes. Its
 // aligned body arrives by one bulk copy; the at most two partial end vectors
 // are loaded by the threads that own them, with -inf outside the slice. Per
-// row: one sweep for (m, s, u); the states of the cluster's CTAs meet by
-// pushes; every CTA forms the row's factors from the same bits; the gradient
+// row: one sweep for (m, s, u); the states of the cluster's warps meet by
+// pushes; every warp forms the row's factors from the same bits; the gradient
 // is written from shared memory; then the copy of the next row that counts
-// starts, its latency hidden behind the SM's other CTAs.
+// starts (rows past the grid), its latency hidden behind the SM's other CTAs.
+// HBM-bound: 8192 x 50257 bf16 245 us with the loss's sum, 6.7 TB/s of logits
+// and gradient; 4096 x 128256 f32 with an entropy bonus 606 us, 6.9 TB/s. A
+// reduction over each CTA before the exchange, and one warp forming the
+// factors: 256 and 624 us.
 struct alignas(16) PolicyHeader {
     WarpXchg<kStagedThreads / 32> xg;
     uint64_t bar;
@@ -575,7 +581,9 @@ __global__ void __launch_bounds__(kStagedThreads, 8) k_policy_staged(ObjArgs a, 
 // ---------------------------------------------------------------------------
 // k_policy_warp: the policy's loss and gradient of short rows, a warp per row
 // that it holds in registers (at most kV vectors per lane, and a partial vector
-// at either end by single elements).
+// at either end by single elements). Bound by a row's own latencies (weight and
+// label, logits, x[label], the gradient's stores) over the warps resident: 8192
+// x 2000 bf16 18.6 us, 3.5 TB/s; a staged CTA per row 36.7 us.
 template <typename T, bool kEnt, int kV>
 __global__ void __launch_bounds__(kScanThreads, kV > 8 ? 3 : kV > 4 ? 6 : 8) k_policy_warp(ObjArgs a) {
     constexpr int N = Vec<T>::kN;
@@ -665,9 +673,10 @@ __global__ void __launch_bounds__(kScanThreads, kV > 8 ? 3 : kV > 4 ? 6 : 8) k_p
 // ---------------------------------------------------------------------------
 // k_join: one CTA per pair (looping). Half of its threads sum the chosen
 // sequence's w logp (and w, for averages), half the rejected's, each in a fixed
-// order; one thread forms the pair's loss and the factors
-// dloss / dlogp of the two sequences' rows. The CTA that finishes last adds
-// the pairs' losses up, again in a fixed order.
+// order; one thread forms the pair's loss and the factors dloss / dlogp of the
+// two sequences' rows. The CTA that finishes last adds the pairs' losses up,
+// again in a fixed order. A chain of latencies, about 5 us behind the rows (f64
+// sums and butterflies: 7 us): 24 pairs of 6001 rows.
 constexpr int kJoinThreads = 256;
 
 // A sum over rows as an unevaluated pair hi + lo of f32: hi the rounded sum,
@@ -811,7 +820,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(JoinArgs j) {
 // ---------------------------------------------------------------------------
 // k_pair_grad: factor ([y] - p) of every row, a CTA per part of kPartBytes of
 // a row. Rows whose factor is 0 (no weight, or in no sequence) are written as
-// zeros without being read.
+// zeros without being read. HBM-bound: 1400 rows of 128256 bf16, 3/4 of them
+// read, 92 us, 6.8 TB/s. 3000 rows' whole step with 256 threads x 4 vectors in
+// flight 293 us, x 1 297, 128 x 4 296, parts of 64 KB 297.
 constexpr int kPartBytes = 32768;
 constexpr int kPairThreads = 256;
 constexpr int kPairUnroll = 4;
@@ -842,7 +853,8 @@ __global__ void __launch_bounds__(kPairThreads) k_pair_grad(ObjArgs a, int parts
 // programmatic dependent of the row kernel. Thread g of all sums rows g, g +
 // all, ... as f32 pairs; a butterfly over each warp, then over the CTA's warps;
 // a cluster's CTAs meet in CTA 0's shared memory. A fixed shape for a number
-// of rows: the same bits every run.
+// of rows: the same bits every run. About 2.5 us behind the row kernel (a
+// cluster of f64 butterflies: 4.5 us).
 constexpr int kSumCtas = 8;
 constexpr int kSumThreads = 512;
 constexpr int64_t kSumOneCta = 8192;  // rows up to here: one CTA
@@ -1009,8 +1021,9 @@ bool forward_warp(DType t, int64_t rows, int64_t vocab, const DeviceInfo &dev) {
 }
 
 // Rows a warp holds in its registers. Measured (us, policy steps, warp against
-// staged CTA): 8192 rows of 1000 bf16 12.4, 32.9, of 2000 19.2, 36.0, of 4000
-// 31.1, 43.7, of 2000 f32 27.1, 40.6; 300 rows of 2000 bf16 6.2, 8.2.
+// staged CTA): 8192 rows of 1000 bf16 12.4, 33.1, of 2000 18.6, 36.7, of 4000
+// 31.0, 44.3, of 2000 f32 28.4, 41.0; 300 rows of 2000 bf16 6.3, 8.2. In 250
+// registers, rows of 9 / 12 / 16 KB: 41.1, 43.4 / 45.4, 48.5 / 60.6, 55.8.
 constexpr int64_t kWarpStepBytes = 8192;
 
 // Every row kernel loops over rows, so fewer clusters (or CTAs of a warp per
@@ -1071,14 +1084,15 @@ static int64_t staged_smem(DType t, int cols) {
 
 // CTAs per row of the staged kernel; 0: the row does not fit a cluster. What
 // hides a row's latencies (copy, exchange, write) is the bytes an SM holds, so
-// the split that holds most of them, in at most six CTAs. Measured (us, 128
-// threads per CTA, CTAs per row: time; CTAs per SM x KB): 4096 x 128256 f32
-// 8: 766; 3 x 64, 10: 651; 4 x 51, 11: 707; 4 x 47, 12: 626; 5 x 43; 8192 x
-// 50257 bf16 2: 256.0; 4 x 50, 3: 256.6; 6 x 34, 4: 276; 8 x 25; 4096 x 32000
-// bf16 1: 80.3; 3 x 64, 2: 77.9; 6 x 32, 3: 86.6; 8 x 21. 256 threads: 640 at
-// 10, 259 at 2, 79.9 at 1. Clusters persistent over rows, each row's copy
-// issued behind the last one's write: 651 -> 675 at 10 CTAs, 256 -> 276 at 2,
-// 78 -> 91 at 2 -- the hardware's own scheduling balances better.
+// the split that holds most of them, in at most six CTAs. Measured (us, CTAs
+// per row: time; CTAs per SM x KB): 4096 x 128256 f32 8: 674; 3 x 64, 9: 724;
+// 3 x 57, 10: 613; 4 x 51, 11: 638; 4 x 47, 12: 606; 5 x 43, 14: 660; 5 x 37;
+// 8192 x 50257 bf16 1: 273; 2 x 98, 2: 246.2; 4 x 50, 3: 246.3; 6 x 34, 4: 257;
+// 8 x 25; 4096 x 32000 bf16 1: 75.8; 3 x 64, 2: 74.7; 6 x 32, 3: 82.0; 8 x 21.
+// (Before the warps exchanged their states: 256 threads per CTA 640 at 10, 259
+// at 2, 79.9 at 1 against 626, 256, 78; clusters persistent over rows, each
+// row's copy issued behind the last one's write, 651 -> 675 at 10, 256 -> 276 at
+// 2, 78 -> 91 at 2: the hardware's own scheduling balances better.)
 // With few rows a row is split further, like a forward row.
 static int staged_split(DType t, int64_t rows, int64_t vocab, const DeviceInfo &dev) {
     constexpr int64_t kPerSm = 228 * 1024, kReserved = 1024;
