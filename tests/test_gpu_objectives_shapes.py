@@ -286,3 +286,77 @@ def test_drawn(seed):
     a_case(rows, vocab, vocab + rng.choice([0, 0, 1, 7, 64]), dtype, rng.choice([0, 0, 1, 4, 7]), rng.choice([0.0, 0.3, 0.9]),
            rng.choice([1.0, 0.5, 1.7]), rng.choice([0.0, 0.2]), rng.choice([0.0, 0.03]), seed, rng.choice([1, 2, 9]),
            rng.choice([0, 0, 1, 3]), rng.choice([0, 0, 2, 5]), rng.choice(["sigmoid", "squared"]))
+
+
+def c_output(n, dtype=torch.float32):
+    """n elements between sentinels, and a check that the sentinels are whole."""
+    buf = torch.full((n + 96,), SENTINEL, dtype=dtype, device=DEV)
+
+    def whole():
+        return bool((buf[:48] == SENTINEL).all()) and bool((buf[48 + n:] == SENTINEL).all())
+    return buf[48:48 + n], whole
+
+
+@pytest.mark.parametrize("rows,vocab", [(1, 5), (37, 900), (130, 9000), (5, 100003)])
+def test_c_calls_write_their_outputs_only(rows, vocab):
+    """The C ABI: every output between sentinels, the work buffer of a preference
+    call used by two calls in a row, a reference that is not wanted never read."""
+    import ctypes
+    L, par = ce.lib(), ce.Policy(1.0, 1.0, 0.2, 0.2, 0.0, 0.01)
+    x, g = logits_at(rows, vocab, vocab, torch.bfloat16, seed=rows)
+    y, w, old, ref, adv = inputs(rows, vocab, g, x, 0.3)
+    bad_ref = torch.full((rows,), math.nan, device=DEV)
+    s = torch.cuda.current_stream().cuda_stream
+    outs = [c_output(rows) for _ in range(3)] + [c_output(1)]
+    grad = c_output(rows * vocab, torch.bfloat16)
+    (loss_rows, _), (logp, _), (ent, _), (loss, _) = outs
+    st = L.policy_step(x.data_ptr(), 1, rows, vocab, vocab, y.data_ptr(), old.data_ptr(), adv.data_ptr(),
+                       bad_ref.data_ptr(), w.data_ptr(), ctypes.byref(par), grad[0].data_ptr(), vocab,
+                       loss_rows.data_ptr(), logp.data_ptr(), ent.data_ptr(), loss.data_ptr(), s)
+    assert st == ce.CE_OK and all(whole() for _, whole in outs + [grad])
+    want = R.policy64(x, y, old, adv, 1.0, weights=w, entropy_coef=0.01)
+    check({"loss": loss[0], "loss_rows": loss_rows, "logp": logp, "entropy": ent, "grad": grad[0].view(rows, vocab)}, want,
+          "policy_step")
+    st = L.policy_loss(x.data_ptr(), 1, rows, vocab, vocab, y.data_ptr(), old.data_ptr(), adv.data_ptr(), None,
+                       w.data_ptr(), ctypes.byref(par), loss_rows.data_ptr(), logp.data_ptr(), None, loss.data_ptr(), s)
+    assert st == ce.CE_OK and all(whole() for _, whole in outs)
+    check({"loss": loss[0], "loss_rows": loss_rows, "logp": logp}, want, "policy_loss")
+    assert L.logp_rows(x.data_ptr(), 1, rows, vocab, vocab, y.data_ptr(), w.data_ptr(), 1.0, logp.data_ptr(),
+                       ent.data_ptr(), s) == ce.CE_OK
+    assert all(whole() for _, whole in outs)
+    check({"logp": logp, "entropy": ent}, want, "logp_rows")
+
+    ends = [0, rows // 3, rows // 2, rows // 2, rows]
+    offs, pp = torch.tensor(ends, device=DEV), ce.Preference(0.5, 1.0, 0.2, 0.0, 0.1, 0, 0)
+    seq, pairs, work = c_output(4), c_output(2), c_output(4 * (rows + 1))
+    for _ in range(2):
+        st = L.preference_step(x.data_ptr(), 1, rows, vocab, vocab, y.data_ptr(), w.data_ptr(), offs.data_ptr(), 2, None,
+                               ctypes.byref(pp), grad[0].data_ptr(), vocab, logp.data_ptr(), seq[0].data_ptr(),
+                               pairs[0].data_ptr(), loss.data_ptr(), work[0].data_ptr(), s)
+        assert st == ce.CE_OK and all(whole() for _, whole in outs + [grad, seq, pairs, work])
+        want = R.preference64(x, y, ends, 0.5, weights=w, beta=0.2, margin=0.1)
+        check({"loss": loss[0], "loss_pairs": pairs[0], "seq_logp": seq[0], "logp": logp,
+               "grad": grad[0].view(rows, vocab)}, want, "preference_step")
+        loss.fill_(SENTINEL)
+    small = c_output(4)
+    st = L.preference_loss(x.data_ptr(), 1, rows, vocab, vocab, y.data_ptr(), w.data_ptr(), offs.data_ptr(), 2, None,
+                           ctypes.byref(pp), logp.data_ptr(), seq[0].data_ptr(), pairs[0].data_ptr(), loss.data_ptr(),
+                           small[0].data_ptr(), s)
+    assert st == ce.CE_OK and all(whole() for _, whole in outs + [seq, pairs, small])
+    check({"loss": loss[0], "loss_pairs": pairs[0], "seq_logp": seq[0], "logp": logp}, want, "preference_loss")
+
+
+@pytest.mark.parametrize("which", ["old_logp", "advantages", "ref_logp"])
+def test_numbers_that_are_not(which):
+    """A NaN among a row's numbers makes that row NaN, and no other."""
+    rows, vocab = 9, 300
+    x, g = logits_at(rows, vocab, vocab, torch.float32, seed=2)
+    y, w, old, ref, adv = inputs(rows, vocab, g, x, 0.0)
+    kw = {"old_logp": old, "advantages": adv, "ref_logp": ref}
+    kw[which] = kw[which].clone()
+    kw[which][4] = math.nan
+    grad, loss, rows_, logp, _ = ce.policy_step(x, y, scale=1.0, kl_coef=0.1, **kw)
+    want = R.policy64(x, y, kw["old_logp"], kw["advantages"], 1.0, ref=kw["ref_logp"], kl_coef=0.1)
+    check({"grad": grad, "loss": loss, "loss_rows": rows_, "logp": logp}, want, which)
+    assert math.isnan(rows_[4]) and bool(torch.isnan(grad[4]).all()) and not math.isnan(logp[4])
+    assert int(torch.isnan(rows_).sum()) == 1
