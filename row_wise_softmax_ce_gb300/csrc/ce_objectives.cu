@@ -898,6 +898,9 @@ __global__ void __launch_bounds__(kSumThreads) k_weighted_sum(const float *__res
 // ---------------------------------------------------------------------------
 // launchers
 
+// cluster 0: a launch without cluster dimensions, for kernels that execute no
+// instruction on shared::cluster addresses (st.async is illegal there, to the
+// CTA's own shared memory too).
 struct LaunchConfig {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
