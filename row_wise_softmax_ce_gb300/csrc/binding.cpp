@@ -12,7 +12,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -137,7 +137,12 @@ struct WithoutGil {
     ~WithoutGil() { PyEval_RestoreThread(state); }
 };
 
-at::Tensor f32(const Logits &x, at::IntArrayRef sizes) { return at::empty(sizes, x.t.options().dtype(at::kFloat)); }
+// Uninitialised device memory from PyTorch's allocator, without the dispatcher
+// (four to six outputs a call).
+at::Tensor empty(const Logits &x, at::IntArrayRef sizes, at::ScalarType type) {
+    return at::detail::empty_cuda(sizes, type, x.t.device(), std::nullopt);
+}
+at::Tensor f32(const Logits &x, at::IntArrayRef sizes) { return empty(x, sizes, at::kFloat); }
 float *data(const at::Tensor &t) { return t.defined() ? static_cast<float *>(t.data_ptr()) : nullptr; }
 ce_stream_t stream_of(const Logits &x) {
     return reinterpret_cast<ce_stream_t>(c10::cuda::getCurrentCUDAStream(x.t.device().index()).stream());
@@ -205,7 +210,7 @@ PyObject *policy(PyObject *const *a) {
         lp = f32(x, {x.rows});
         loss = f32(x, {});
         if (step) {
-            if (!grad.defined()) grad = at::empty({x.rows, x.vocab}, x.t.options());
+            if (!grad.defined()) grad = empty(x, {x.rows, x.vocab}, x.t.scalar_type());
             st = policy_step(x.t.data_ptr(), x.dtype, x.rows, x.vocab, x.stride, labels, old, adv, ref, w, &par,
                              grad.data_ptr(), grad_stride, data(rows), data(lp), data(ent.t), data(loss), stream_of(x));
         } else {
@@ -247,7 +252,7 @@ PyObject *preference(PyObject *const *a) {
         loss = f32(x, {});
         work = f32(x, {4 * (step ? x.rows + 1 : 1)});
         if (step) {
-            if (!grad.defined()) grad = at::empty({x.rows, x.vocab}, x.t.options());
+            if (!grad.defined()) grad = empty(x, {x.rows, x.vocab}, x.t.scalar_type());
             st = preference_step(x.t.data_ptr(), x.dtype, x.rows, x.vocab, x.stride, labels, w,
                                  offsets.const_data_ptr<int64_t>(), pairs, ref, &par, grad.data_ptr(), grad_stride,
                                  data(lp), data(seq), data(pair_losses), data(loss), work.data_ptr(), stream_of(x));
