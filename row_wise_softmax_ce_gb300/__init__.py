@@ -570,7 +570,7 @@ def logp_rows(logits: torch.Tensor, labels: torch.Tensor, weights: torch.Tensor 
     ``(logp, entropy)`` from the same read. ``weights`` (f32 ``[rows]``): rows of
     weight 0 are not read and give 0."""
     got = _done("logp_rows", (_objectives or _bound()).logp_rows(logits, labels, weights, temperature, vocab, entropy, out))
-    return got[0] if entropy is False else got
+    return got if got[1] is not None else got[0]
 
 
 def policy_loss(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor,

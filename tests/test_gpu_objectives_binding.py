@@ -175,3 +175,10 @@ def test_leaves_that_require_grad():
     grad = ce.policy_step(leaf.detach(), y, f, f + 1, 1.0)[0]
     leaf.grad = grad
     assert leaf.grad is grad
+
+
+def test_entropy_not_wanted():
+    """False and None alike: the log-probabilities alone."""
+    x, y, f, _ = batch()
+    assert torch.equal(ce.logp_rows(x, y, entropy=None), ce.logp_rows(x, y))
+    assert ce.policy_loss(x, y, f, f, 1.0, entropy=None)[3] is None
