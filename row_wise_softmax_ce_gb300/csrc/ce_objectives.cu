@@ -3,7 +3,7 @@
 //
 //   logp_rows        logp = (x_y - m) / T - log s, H = log s - u / (T s)
 //   policy_loss      + the clipped loss of exp(logp - old), the KL term, the
-//   policy_step        entropy bonus; its gradient e (a + b (x - m)) + [y] c
+//   policy_step        entropy bonus; its gradient e (a + b log2 e) + [label] c
 //   preference_loss  rows -> sequences -> pairs -> loss; the gradient of a
 //   preference_step    row is its pair's factor times ([y] - p)
 //

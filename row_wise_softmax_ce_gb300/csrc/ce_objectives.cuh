@@ -137,7 +137,8 @@ struct TokState {
 __device__ __forceinline__ TokState tok_empty() { return TokState{-INFINITY, 0.0f, 0.0f}; }
 
 // d = x - m is taken times a weight of 0 where x is -inf (or far below): keep
-// it finite there. A NaN d keeps its NaN weight.
+// it finite there. A NaN d keeps its NaN weight. For a row's sums, which no
+// large factor multiplies here; gradient_exponent is the gradient's.
 __device__ __forceinline__ float finite_below(float d) { return fmaxf(d, -1.0e30f); }
 
 // move the state to a max m1 >= s.m (m1 above -inf)
@@ -366,7 +367,7 @@ __device__ __forceinline__ TokState tok_scan(const T *__restrict__ p, int n, flo
 // What a row's state, its label's logit and its own numbers come to.
 struct TokRow {
     float logp, entropy, loss;
-    // gradient: e (a + b (x - m)) + [label] c, e = 2^((x - m) k)
+    // gradient: e (a + b y) + [label] c, y = (x - m) k, e = 2^y
     float m, a, b, c;
 };
 
@@ -410,12 +411,19 @@ __device__ __forceinline__ TokRow policy_row(const ObjArgs &a, const TokState &g
     if (kEnt) {
         r.loss -= a.bonus * r.entropy;
         r.a += a.bonus * (r.entropy - log_s) * rcp * f;
-        r.b = a.bonus * a.inv_t * rcp * f;
+        r.b = a.bonus * 0.69314718f * rcp * f;  // y ln 2 = (x - m) / T
     }
     return r;
 }
 
-// e (a + b d) over one vector, rounded once to T
+// The exponent as the gradient's entropy term takes it: held at -128, where
+// 2^y is 0 already, so that a masked column is 0 times a finite number. b y is
+// then of a's own order whatever the temperature and the scale; with x - m in
+// place of y, b would hold another 1 / T and -inf or the lowest value times it
+// overflow.
+__device__ __forceinline__ float gradient_exponent(float y) { return fmaxf(y, -128.0f); }
+
+// e (a + b y) over one vector, rounded once to T
 template <typename T, bool kB>
 __device__ __forceinline__ uint4 tok_grad_vec(const uint4 &v, float m, float k, float a, float b) {
     const float2 nm = make_float2(-m, -m), kk = make_float2(k, k), aa = make_float2(a, a), bb = make_float2(b, b);
@@ -425,7 +433,7 @@ __device__ __forceinline__ uint4 tok_grad_vec(const uint4 &v, float m, float k, 
         const float2 d = __fadd2_rn(Vec<T>::pair(v, i), nm);
         const float2 y = __fmul2_rn(d, kk);
         const float2 e = make_float2(ex2_ftz(y.x), ex2_ftz(y.y));
-        const float2 c = kB ? __ffma2_rn(make_float2(finite_below(d.x), finite_below(d.y)), bb, aa) : aa;
+        const float2 c = kB ? __ffma2_rn(make_float2(gradient_exponent(y.x), gradient_exponent(y.y)), bb, aa) : aa;
         Vec<T>::set_pair(o, i, __fmul2_rn(e, c));
     }
     return o;
@@ -435,13 +443,13 @@ __device__ __forceinline__ uint4 tok_grad_vec(const uint4 &v, float m, float k, 
 // term c added in the product's own rounding
 template <bool kB>
 __device__ __forceinline__ float tok_grad1(float x, float m, float k, float a, float b) {
-    const float d = x - m;
-    return __fmul_rn(ex2_ftz(__fmul_rn(d, k)), kB ? __fmaf_rn(finite_below(d), b, a) : a);
+    const float y = __fmul_rn(x - m, k);
+    return __fmul_rn(ex2_ftz(y), kB ? __fmaf_rn(gradient_exponent(y), b, a) : a);
 }
 template <bool kB>
 __device__ __forceinline__ float tok_label1(float x, float m, float k, float a, float b, float c) {
-    const float d = x - m;
-    return __fmaf_rn(ex2_ftz(__fmul_rn(d, k)), kB ? __fmaf_rn(finite_below(d), b, a) : a, c);
+    const float y = __fmul_rn(x - m, k);
+    return __fmaf_rn(ex2_ftz(y), kB ? __fmaf_rn(gradient_exponent(y), b, a) : a, c);
 }
 
 }  // namespace cerows

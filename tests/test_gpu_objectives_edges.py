@@ -1,0 +1,67 @@
+"""The objectives where their constants are far from 1 and their tensors are
+used again: temperatures and scales over the accepted range, beside masked
+columns. Against the 64-bit definition (tests/objectives_ref.py)."""
+import math
+
+import pytest
+import torch
+
+import objectives_ref as R
+import row_wise_softmax_ce_gb300 as ce
+from test_gpu_objectives import DEV, TYPES, check, ids, logits_at
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    torch.cuda.set_device(0)
+    ce.device_error_reset()
+    yield
+    assert ce.device_error_count() == (0, 0)
+
+
+def wider(want, scale, T, adv, bonus):
+    """The gradient's bound with what a flushed probability is worth: p below
+    2^-126 counts as 0, which leaves out at most scale / T p (|g| + |bonus|
+    |log p + H|) of a column, |g| <= 2 |A| here (the ratio is 1) and |log p + H|
+    <= 88 + log 2^24 < 110 at the largest such p (p |log p| falls below it)."""
+    value, bound = want["grad"]
+    lost = 2.0 ** -126 * abs(scale) / T * (2 * adv.double().abs() + abs(bonus) * 110)
+    return dict(want, grad=(value, bound + lost[:, None]))
+
+
+# a warp per row, rows staged in shared memory, rows read twice
+VOCABS = {torch.float32: (1000, 33001, (1 << 20) + 3), torch.bfloat16: (1000, 33001, (1 << 21) + 3),
+          torch.float16: (1000, 33001, (1 << 21) + 3)}
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("kernel", range(3), ids=["warp", "staged", "stream"])
+@pytest.mark.parametrize("T", [1e-6, 1e-3, 1e3, 1e6])
+def test_masked_columns_at_far_temperatures(dtype, kernel, T):
+    """Columns of -inf have a gradient of 0 whatever the temperature, the scale
+    and the entropy bonus; columns of the lowest value have the formula's."""
+    rows, vocab = 4, VOCABS[dtype][kernel]
+    x, g = logits_at(rows, vocab, vocab + 1, dtype, seed=vocab)
+    ban = torch.rand(vocab, generator=g, device=DEV) < 0.5
+    ban[vocab // 2] = False
+    x[0, ban] = -math.inf
+    x[1, ban] = torch.finfo(dtype).min
+    x[2, : vocab // 2] = -math.inf
+    x[2, vocab // 2 + 1:] = torch.finfo(dtype).min
+    y = x.float().argmax(1)
+    adv = torch.tensor([1.0, -0.5, 2.0, 0.25], device=DEV)
+    old = R.logp64(x, y, temperature=T)["logp"][0].float()
+    # f16 gradients end at 65504: scales whose factor scale / T stays below
+    scales = (T, 3e4 * T) if dtype == torch.float16 else (T, 1.0, 65536.0)
+    for scale in scales:
+        for bonus in (0.0, 0.01, 1.0):
+            what = f"{vocab} T={T} scale={scale} bonus={bonus}"
+            want = wider(R.policy64(x, y, old, adv, scale, entropy_coef=bonus, temperature=T), scale, T, adv, bonus)
+            for entropy in (False, True):
+                got = ce.policy_step(x, y, old, adv, scale, entropy_coef=bonus, temperature=T, entropy=entropy)
+                check(dict(zip(("grad", "loss", "loss_rows", "logp", "entropy"), got)), want, what)
+                assert not got[0][x == -math.inf].any(), what
