@@ -367,13 +367,14 @@ __device__ __forceinline__ TokState tok_scan(const T *__restrict__ p, int n, flo
 // What a row's state, its label's logit and its own numbers come to.
 struct TokRow {
     float logp, entropy, loss;
+    float mean;  // sum of p_j (x_j - m) / T = log s - H, <= 0 (entropies only)
     // gradient: e (a + b y) + [label] c, y = (x - m) k, e = 2^y
     float m, a, b, c;
 };
 
 __device__ __forceinline__ float nan_f() { return __int_as_float(0x7fffffff); }
 
-// logp = (x_y - m) / T - log s; H = log s - u / (T s). NaN for a bad label and
+// logp = (x_y - m) / T - log s; H = log s - mean, mean = u / (T s). NaN for a bad label and
 // for a row that holds a NaN or +inf, or nothing above -inf.
 template <bool kEnt>
 __device__ __forceinline__ TokRow tok_row(const TokState &g, float xl, bool lab_ok, float inv_t, float *log_s) {
@@ -382,7 +383,10 @@ __device__ __forceinline__ TokRow tok_row(const TokState &g, float xl, bool lab_
     *log_s = logf(g.s);
     r.m = g.m;
     r.logp = bad || !lab_ok ? nan_f() : (xl - g.m) * inv_t - *log_s;
-    if (kEnt) r.entropy = bad ? nan_f() : *log_s - g.u * inv_t / g.s;
+    if (kEnt) {
+        r.mean = g.u * inv_t / g.s;
+        r.entropy = bad ? nan_f() : *log_s - r.mean;
+    }
     return r;
 }
 
@@ -410,7 +414,10 @@ __device__ __forceinline__ TokRow policy_row(const ObjArgs &a, const TokState &g
     r.a = -d * rcp * f;
     if (kEnt) {
         r.loss -= a.bonus * r.entropy;
-        r.a += a.bonus * (r.entropy - log_s) * rcp * f;
+        // log p_j + H = (x_j - m) / T - mean. Not entropy - log s for -mean: that
+        // returns it with the entropy's rounding, of the size of the whole
+        // difference where a row is nearly flat
+        r.a -= a.bonus * r.mean * rcp * f;
         r.b = a.bonus * 0.69314718f * rcp * f;  // y ln 2 = (x - m) / T
     }
     return r;

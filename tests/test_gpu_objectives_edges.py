@@ -65,3 +65,38 @@ def test_masked_columns_at_far_temperatures(dtype, kernel, T):
                 got = ce.policy_step(x, y, old, adv, scale, entropy_coef=bonus, temperature=T, entropy=entropy)
                 check(dict(zip(("grad", "loss", "loss_rows", "logp", "entropy"), got)), want, what)
                 assert not got[0][x == -math.inf].any(), what
+
+
+def bonus64(x, f, bonus, T):
+    """f bonus p_j (log p_j + H) in 64 bits, and its bound. With D = (m - x_j) /
+    T, log p_j + H = -D - mean, mean = sum of p (x - m) / T:
+      p     its relative error, as in objectives_ref.grad64: err_s + (3 D + 8) U
+      D     3 U of the exponent, 5 U of the factor and the product
+      mean  sum of e D over s: terms of one sign, so err_s for the sum, err_s for
+            s, 8 U for the terms, the quotient and the factor
+    -- no error of the size of the entropy's own rounding (U log V)."""
+    z = x.double() / T
+    D = z.amax(1, keepdim=True) - z
+    e = (-D).exp()
+    p = e / e.sum(1, keepdim=True)
+    mean = -(p * D).sum(1, keepdim=True)
+    value = abs(f) * bonus * p * (-D - mean)
+    err_s = (6 + R.depth(x.shape[1])) * R.U
+    rel_p = err_s + (3 * D + 8) * R.U
+    bound = abs(f) * bonus * p * (D * (rel_p + 8 * R.U) + mean.abs() * (rel_p + 2 * err_s + 8 * R.U))
+    return value, bound + value.abs() * (R.HALF_STEP[x.dtype] + 4 * R.U) + R.LEAST[x.dtype]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("kernel", range(3), ids=["warp", "staged", "stream"])
+@pytest.mark.parametrize("T", [1.0, 1e3, 1e5, 1e6])
+def test_entropy_gradient_of_flat_rows(dtype, kernel, T):
+    """The entropy bonus alone (no advantage): its gradient is as accurate on a
+    row that the temperature makes nearly flat as anywhere."""
+    rows, vocab = 4, VOCABS[dtype][kernel]
+    x, g = logits_at(rows, vocab, vocab, dtype, seed=vocab + 1)
+    y = torch.randint(0, vocab, (rows,), generator=g, device=DEV)
+    old = R.logp64(x, y, temperature=T)["logp"][0].float()
+    scale = T * T * vocab  # columns of order x - m, in range of f16
+    grad = ce.policy_step(x, y, old, torch.zeros(rows, device=DEV), scale, entropy_coef=1.0, temperature=T)[0]
+    R.assert_near(grad, bonus64(x, scale / T, 1.0, T), f"{vocab} T={T}")
