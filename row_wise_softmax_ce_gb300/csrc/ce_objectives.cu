@@ -859,9 +859,11 @@ constexpr int kSumCtas = 8;
 constexpr int kSumThreads = 512;
 constexpr int64_t kSumOneCta = 8192;  // rows up to here: one CTA
 
-__global__ void __launch_bounds__(kSumThreads) k_weighted_sum(const float *__restrict__ loss,
-                                                              const float *__restrict__ weights, int64_t rows,
-                                                              double scale, float *__restrict__ out) {
+// `loss` is written by the grid that this one overlaps until wait_prerequisites:
+// not read-only for this kernel's whole life, so neither __restrict__ nor a
+// non-coherent load, and read behind the wait only.
+__global__ void __launch_bounds__(kSumThreads) k_weighted_sum(const float *loss, const float *__restrict__ weights,
+                                                              int64_t rows, double scale, float *out) {
     __shared__ Sum2 warp_part[kSumThreads / 32];
     __shared__ double cta_part[kSumCtas];
     const uint32_t rank = cluster_rank(), C = cluster_size();

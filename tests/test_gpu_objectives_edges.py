@@ -100,3 +100,34 @@ def test_entropy_gradient_of_flat_rows(dtype, kernel, T):
     scale = T * T * vocab  # columns of order x - m, in range of f16
     grad = ce.policy_step(x, y, old, torch.zeros(rows, device=DEV), scale, entropy_coef=1.0, temperature=T)[0]
     R.assert_near(grad, bonus64(x, scale / T, 1.0, T), f"{vocab} T={T}")
+
+
+@pytest.mark.parametrize("rows", [1, 300, 8192, 8193, 40000])
+def test_sum_of_the_pass_before_it(rows):
+    """The C call over and over into the same buffers, the losses changing sign
+    and size from pass to pass, nothing between the passes: each loss is the sum
+    of its own pass's row losses, over one CTA's rows and a cluster's."""
+    import ctypes
+    vocab, passes = 40, 60
+    L, par = ce.lib(), ce.Policy(1.0, 1.0, 0.2, 0.2, 0.0, 0.0)
+    x, g = logits_at(rows, vocab, vocab, torch.float32, seed=rows)
+    y = torch.randint(0, vocab, (rows,), generator=g, device=DEV)
+    old = ce.logp_rows(x, y)
+    advs = [(-1.0) ** i * (1 + i) * (torch.rand(rows, generator=g, device=DEV) + 0.5) for i in range(passes)]
+    loss_rows, logp = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    kept = [torch.empty(rows, device=DEV) for _ in range(passes)]
+    losses = torch.full((passes,), math.nan, device=DEV)
+    s = torch.cuda.current_stream().cuda_stream
+    for i, adv in enumerate(advs):
+        st = L.policy_loss(x.data_ptr(), 0, rows, vocab, vocab, y.data_ptr(), old.data_ptr(), adv.data_ptr(), None, None,
+                           ctypes.byref(par), loss_rows.data_ptr(), logp.data_ptr(), None, losses[i:].data_ptr(), s)
+        assert st == ce.CE_OK
+        if i % 3 == 2:  # mostly nothing between two passes
+            kept[i].copy_(loss_rows)
+    for i in range(2, passes, 3):
+        # the sum is of at least 48 bits relative to its largest partial sum, then one rounding
+        want, size = kept[i].double().sum(), kept[i].double().abs().sum()
+        assert abs(float(losses[i]) - float(want)) <= R.U * abs(float(want)) + 2.0 ** -47 * float(size) * rows, i
+    for i in range(passes):
+        want = -(advs[i].double()).sum()  # ratios of 1 within 1e-5
+        assert abs(float(losses[i]) - float(want)) <= 1e-4 * float(advs[i].double().abs().sum()), i
