@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows(ObjArgs a, int col
         auto early = [&] {
             if (rank == 0 && tid == 0) numbers = load_numbers<T, kMode>(a, row, p, label);
         };
-        TokState st = tok_scan<T, kEnt, kScanUnroll, kScanThreads>(p + c0, n, a.k, tid, early);
+        TokState st = tok_scan<T, kEnt, kScanUnroll, kScanThreads, true>(p + c0, n, a.k, tid, early);
         st = tok_warp_reduce<kEnt>(st, a.k);
         const float4 mine = make_float4(st.m, st.s, st.u, 0.0f);
         if (C > 1) {
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kScanThreads, 8) k_obj_rows_warp(ObjArgs a) {
         auto early = [&] {
             if (lane == 0) numbers = load_numbers<T, kMode>(a, row, p, label);
         };
-        TokState st = tok_scan<T, kEnt, kScanUnroll, 32>(p, a.vocab, a.k, lane, early);
+        TokState st = tok_scan<T, kEnt, kScanUnroll, 32, true>(p, a.vocab, a.k, lane, early);
         st = tok_warp_reduce<kEnt>(st, a.k);
         if (lane == 0) write_row<kMode, kEnt>(a, row, st, numbers, w);
     }
@@ -298,7 +298,8 @@ __device__ __forceinline__ void zero_slice(T *g, int n, int tid, int nt) {
 
 // ---------------------------------------------------------------------------
 // k_policy_stream: the policy's loss and gradient; the cluster's CTAs read
-// their slices twice (state, then gradient).
+// their slices twice (state, then gradient), both times by coherent loads: the
+// gradient may be written over the logits.
 template <typename T, bool kEnt>
 __global__ void __launch_bounds__(kRowsThreads, 4) k_policy_stream(ObjArgs a, int cols) {
     __shared__ TokState red[32];
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(kRowsThreads, 4) k_policy_stream(ObjArgs a, in
             adv = a.adv[row];
             if (a.ref_logp) ref = a.ref_logp[row];
         }
-        TokState st = tok_scan<T, kEnt, kRowsUnroll, kRowsThreads>(p, n, a.k, tid, [] {});
+        TokState st = tok_scan<T, kEnt, kRowsUnroll, kRowsThreads, false>(p, n, a.k, tid, [] {});
         st = tok_block_reduce_w0<kEnt>(st, red, a.k);
         if (used == 0) cluster_wait();
         if (tid == 0) tok_publish(xg, used, rank, C, st, xl);

@@ -321,14 +321,26 @@ __device__ __forceinline__ TokState warp_xchg_collect(WarpXchg<kW> &x, int64_t n
     return tok_warp_reduce<kEnt>(st, k);
 }
 
+// Loads of logits that are read once: past L1, on the read-only path where the
+// kernel writes nothing over them (kRead), by coherent loads where a gradient
+// may be written over them (in place).
+template <bool kRead>
+__device__ __forceinline__ uint4 ld_logits(const uint4 *p) {
+    return kRead ? ld_stream_u4(p) : __ldcs(p);
+}
+template <bool kRead, typename T>
+__device__ __forceinline__ T ld_logits(const T *p) {
+    return kRead ? __ldg(p) : __ldcs(p);
+}
+
 // Push the columns [0, n) at p: a scalar head up to the first 16-byte
 // boundary, 16-byte vectors kU at a time per thread, a scalar tail. A partial
 // group is filled up with -inf (which adds nothing) rather than read vector by
 // vector, so a thread's loads never wait for one another. `early` runs once
 // the first group's loads are on their way: a load that it waits for costs no
 // more than they do.
-template <typename T, bool kEnt, int kU, int kT, typename Early>
-__device__ __forceinline__ TokState tok_scan(const T *__restrict__ p, int n, float k, int tid, Early early) {
+template <typename T, bool kEnt, int kU, int kT, bool kRead, typename Early>
+__device__ __forceinline__ TokState tok_scan(const T *p, int n, float k, int tid, Early early) {
     TokState st = tok_empty();
     constexpr int N = Vec<T>::kN, kStep = kU * kT;
     const int off = static_cast<int>((reinterpret_cast<uintptr_t>(p) / sizeof(T)) % N);
@@ -340,18 +352,18 @@ __device__ __forceinline__ TokState tok_scan(const T *__restrict__ p, int n, flo
     auto load = [&](int q0) {
 #pragma unroll
         for (int u = 0; u < kU; ++u)
-            v[u] = q0 + u * kT < nvec ? ld_stream_u4(pv + q0 + u * kT) : Vec<T>::lowest();
+            v[u] = q0 + u * kT < nvec ? ld_logits<kRead>(pv + q0 + u * kT) : Vec<T>::lowest();
     };
     T ends[2];
     load(tid);
-    if (tid < head) ends[0] = p[tid];
-    if (tid < tail) ends[1] = p[head + N * nvec + tid];
+    if (tid < head) ends[0] = ld_logits<kRead>(p + tid);
+    if (tid < tail) ends[1] = ld_logits<kRead>(p + head + N * nvec + tid);
     early();
     tok_push<T, kEnt, kU>(st, v, k);
     int q = tid + kStep;
     for (; q + (kU - 1) * kT < nvec; q += kStep) {
 #pragma unroll
-        for (int u = 0; u < kU; ++u) v[u] = ld_stream_u4(pv + q + u * kT);
+        for (int u = 0; u < kU; ++u) v[u] = ld_logits<kRead>(pv + q + u * kT);
         tok_push<T, kEnt, kU>(st, v, k);
     }
     if (q < nvec) {

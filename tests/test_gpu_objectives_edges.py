@@ -131,3 +131,22 @@ def test_sum_of_the_pass_before_it(rows):
     for i in range(passes):
         want = -(advs[i].double()).sum()  # ratios of 1 within 1e-5
         assert abs(float(losses[i]) - float(want)) <= 1e-4 * float(advs[i].double().abs().sum()), i
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("kernel", range(3), ids=["warp", "staged", "stream"])
+def test_in_place_of_rows_that_share_lines(dtype, kernel):
+    """Odd rows without padding, so that neighbouring rows and slices share
+    their 128-byte lines, written in place: the bits of a gradient of its own."""
+    rows, vocab = (2000, 1000, 9)[kernel], VOCABS[dtype][kernel]
+    vocab += vocab % 2 == 0
+    rows = min(rows, (1 << 26) // vocab)
+    x, g = logits_at(rows, vocab, vocab, dtype, seed=vocab + 2, offset=3)
+    y = torch.randint(0, vocab, (rows,), generator=g, device=DEV)
+    old, adv = torch.full((rows,), -12.0, device=DEV), torch.randn(rows, generator=g, device=DEV)
+    own = ce.policy_step(x, y, old, adv, 1.0, entropy_coef=0.01)
+    for _ in range(2):
+        z = torch.empty(x.numel() + 3, dtype=dtype, device=DEV)[3:].view(rows, vocab)  # at the phase of x
+        z.copy_(x)
+        there = ce.policy_step(z, y, old, adv, 1.0, entropy_coef=0.01, grad=z)
+        assert all(torch.equal(a, b) for a, b in zip(there[:4], own[:4]))
