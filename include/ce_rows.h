@@ -366,6 +366,8 @@ CE_API int ce_grad_from_stats(const float *logits, int64_t rows, int64_t vocab, 
  *    grad_stride elements apart (grad_stride >= vocab; columns vocab and up
  *    are not written). grad == logits (in place) is allowed when grad_stride
  *    == stride (or rows == 1); any other overlap is CE_EINVAL.
+ *  - Outputs and the work buffer share no byte with an input or with one
+ *    another (CE_EINVAL); they may lie in the padding of the logits' rows.
  *  - A label outside [0, vocab) on a row that counts gives that row a NaN
  *    log-probability (and so a NaN loss and gradient row) and increments the
  *    device counter. A row holding a NaN or +inf, or nothing above -inf, is

@@ -568,7 +568,8 @@ def logp_rows(logits: torch.Tensor, labels: torch.Tensor, weights: torch.Tensor 
     """The log-probability of each row's label under softmax(logits /
     temperature), f32 ``[rows]``; with ``entropy`` (True or a tensor) the pair
     ``(logp, entropy)`` from the same read. ``weights`` (f32 ``[rows]``): rows of
-    weight 0 are not read and give 0."""
+    weight 0 are not read and give 0. ``out`` and ``entropy``, here and
+    below, share no memory with an input or with each other."""
     got = _done("logp_rows", (_objectives or _bound()).logp_rows(logits, labels, weights, temperature, vocab, entropy, out))
     return got if got[1] is not None else got[0]
 

@@ -11,6 +11,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstdlib>
+#include <initializer_list>
 #include <mutex>
 
 #include "ce_internal.h"
@@ -707,6 +708,43 @@ static int check_objective_grad(const void *logits, int dtype, int64_t rows, int
                : CE_OK;
 }
 
+struct Bytes {
+    const void *p;
+    int64_t n;
+};
+
+// Do `rows` rows of row_bytes, stride_bytes apart, and a flat array share a byte?
+// Not where the array lies in the rows' padding.
+static bool rows_meet(const void *base, int64_t rows, int64_t row_bytes, int64_t stride_bytes, const Bytes &flat) {
+    if (base == nullptr || flat.p == nullptr || rows <= 0 || flat.n <= 0) return false;
+    if (!ranges_overlap(base, (rows - 1) * stride_bytes + row_bytes, flat.p, flat.n)) return false;
+    const uintptr_t b = reinterpret_cast<uintptr_t>(base), f = reinterpret_cast<uintptr_t>(flat.p);
+    if (f <= b) return true;
+    const int64_t at = static_cast<int64_t>((f - b) % static_cast<uintptr_t>(stride_bytes));
+    return at < row_bytes || at + flat.n > stride_bytes;
+}
+
+// Outputs share no byte with an input or with one another (the gradient with
+// the logits: check_objective_grad). The kernels read a row's weight, label and
+// range in many threads, some after others' rows have been written: over a
+// shared byte they would not agree on what a row is, and wait for one another.
+static int check_apart(const ObjArgs &a, int dtype, const void *grad, int64_t grad_stride,
+                       std::initializer_list<Bytes> inputs, std::initializer_list<Bytes> outputs) {
+    const int64_t size = dtype == CE_F32 ? 4 : 2, row = a.vocab * size;
+    for (const Bytes &o : outputs) {
+        if (rows_meet(a.logits, a.rows, row, a.stride * size, o)) return CE_EINVAL;
+        if (rows_meet(grad, a.rows, row, grad_stride * size, o)) return CE_EINVAL;
+        if (o.p == nullptr || o.n <= 0) continue;
+        for (const Bytes &i : inputs)
+            if (i.p != nullptr && i.n > 0 && ranges_overlap(o.p, o.n, i.p, i.n)) return CE_EINVAL;
+        for (const Bytes *q = &o + 1; q != outputs.end(); ++q)
+            if (q->p != nullptr && q->n > 0 && ranges_overlap(o.p, o.n, q->p, q->n)) return CE_EINVAL;
+    }
+    for (const Bytes &i : inputs)
+        if (rows_meet(grad, a.rows, row, grad_stride * size, i)) return CE_EINVAL;
+    return CE_OK;
+}
+
 int logp_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride, const int64_t *labels,
               const float *weights, double temperature, float *logp, float *entropy, ce_stream_t stream) {
     ObjArgs a;
@@ -714,6 +752,9 @@ int logp_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_
     if (st) return st;
     if (misaligned(entropy, 4)) return CE_EALIGN;
     if (rows == 0) return CE_OK;
+    if ((st = check_apart(a, dtype, nullptr, 0, {{labels, 8 * rows}, {weights, 4 * rows}},
+                          {{logp, 4 * rows}, {entropy, 4 * rows}})))
+        return st;
     DeviceInfo dev;
     if ((st = current_device(&dev))) return st;
     a.entropy = entropy;
@@ -739,6 +780,14 @@ static int policy_pass(const void *logits, int dtype, int64_t rows, int64_t voca
         misaligned(entropy, 4) || misaligned(loss, 4))
         return CE_EALIGN;
     if (step && (st = check_objective_grad(logits, dtype, rows, vocab, stride, grad, grad_stride))) return st;
+    if ((st = check_apart(a, dtype, grad, grad_stride,
+                          {{labels, 8 * rows},
+                           {weights, 4 * rows},
+                           {old_logp, 4 * rows},
+                           {advantages, 4 * rows},
+                           {a.kl != 0.0f ? ref_logp : nullptr, 4 * rows}},
+                          {{loss_rows, 4 * rows}, {logp, 4 * rows}, {entropy, 4 * rows}, {loss, 4}})))
+        return st;
     DeviceInfo dev;
     if ((st = current_device(&dev))) return st;
     if (rows > 0) {
@@ -794,6 +843,11 @@ static int preference_pass(const void *logits, int dtype, int64_t rows, int64_t 
         misaligned(loss, 4) || misaligned(work, 16))
         return CE_EALIGN;
     if (step && (st = check_objective_grad(logits, dtype, rows, vocab, stride, grad, grad_stride))) return st;
+    if ((st = check_apart(
+             a, dtype, grad, grad_stride,
+             {{labels, 8 * rows}, {weights, 4 * rows}, {offsets, 8 * (2 * pairs + 1)}, {ref_logp, 8 * pairs}},
+             {{logp, 4 * rows}, {seq_logp, 8 * pairs}, {loss_pairs, 4 * pairs}, {loss, 4}, {work, 16 * (step ? rows + 1 : 1)}})))
+        return st;
     DeviceInfo dev;
     if ((st = current_device(&dev))) return st;
     const DType t = static_cast<DType>(dtype);
@@ -847,7 +901,7 @@ const char *ce_status_string(int status) {
     switch (status) {
     case CE_OK: return "ok";
     case CE_EINVAL:
-        return "invalid argument (null pointer, size, stride, vocab > 2^24, scale, type, constant of a loss or forced plan)";
+        return "invalid argument (null pointer, size, stride, overlap, vocab > 2^24, scale, type, constant of a loss or forced plan)";
     case CE_EALIGN: return "pointer not aligned to its element size";
     case CE_ECUDA: return "CUDA runtime error at launch (see ce_last_cuda_error)";
     case CE_EDEVICE: return "no usable sm_103 CUDA device";

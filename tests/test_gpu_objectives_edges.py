@@ -150,3 +150,20 @@ def test_in_place_of_rows_that_share_lines(dtype, kernel):
         z.copy_(x)
         there = ce.policy_step(z, y, old, adv, 1.0, entropy_coef=0.01, grad=z)
         assert all(torch.equal(a, b) for a, b in zip(there[:4], own[:4]))
+
+
+def test_given_outputs_over_other_tensors_are_refused():
+    x, y = torch.randn(6, 50, device=DEV), torch.zeros(6, dtype=torch.int64, device=DEV)
+    f, w, two = torch.zeros(6, device=DEV), torch.ones(7, device=DEV), torch.empty(6, device=DEV)
+    for kw in (dict(out=two, entropy=two), dict(out=w[1:], weights=w[:6]), dict(entropy=w[:6], weights=w[:6]),
+               dict(out=x[2, 10:16])):
+        with pytest.raises(ce.CeError):
+            ce.logp_rows(x, y, **kw)
+    for call in (ce.policy_loss, ce.policy_step):
+        for kw in (dict(entropy=f), dict(entropy=w[1:], weights=w[:6]), dict(entropy=x[0, :6])):
+            with pytest.raises(ce.CeError):
+                call(x, y, f, f, 1.0, **kw)
+    assert bool((w == 1).all()) and not f.any()
+    wide = torch.randn(6, 60, device=DEV)
+    got = ce.logp_rows(wide, y, vocab=50, out=wide[3, 52:58])  # the padding of a row is not the logits'
+    assert torch.equal(got, ce.logp_rows(wide[:, :50], y))
