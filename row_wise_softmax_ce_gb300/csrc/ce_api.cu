@@ -23,7 +23,6 @@ namespace {
 
 constexpr int kVersion = 10000;            // 1.0.0
 constexpr int64_t kMaxVocab = 1ll << 24;   // tokens are written exactly as f32
-constexpr int kMaxDevices = 64;
 constexpr int kStagedTargetCols = 16384;   // 64 KB of f32 per CTA: 3 CTAs per SM
 constexpr int kStagedTargetCols4 = 13816;  // the widest slice of which 4 CTAs fit an SM's 228 KB
                                            // (2 KB header, 16-byte grid, 1 KB reserved per CTA)
@@ -60,7 +59,8 @@ bool misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int round_up4(int64_t v) { return static_cast<int>((v + 3) & ~int64_t(3)); }
 
-// The current device, its properties, and the kernels' attributes (set once).
+// The current device, its properties, and the kernels' attributes (set once; the
+// objectives' kernels set theirs at their first launch).
 int current_device(DeviceInfo *out) {
     int dev = -1;
     cudaError_t e = cudaGetDevice(&dev);
@@ -83,7 +83,6 @@ int current_device(DeviceInfo *out) {
         }
         if (d.cc_major != 10 || d.cc_minor != 3) return CE_EDEVICE;  // built for sm_103a only
         if ((e = set_kernel_attributes(d)) != cudaSuccess) return cuda_status(e);
-        if ((e = set_objective_attributes(d)) != cudaSuccess) return cuda_status(e);
         g_dev[dev] = d;
         g_ready[dev] = true;
     }
@@ -983,7 +982,7 @@ static int read_counter(ce_stream_t stream, int which, int64_t *out) {
     if (st) return st;
     unsigned long long v[2] = {0ull, 0ull}, o[2] = {0ull, 0ull};
     if ((st = cuda_status(read_status(v, stream)))) return st;
-    if ((st = cuda_status(read_objective_status(o, stream)))) return st;
+    if ((st = cuda_status(read_objective_status(o, dev, stream)))) return st;
     *out = static_cast<int64_t>(v[which] + o[which]);
     return CE_OK;
 }
@@ -997,7 +996,7 @@ int ce_device_error_reset(ce_stream_t stream) {
     int st = current_device(&dev);
     if (st) return st;
     if ((st = cuda_status(reset_status(stream)))) return st;
-    return cuda_status(reset_objective_status(stream));
+    return cuda_status(reset_objective_status(dev, stream));
 }
 
 int ce_debug_force(int path, int cluster, int threads) {

@@ -67,6 +67,8 @@ struct Plan {
     int64_t clusters = 0;  // clusters in the grid (each loops over rows)
 };
 
+constexpr int kMaxDevices = 64;
+
 struct DeviceInfo {
     int device = -1;
     int sms = 0;
@@ -134,7 +136,6 @@ struct JoinArgs {
     uint32_t *done;
 };
 
-cudaError_t set_objective_attributes(const DeviceInfo &dev);
 cudaError_t launch_obj_rows(DType t, ObjMode mode, const ObjArgs &a, const DeviceInfo &dev, cudaStream_t s);
 cudaError_t launch_policy_grad(DType t, const ObjArgs &a, const DeviceInfo &dev, cudaStream_t s);
 cudaError_t launch_join(const JoinArgs &j, const DeviceInfo &dev, cudaStream_t s);
@@ -142,8 +143,9 @@ cudaError_t launch_preference_grad(DType t, const ObjArgs &a, const DeviceInfo &
 // *out = scale * sum of weights[i] * loss[i] (weights null: 1), summed in f64
 cudaError_t launch_weighted_sum(const float *loss, const float *weights, int64_t rows, double scale, float *out,
                                 cudaStream_t s);
-cudaError_t read_objective_status(unsigned long long out[2], cudaStream_t s);
-cudaError_t reset_objective_status(cudaStream_t s);
+// nothing to read or reset on a device that has launched no objective
+cudaError_t read_objective_status(unsigned long long out[2], const DeviceInfo &dev, cudaStream_t s);
+cudaError_t reset_objective_status(const DeviceInfo &dev, cudaStream_t s);
 
 cudaError_t set_kernel_attributes(const DeviceInfo &dev);
 cudaError_t max_active_clusters(const Plan &p, Op op, int *n);

@@ -19,6 +19,7 @@
 //   k_pair_grad      the gradient of a preference batch, the rows read again
 //   k_weighted_sum   the policy's loss, a fixed-shape tree of f32 pairs
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "ce_internal.h"
@@ -929,48 +930,74 @@ struct LaunchConfig {
     }
 };
 
+// Devices (a bit each) that have launched an objective. Touching a kernel or a
+// variable of this file loads all of its code, 10 ms once: no other function of
+// the library's does.
+std::atomic<uint64_t> g_launched{0};
+static_assert(kMaxDevices <= 64, "a bit per device");
+
+uint64_t bit_of(const DeviceInfo &dev) { return uint64_t(1) << dev.device; }
+bool launched(const DeviceInfo &dev) { return g_launched.load(std::memory_order_acquire) & bit_of(dev); }
+void launches(const DeviceInfo &dev) {
+    if (!launched(dev)) g_launched.fetch_or(bit_of(dev), std::memory_order_release);
+}
+
+// A kernel and the devices on which its attributes are set: clusters of up to 16
+// CTAs, and as much shared memory as a CTA may have. Set at the kernel's first
+// launch on a device.
+struct Kernel {
+    const void *fn;
+    bool smem;
+    std::atomic<uint64_t> set{0};
+    Kernel(const void *f, bool dynamic_smem) : fn(f), smem(dynamic_smem) {}
+};
+cudaError_t ready(Kernel &k, const DeviceInfo &dev) {
+    const uint64_t bit = bit_of(dev);
+    if (k.set.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && k.smem)
+        e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, dev.max_smem_optin);
+    if (e == cudaSuccess) k.set.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
 template <typename T, int kMode, bool kEnt>
-const void *rows_kernel_m(bool warp) {
-    return warp ? reinterpret_cast<const void *>(&k_obj_rows_warp<T, kMode, kEnt>)
-                : reinterpret_cast<const void *>(&k_obj_rows<T, kMode, kEnt>);
+Kernel &rows_kernel_m(bool warp) {
+    static Kernel row_warp(reinterpret_cast<const void *>(&k_obj_rows_warp<T, kMode, kEnt>), false),
+        row_cta(reinterpret_cast<const void *>(&k_obj_rows<T, kMode, kEnt>), false);
+    return warp ? row_warp : row_cta;
 }
 
 template <typename T>
-const void *rows_kernel_t(ObjMode mode, bool ent, bool warp) {
+Kernel &rows_kernel_t(ObjMode mode, bool ent, bool warp) {
     if (mode == kObjPreference) return rows_kernel_m<T, kObjPreference, false>(warp);
     if (mode == kObjPolicy)
         return ent ? rows_kernel_m<T, kObjPolicy, true>(warp) : rows_kernel_m<T, kObjPolicy, false>(warp);
     return ent ? rows_kernel_m<T, kObjLogp, true>(warp) : rows_kernel_m<T, kObjLogp, false>(warp);
 }
 
-const void *rows_kernel(DType t, ObjMode mode, bool ent, bool warp) {
+Kernel &rows_kernel(DType t, ObjMode mode, bool ent, bool warp) {
     return t == kF32    ? rows_kernel_t<float>(mode, ent, warp)
            : t == kBF16 ? rows_kernel_t<__nv_bfloat16>(mode, ent, warp)
                         : rows_kernel_t<__half>(mode, ent, warp);
 }
 
-template <typename T>
-const void *policy_stream_t(bool ent) {
-    return ent ? reinterpret_cast<const void *>(&k_policy_stream<T, true>)
-               : reinterpret_cast<const void *>(&k_policy_stream<T, false>);
-}
-
-const void *policy_stream(DType t, bool ent) {
-    return t == kF32    ? policy_stream_t<float>(ent)
-           : t == kBF16 ? policy_stream_t<__nv_bfloat16>(ent)
-                        : policy_stream_t<__half>(ent);
+template <typename T, bool kEnt>
+Kernel &policy_cluster_m(bool staged) {
+    static Kernel once(reinterpret_cast<const void *>(&k_policy_staged<T, kEnt>), true),
+        twice(reinterpret_cast<const void *>(&k_policy_stream<T, kEnt>), false);
+    return staged ? once : twice;
 }
 
 template <typename T>
-const void *policy_staged_t(bool ent) {
-    return ent ? reinterpret_cast<const void *>(&k_policy_staged<T, true>)
-               : reinterpret_cast<const void *>(&k_policy_staged<T, false>);
+Kernel &policy_cluster_t(bool ent, bool staged) {
+    return ent ? policy_cluster_m<T, true>(staged) : policy_cluster_m<T, false>(staged);
 }
 
-const void *policy_staged(DType t, bool ent) {
-    return t == kF32    ? policy_staged_t<float>(ent)
-           : t == kBF16 ? policy_staged_t<__nv_bfloat16>(ent)
-                        : policy_staged_t<__half>(ent);
+Kernel &policy_cluster(DType t, bool ent, bool staged) {
+    return t == kF32    ? policy_cluster_t<float>(ent, staged)
+           : t == kBF16 ? policy_cluster_t<__nv_bfloat16>(ent, staged)
+                        : policy_cluster_t<__half>(ent, staged);
 }
 
 template <typename T, int kV>
@@ -1047,30 +1074,13 @@ int cols_of(int64_t vocab, int c) { return static_cast<int>(((vocab + c - 1) / c
 
 }  // namespace
 
-cudaError_t set_objective_attributes(const DeviceInfo &dev) {
-    for (DType t : {kF32, kBF16, kF16})
-        for (bool ent : {false, true}) {
-            for (ObjMode m : {kObjLogp, kObjPolicy, kObjPreference}) {
-                cudaError_t e = cudaFuncSetAttribute(rows_kernel(t, m, ent, false), cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-                if (e != cudaSuccess) return e;
-            }
-            for (const void *f : {policy_stream(t, ent), policy_staged(t, ent)}) {
-                cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-                if (e != cudaSuccess) return e;
-            }
-            cudaError_t e = cudaFuncSetAttribute(policy_staged(t, ent), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 dev.max_smem_optin);
-            if (e != cudaSuccess) return e;
-        }
-    return cudaSuccess;
-}
-
 cudaError_t launch_obj_rows(DType t, ObjMode mode, const ObjArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+    launches(dev);
     if (forward_warp(t, a.rows, a.vocab, dev)) {
         ObjArgs aa = a;
         void *args[] = {&aa};
         LaunchConfig l(warp_ctas(a), kScanThreads, 0, false, s);
-        return cudaLaunchKernelExC(&l.cfg, rows_kernel(t, mode, wants_entropy(a), true), args);
+        return cudaLaunchKernelExC(&l.cfg, rows_kernel(t, mode, wants_entropy(a), true).fn, args);
     }
     // a cluster of several CTAs takes one row, no more and no fewer
     const int64_t clusters = capped(a.rows, a);
@@ -1078,8 +1088,10 @@ cudaError_t launch_obj_rows(DType t, ObjMode mode, const ObjArgs &a, const Devic
     ObjArgs aa = a;
     int cols = cols_of(a.vocab, c);
     void *args[] = {&aa, &cols};
+    Kernel &k = rows_kernel(t, mode, wants_entropy(a), false);
+    if (cudaError_t e = ready(k, dev); e != cudaSuccess) return e;
     LaunchConfig l(clusters * c, kScanThreads, c, false, s);
-    return cudaLaunchKernelExC(&l.cfg, rows_kernel(t, mode, wants_entropy(a), false), args);
+    return cudaLaunchKernelExC(&l.cfg, k.fn, args);
 }
 
 // Shared memory of a staged CTA that holds `cols` columns at any phase.
@@ -1116,6 +1128,7 @@ static int staged_split(DType t, int64_t rows, int64_t vocab, const DeviceInfo &
 }
 
 cudaError_t launch_policy_grad(DType t, const ObjArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+    launches(dev);
     const bool ent = wants_entropy(a);
     const int64_t clusters = capped(a.rows, a);
     ObjArgs aa = a;
@@ -1133,8 +1146,10 @@ cudaError_t launch_policy_grad(DType t, const ObjArgs &a, const DeviceInfo &dev,
     int cols = cols_of(a.vocab, c);
     void *args[] = {&aa, &cols};
     const int threads = staged ? kStagedThreads : kRowsThreads;
+    Kernel &k = policy_cluster(t, ent, staged);
+    if (cudaError_t e = ready(k, dev); e != cudaSuccess) return e;
     LaunchConfig l(clusters * c, threads, c, false, s, staged ? static_cast<int>(staged_smem(t, cols)) : 0);
-    return cudaLaunchKernelExC(&l.cfg, staged ? policy_staged(t, ent) : policy_stream(t, ent), args);
+    return cudaLaunchKernelExC(&l.cfg, k.fn, args);
 }
 
 cudaError_t launch_join(const JoinArgs &j, const DeviceInfo &dev, cudaStream_t s) {
@@ -1175,14 +1190,17 @@ cudaError_t launch_weighted_sum(const float *loss, const float *weights, int64_t
     return cudaLaunchKernelEx(&l.cfg, k_weighted_sum, loss, weights, rows, scale, out);
 }
 
-cudaError_t read_objective_status(unsigned long long out[2], cudaStream_t s) {
+cudaError_t read_objective_status(unsigned long long out[2], const DeviceInfo &dev, cudaStream_t s) {
+    out[0] = out[1] = 0ull;
+    if (!launched(dev)) return cudaSuccess;
     cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_objective_status, sizeof(unsigned long long) * 2, 0,
                                               cudaMemcpyDeviceToHost, s);
     if (e != cudaSuccess) return e;
     return cudaStreamSynchronize(s);
 }
 
-cudaError_t reset_objective_status(cudaStream_t s) {
+cudaError_t reset_objective_status(const DeviceInfo &dev, cudaStream_t s) {
+    if (!launched(dev)) return cudaSuccess;
     static const unsigned long long zero[2] = {0ull, 0ull};
     return cudaMemcpyToSymbolAsync(g_objective_status, zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
 }
