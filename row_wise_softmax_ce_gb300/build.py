@@ -26,6 +26,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcerows.so")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_FOR = os.path.join(BUILD, "binding_for.txt")  # what the binding was built against
 
 SOURCES = ["ce_kernels.cu", "ce_objectives.cu", "ce_api.cu"]
 HEADERS = ["ce_device.cuh", "ce_objectives.cuh", "ce_internal.h"]
@@ -50,6 +51,8 @@ def _inputs() -> list[str]:
 def up_to_date() -> bool:
     if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
+    if _read(BINDING_FOR) != _binding_for():
+        return False  # another PyTorch or Python since
     t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
@@ -66,6 +69,20 @@ def _run(cmd: list[str], verbose: bool, what: str) -> None:
 
 def _torch_dir() -> str:
     return list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+
+
+def _read(path: str) -> str:
+    try:
+        with open(path) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
+def _binding_for() -> str:
+    """The Python ABI and the PyTorch (where it is, and its version file) that a binding fits."""
+    torch = _torch_dir()
+    return "\n".join([sysconfig.get_config_var("SOABI") or "", torch, _read(os.path.join(torch, "version.py"))])
 
 
 def _compile_binding(cc: str, verbose: bool) -> str:
@@ -85,11 +102,14 @@ def _link_binding(obj: str, verbose: bool) -> None:
     _run([os.environ.get("CXX", "g++"), "-shared", obj, "-o", tmp, f"-L{_torch_dir()}/lib", *[f"-l{n}" for n in libs],
           f"-L{PKG}", "-l:libcerows.so", "-Wl,-rpath,$ORIGIN", "-Wl,-z,now"], verbose, "the binding")
     os.replace(tmp, BINDING)
+    with open(BINDING_FOR, "w") as f:
+        f.write(_binding_for())
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile and link; returns the library path. Rebuilds only when a
-    source is newer than the library (or ``force``)."""
+    source is newer than the library or the binding was built against another
+    PyTorch or Python (or ``force``)."""
     if not force and not ptxas_info and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
