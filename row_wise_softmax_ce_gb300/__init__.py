@@ -597,7 +597,8 @@ def policy_step(logits: torch.Tensor, labels: torch.Tensor, old_logp: torch.Tens
     type, from one read: returns ``(grad, loss, loss_rows, logp, entropy)``.
     ``grad`` may be the logits themselves (in place) or any ``[rows, >= vocab]``
     tensor with contiguous rows (columns past vocab are left alone); dense
-    ``[rows, vocab]`` when not given."""
+    ``[rows, vocab]`` when not given. A tensor that is written to, here and in the
+    other objectives, counts as changed in place for autograd."""
     return _done("policy_step", (_objectives or _bound()).policy(
         True, logits, labels, old_logp, advantages, scale, ref_logp, weights, clip_low, clip_high, kl_coef,
         entropy_coef, temperature, vocab, entropy, grad))

@@ -148,6 +148,15 @@ ce_stream_t stream_of(const Logits &x) {
     return reinterpret_cast<ce_stream_t>(c10::cuda::getCurrentCUDAStream(x.t.device().index()).stream());
 }
 
+// Tells autograd that a call wrote to a tensor of the caller's, as an in-place
+// operation of PyTorch does: a backward pass that saved it raises an error
+// instead of reading what is there now. Inference tensors keep no version.
+void written(int status, PyObject *given) {
+    if (status != CE_OK || !THPVariable_Check(given)) return;
+    const at::Tensor &t = THPVariable_Unpack(given);
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // The tensors as a tuple (None for one that was not wanted), or the status.
 PyObject *result(int status, std::initializer_list<at::Tensor> tensors) {
     if (status != CE_OK) return PyLong_FromLong(status);
@@ -183,6 +192,8 @@ PyObject *logp(PyObject *const *a) {
         st = logp_rows(x.t.data_ptr(), x.dtype, x.rows, x.vocab, x.stride, labels, w, temperature, data(out),
                        data(ent.t), stream_of(x));
     }
+    written(st, a[5]);
+    written(st, a[6]);
     return result(st, {out, ent.t});
 }
 
@@ -218,6 +229,8 @@ PyObject *policy(PyObject *const *a) {
                              data(rows), data(lp), data(ent.t), data(loss), stream_of(x));
         }
     }
+    written(st, a[14]);
+    written(st, a[15]);
     return step ? result(st, {grad, loss, rows, lp, ent.t}) : result(st, {loss, rows, lp, ent.t});
 }
 
@@ -262,6 +275,7 @@ PyObject *preference(PyObject *const *a) {
                                  data(pair_losses), data(loss), work.data_ptr(), stream_of(x));
         }
     }
+    written(st, a[14]);
     return step ? result(st, {grad, loss, pair_losses, seq, lp}) : result(st, {loss, pair_losses, seq, lp});
 }
 

@@ -167,3 +167,37 @@ def test_given_outputs_over_other_tensors_are_refused():
     wide = torch.randn(6, 60, device=DEV)
     got = ce.logp_rows(wide, y, vocab=50, out=wide[3, 52:58])  # the padding of a row is not the logits'
     assert torch.equal(got, ce.logp_rows(wide[:, :50], y))
+
+
+def test_writing_to_a_tensor_counts_as_in_place():
+    """A caller's tensor that a call writes to has a new version, so that a
+    backward pass that saved it refuses; what is only read has not, nor what a
+    refused call would have written."""
+    head = torch.randn(50, 8, device=DEV, requires_grad=True)
+    y, f = torch.zeros(6, dtype=torch.int64, device=DEV), torch.zeros(6, device=DEV)
+    ends = torch.tensor([0, 3, 6], device=DEV)
+    for call in (lambda z, g: ce.policy_step(z, y, f, f + 1, 1.0, grad=g),
+                 lambda z, g: ce.preference_step(z, y, ends, 1.0, grad=g)):
+        x = torch.randn(6, 8, device=DEV) @ head.t()
+        loss = (x * x).sum()  # saves x
+        call(x.detach(), None)
+        loss.backward(retain_graph=True)
+        call(x.detach(), x.detach())
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    x, out, ent = torch.randn(6, 50, device=DEV), torch.empty(6, device=DEV), torch.empty(6, device=DEV)
+    ce.logp_rows(x, y, out=out, entropy=ent)
+    assert (x._version, y._version, out._version, ent._version) == (0, 0, 1, 1)
+    ce.policy_loss(x, y, f, f, 1.0, entropy=ent)
+    grad = torch.empty(6, 50, device=DEV)
+    ce.policy_step(x, y, f, f, 1.0, entropy=ent, grad=grad)
+    assert (x._version, f._version, ent._version, grad._version) == (0, 0, 3, 1)
+    with pytest.raises(ce.CeError):
+        ce.policy_step(x, y, f, f, 1.0, temperature=0.0, grad=grad)
+    assert grad._version == 1
+    with torch.inference_mode():
+        z, out = torch.randn(6, 50, device=DEV), torch.empty(6, device=DEV)
+        want = ce.policy_step(z, y, f, f + 1, 1.0)[0]
+        ce.logp_rows(z, y, out=out)
+        assert torch.equal(ce.policy_step(z, y, f, f + 1, 1.0, grad=z)[0], want)
+    ce.logp_rows(z, y, out=out)  # inference tensors outside the mode: no version to count
