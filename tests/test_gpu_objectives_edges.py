@@ -201,3 +201,18 @@ def test_writing_to_a_tensor_counts_as_in_place():
         ce.logp_rows(z, y, out=out)
         assert torch.equal(ce.policy_step(z, y, f, f + 1, 1.0, grad=z)[0], want)
     ce.logp_rows(z, y, out=out)  # inference tensors outside the mode: no version to count
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("vocab", [905000, 920000, 920800, 921600])
+def test_rows_that_fill_a_cluster(dtype, vocab):
+    """Rows around the longest that the shared memory of 16 CTAs holds (about
+    3.5 MB), at a phase of their own: staged below it, read twice above."""
+    vocab *= 1 if dtype == torch.float32 else 2
+    x, g = logits_at(3, vocab, vocab + 1, dtype, seed=7, offset=1)
+    y = torch.randint(0, vocab, (3,), generator=g, device=DEV)
+    adv = torch.randn(3, generator=g, device=DEV)
+    old = R.logp64(x, y)["logp"][0].float() + 0.05
+    want = R.policy64(x, y, old, adv, 64.0, entropy_coef=0.01)
+    got = ce.policy_step(x, y, old, adv, 64.0, entropy_coef=0.01, entropy=True)
+    check(dict(zip(("grad", "loss", "loss_rows", "logp", "entropy"), got)), want, f"{vocab}")
