@@ -355,13 +355,20 @@ CE_API int ce_grad_from_stats(const float *logits, int64_t rows, int64_t vocab, 
  *  - dtype: CE_F32, CE_BF16 or CE_F16, the type of the logits and of their
  *    gradient. Everything else of a row is f32; row statistics, losses and
  *    the gradient are computed in f32 and a gradient is rounded once, at the
- *    end. Sums over rows carry at least 48 bits and are rounded once to f32.
+ *    end. Sums over rows carry at least 48 bits relative to their largest
+ *    partial sum and are rounded once to f32; a partial sum beyond f32 makes
+ *    them infinite, also where `scale` would bring the result back.
+ *  - f32 ends the range of a row's gradient factors too (scale, weight and 1 / T
+ *    together with the loss's own factor): beyond it the row's gradient is not
+ *    finite. A probability below 2^-126 relative to the row's largest counts
+ *    as 0.
  *  - temperature T > 0 (1e-6 <= T <= 1e6): the distribution of a row is
  *    softmax(x / T); gradients are with respect to x.
  *  - weights: [rows] f32, or NULL (every row counts 1). A row of weight 0 (a
  *    prompt or padding token) takes no part: its logits, its label and its
- *    other inputs may hold anything and are not read, its outputs are 0 and
- *    its gradient row is zeros.
+ *    other inputs may hold anything, its outputs are 0 and its gradient row is
+ *    zeros. Of such a row only the weight and the label are loaded (and the
+ *    label not used).
  *  - gradients are with respect to the scaled loss and are written to rows
  *    grad_stride elements apart (grad_stride >= vocab; columns vocab and up
  *    are not written). grad == logits (in place) is allowed when grad_stride
@@ -452,6 +459,9 @@ typedef struct ce_preference {
  *     hinge    l = max(0, 1 - z)
  *     squared  l = (h - margin - 1 / (2 beta))^2
  *     loss = scale * sum_p l_p
+ * h is formed in f64; sigmoid and hinge round z once to f32 and go on in f32, so
+ * the loss and the factor of a saturated pair carry a relative error of
+ * |z| 2^-24.
  *   offsets: [2 * pairs + 1] int64 on the device, non-decreasing, within
  *     [0, rows]. Rows in no sequence count as rows of weight 0. A sequence may
  *     be empty (L = 0). Nothing is read or written out of range whatever the

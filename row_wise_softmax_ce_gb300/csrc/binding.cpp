@@ -138,7 +138,9 @@ struct WithoutGil {
 };
 
 // Uninitialised device memory from PyTorch's allocator, without the dispatcher
-// (four to six outputs a call).
+// (four to six outputs a call: policy step 64 x 1000 11.5 -> 10.5 us on the
+// host). empty_cuda is not part of PyTorch's public interface; it is there, with
+// these arguments, in 2.9 and 2.11, and a version without it fails to compile.
 at::Tensor empty(const Logits &x, at::IntArrayRef sizes, at::ScalarType type) {
     return at::detail::empty_cuda(sizes, type, x.t.device(), std::nullopt);
 }

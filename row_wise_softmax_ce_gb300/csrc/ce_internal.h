@@ -140,7 +140,9 @@ cudaError_t launch_obj_rows(DType t, ObjMode mode, const ObjArgs &a, const Devic
 cudaError_t launch_policy_grad(DType t, const ObjArgs &a, const DeviceInfo &dev, cudaStream_t s);
 cudaError_t launch_join(const JoinArgs &j, const DeviceInfo &dev, cudaStream_t s);
 cudaError_t launch_preference_grad(DType t, const ObjArgs &a, const DeviceInfo &dev, cudaStream_t s);
-// *out = scale * sum of weights[i] * loss[i] (weights null: 1), summed in f64
+// *out = scale * sum of weights[i] * loss[i] (weights null: 1), summed as pairs of
+// f32 (hi, lo); f64 joins the last parts and applies the scale. Infinite once a
+// partial sum passes f32, whatever the scale.
 cudaError_t launch_weighted_sum(const float *loss, const float *weights, int64_t rows, double scale, float *out,
                                 cudaStream_t s);
 // nothing to read or reset on a device that has launched no objective

@@ -770,6 +770,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(JoinArgs j) {
                 loss = static_cast<float>(off * off);
                 dh = static_cast<float>(2.0 * off);
             } else {
+                // f32 from here on, a relative error of |z| 2^-24: exp and log1p of one
+                // thread in f64 make a step of 4 pairs x 1000 take 10.9 us, not 9.2
                 const float z = static_cast<float>(j.beta * h - j.margin), beta = static_cast<float>(j.beta);
                 if (j.kind == 1) {
                     // NaN z: NaN, not the 0 of fmaxf
@@ -1111,6 +1113,14 @@ static int64_t staged_smem(DType t, int cols) {
 // at 2, 79.9 at 1 against 626, 256, 78; clusters persistent over rows, each
 // row's copy issued behind the last one's write, 651 -> 675 at 10, 256 -> 276 at
 // 2, 78 -> 91 at 2: the hardware's own scheduling balances better.)
+// Those are three vocabularies, and the rule was fitted to them. Where one, two
+// or three wide slices just fill an SM it prefers them to five narrow ones, and
+// loses (TB/s of logits and gradient, about 1.5 GB of logits, CTAs per SM in
+// brackets): f32 57344 6.07 (1) beside 58400 7.02, 114688 5.95 (1) beside 116000
+// 7.01, 172000 5.26 (1) beside 173500 6.66, 248320 6.16 (2), 256000 5.68 (3);
+// bf16 114688 5.17 (1) beside 116000 6.86, 56000 6.57 (2) beside 57344 6.94,
+// 145152 6.64 (3) beside 148000 6.79; 28000 and 28800 f32 6.97 and 7.02, 73600
+// and 75000 bf16 6.89 and 6.90 alike.
 // With few rows a row is split further, like a forward row.
 static int staged_split(DType t, int64_t rows, int64_t vocab, const DeviceInfo &dev) {
     constexpr int64_t kPerSm = 228 * 1024, kReserved = 1024;
