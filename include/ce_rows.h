@@ -461,7 +461,7 @@ typedef struct ce_preference {
  *     loss = scale * sum_p l_p
  * h is formed in f64; sigmoid and hinge round z once to f32 and go on in f32, so
  * the loss and the factor of a saturated pair carry a relative error of
- * |z| 2^-24.
+ * |z| 2^-24. Where l has a zero, l near it carries h's absolute error.
  *   offsets: [2 * pairs + 1] int64 on the device, non-decreasing, within
  *     [0, rows]. Rows in no sequence count as rows of weight 0. A sequence may
  *     be empty (L = 0). Nothing is read or written out of range whatever the

@@ -825,7 +825,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_join(JoinArgs j) {
 // k_pair_grad: factor ([y] - p) of every row, a CTA per part of kPartBytes of
 // a row. Rows whose factor is 0 (no weight, or in no sequence) are written as
 // zeros without being read. HBM-bound: 1400 rows of 128256 bf16, 3/4 of them
-// read, 92 us, 6.8 TB/s. 3000 rows' whole step with 256 threads x 4 vectors in
+// read, 90-92 us, 6.8-7.0 TB/s. 3000 rows' whole step with 256 threads x 4 vectors in
 // flight 293 us, x 1 297, 128 x 4 296, parts of 64 KB 297.
 constexpr int kPartBytes = 32768;
 constexpr int kPairThreads = 256;
