@@ -216,3 +216,38 @@ def test_rows_that_fill_a_cluster(dtype, vocab):
     want = R.policy64(x, y, old, adv, 64.0, entropy_coef=0.01)
     got = ce.policy_step(x, y, old, adv, 64.0, entropy_coef=0.01, entropy=True)
     check(dict(zip(("grad", "loss", "loss_rows", "logp", "entropy"), got)), want, f"{vocab}")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("vocab", [1000, 33001])
+@pytest.mark.parametrize("T", [1e-6, 1e-3, 1e3, 1e6])
+def test_far_temperatures(dtype, vocab, T):
+    """Log-probabilities, entropies, the policy loss with its KL term and the
+    preference step over the accepted temperatures, beside masked columns. Labels
+    on the row's largest logit (elsewhere (x - m) / T leaves f32's bounds of first
+    order) and, from T = 1e3, anywhere."""
+    rows = 40
+    x, g = logits_at(rows, vocab, vocab + 3, dtype, seed=vocab + 5)
+    x[::3, torch.rand(vocab, generator=g, device=DEV) < 0.5] = -math.inf
+    x[1::3, torch.rand(vocab, generator=g, device=DEV) < 0.5] = torch.finfo(dtype).min
+    y = x.float().argmax(1)
+    if T > 1:
+        other = torch.randint(0, vocab, (rows,), generator=g, device=DEV)
+        kept = x.gather(1, other[:, None])[:, 0] > torch.finfo(dtype).min / 2
+        y = torch.where(kept, other, y)
+    w = torch.rand(rows, generator=g, device=DEV) + 0.5
+    w[::7] = 0.0
+    want = R.logp64(x, y, w, T)
+    logp, ent = ce.logp_rows(x, y, weights=w, temperature=T, entropy=True)
+    check({"logp": logp, "entropy": ent}, want, "logp_rows")
+    assert torch.equal(ce.logp_rows(x, y, weights=w, temperature=T), logp)
+    old = want["logp"][0].float()
+    adv, ref = torch.randn(rows, generator=g, device=DEV), old + 0.1
+    want = R.policy64(x, y, old, adv, T, ref=ref, weights=w, kl_coef=0.1, temperature=T)
+    step = ce.policy_step(x, y, old, adv, T, ref_logp=ref, weights=w, kl_coef=0.1, temperature=T)
+    check(dict(zip(("grad", "loss", "loss_rows", "logp"), step)), wider(want, T, T, adv.abs() + 1, 0.0), "policy")
+    ends = [0, 9, 20, 31, 40]
+    want = R.preference64(x, y, ends, T, weights=w, temperature=T, beta=0.2)
+    got = ce.preference_step(x, y, torch.tensor(ends, device=DEV), T, weights=w, temperature=T, beta=0.2)
+    check(dict(zip(("grad", "loss", "loss_pairs", "seq_logp", "logp"), got)),
+          wider(want, T, T, torch.ones(rows, device=DEV), 0.0), "preference")
