@@ -153,8 +153,10 @@ ce_stream_t stream_of(const Logits &x) {
 // Tells autograd that a call wrote to a tensor of the caller's, as an in-place
 // operation of PyTorch does: a backward pass that saved it raises an error
 // instead of reading what is there now. Inference tensors keep no version.
+// `given` is a tensor that was checked, or None, True or False (a tensor check of
+// those goes through Python's isinstance).
 void written(int status, PyObject *given) {
-    if (status != CE_OK || !THPVariable_Check(given)) return;
+    if (status != CE_OK || given == Py_None || given == Py_True || given == Py_False) return;
     const at::Tensor &t = THPVariable_Unpack(given);
     if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
