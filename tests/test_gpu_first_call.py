@@ -64,8 +64,7 @@ def run(program):
 
 def test_first_row_losses():
     """With the counters read: 1.0 ms without the objectives' kernels, 11.4 ms
-    with all of them loaded beside; the best of a few processes, on a box that
-    others use too."""
+    with all of them loaded beside; the best of a few processes."""
     times = []
     while len(times) < 4 and min(times, default=1e9) > 4.0:
         times.append(float(run(TIMED)))
