@@ -5,7 +5,9 @@
  * language model's step reads from the same logits (softmax, log-softmax,
  * sampling candidates) and the join of split partial sums; and the objectives
  * over sampled answers and pairs of answers (token log-probabilities, the
- * clipped policy loss, the preference loss), each with its gradient.
+ * clipped policy loss, the preference loss), each with its gradient; and the
+ * choices made from a row's softmax (sampled tokens, the verification of
+ * drafted ones, the routing of rows to experts, with its gradient).
  *
  * Definitions follow the API reference page "gizml:netops"
  * (gizstack.com/docs/reference/gizml/netops.md), section Functions:
@@ -494,6 +496,136 @@ CE_API int preference_step(const void *logits, int dtype, int64_t rows, int64_t 
                            float *logp, float *seq_logp, float *loss_pairs, float *loss, void *work,
                            ce_stream_t stream);
 
+/*
+ * The choices made from a row's softmax.
+ *
+ *  - Logits are CE_F32, CE_BF16 or CE_F16, rows as above; arithmetic is f32,
+ *    sums over a row of 32 bits or more.
+ *  - The random numbers are inputs: f32 in [0, 1); a number outside counts as
+ *    the nearest inside, NaN as 0.
+ *  - Tokens and experts are int64; -1: none. Of equal columns the lowest wins.
+ *  - A row holding a NaN or +inf, or nothing above -inf, is no distribution:
+ *    its token is -1 and its log-probability NaN, and the device counter
+ *    (ce_device_error_count) is incremented. -inf logits of other rows are
+ *    never drawn.
+ *  - Outputs and the work buffer share no byte with an input or with one
+ *    another (CE_EINVAL); they may lie in the padding of the logits' rows.
+ *  - The calls keep nothing between them and are safe side by side on several
+ *    streams, given each its own outputs and work buffer.
+ */
+
+/*
+ * sample_rows: a token drawn from each row's softmax at a temperature. With
+ * e_j = exp((x_j - m) / T), m = max_j x_j and S = sum_j e_j, row i's token is
+ *     the first k with e_0 + ... + e_k > u_i S
+ * (columns in order; e_j below 2^-126 counts as 0). T = 0 is the row's argmax.
+ * Where u_i S lies within the rounding of a border between two columns (a few
+ * 2^-24 of S) either may be taken; the same call gives the same tokens always.
+ *   uniforms: [rows] f32, the u_i.
+ *   temperature: 0, or in [1e-6, 1e6].   temperatures: [rows] f32, likewise,
+ *     instead of it, or NULL; a row whose entry is neither counts as no
+ *     distribution.
+ *   tokens: [rows] int64.   logp: [rows] f32, or NULL: the token's
+ *     log-probability at that temperature (0 for T = 0), as logp_rows gives it.
+ */
+CE_API int sample_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,
+                       const float *uniforms, double temperature, const float *temperatures, int64_t *tokens,
+                       float *logp, ce_stream_t stream);
+
+/*
+ * verify_drafts: drafted tokens accepted or replaced so that what a request
+ * emits is distributed as if every token had been drawn from the target model.
+ * Request s is rows offsets[s] .. offsets[s + 1] - 1. With p and q the softmax
+ * of a row and of its draft row at the row's temperature, (a, u) its two random
+ * numbers and d its draft:
+ *     d is accepted where a q_d < p_d;
+ *     otherwise a token is drawn by u, as sample_rows draws it, from
+ *     max(0, p_j - q_j) in proportion.
+ * A request emits its accepted drafts, row by row, up to the first row that
+ * accepts none, and that row's drawn token. A row without a draft draws from p:
+ * the row behind the last draft of a request has none. A row at temperature 0
+ * draws its argmax and accepts a draft that is it.
+ *   drafts: [rows] int64; negative: the row has none (its draft row is not
+ *     read). A draft of vocab or more is counted and taken for none.
+ *   draft_logits: the logits that the drafts were drawn from, of the logits'
+ *     type, row i at draft_logits + i * draft_stride; NULL: the drafts were
+ *     looked up, not drawn, and q is 1 at d. A draft row that is no distribution
+ *     is counted, its draft not accepted and the token drawn from p; so is the
+ *     token where no column has p_j > q_j.
+ *   offsets: [requests + 1] int64 on the device, non-decreasing, within
+ *     [0, rows]. A request may have no rows. Nothing is read or written out of
+ *     range whatever the table holds: a range that is not valid is counted and
+ *     its request's `accepted` is -1; the tokens of rows that such a table leaves
+ *     to no request or gives to several are not specified.
+ *   uniforms: [rows, 2] f32, the pairs (a, u).   temperature, temperatures: as
+ *     in sample_rows.
+ *   accepted: [requests] int64, the drafts accepted.
+ *   tokens: [rows] int64, what the row emits; -1 for a row behind the request's
+ *     last, and for rows in no request.   logp: [rows] f32, or NULL: the
+ *     token's log-probability under p (0 at temperature 0 and where none is
+ *     emitted).
+ *   work: rows bytes of scratch; two calls that may run at the same time need
+ *     one each.
+ */
+CE_API int verify_drafts(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,
+                         const int64_t *drafts, const void *draft_logits, int64_t draft_stride,
+                         const int64_t *offsets, int64_t requests, const float *uniforms, double temperature,
+                         const float *temperatures, int64_t *accepted, int64_t *tokens, float *logp, void *work,
+                         ce_stream_t stream);
+
+enum ce_route_score { CE_ROUTE_SOFTMAX = 0, CE_ROUTE_SIGMOID = 1 };
+
+/* A router: the scores, experts per row k (1..32), the experts' groups (1..32,
+ * a divisor of the experts), how many of them a row keeps (top_groups), by the
+ * sum of how many of their best members (group_top: 1 or 2); whether the gates
+ * are renormalised, and their scale (finite). */
+typedef struct ce_route {
+    int score, k, groups, top_groups, group_top, renormalise;
+    double scale;
+} ce_route;
+
+/*
+ * route_rows: each row's experts and gates, from router logits [rows, experts],
+ * experts <= 1024. With the scores s = softmax(x) or sigma(x) and c = s + bias:
+ *     a row keeps the top_groups groups with the largest sum of their group_top
+ *     best c (top_groups == groups: all), and of their experts the k best c,
+ *     best first;
+ *     gate = scale s_e, or renormalised scale s_e / (sum of the chosen's s).
+ * The bias has a part in the choice only. An expert whose logit is -inf (or
+ * whose c is NaN or -inf) is never chosen and counts for nothing in its group; a
+ * slot that no expert is left for is -1 with a gate of 0. A row holding a NaN or
+ * +inf has no experts and NaN gates, and is counted. Scores that differ by less
+ * than their rounding may change places, in the groups' sums those below 2^-126
+ * of the row's largest.
+ *   bias: [experts] f32, or NULL.   weights: [rows] f32, or NULL; a row of
+ *     weight 0 is padding: not read, no experts, gates of 0. Other weights all
+ *     mean the same.
+ *   chosen: [rows, k] int64.   gates: [rows, k] f32.
+ *   counts: [experts] int64, or NULL: the rows that chose each expert.
+ */
+CE_API int route_rows(const void *logits, int dtype, int64_t rows, int64_t experts, int64_t stride,
+                      const ce_route *route, const float *bias, const float *weights, int64_t *chosen, float *gates,
+                      int64_t *counts, ce_stream_t stream);
+
+/*
+ * route_grad: the gradient of route_rows' gates with respect to the logits, for
+ * a given choice of experts: with G = scale * gates_grad, c the chosen, f their
+ * share of the sum of their scores and D = sum of f G,
+ *     renormalised  softmax  grad_c = f (G - D);  sigma  f (G - D) (1 - s_c)
+ *     otherwise     softmax  grad_j = s_j ([j chosen] G - sum of s_c G_c)
+ *                   sigma    grad_c = s_c (1 - s_c) G
+ * and 0 elsewhere, in the logits' type. An expert that a row names twice counts
+ * twice. Groups and bias have no part in it (route's are not read); rows of
+ * weight 0 and rows without experts get zeros.
+ *   chosen: [rows, k] int64; -1: none; one outside [-1, experts) is counted and
+ *     taken for none.   gates_grad: [rows, k] f32.
+ *   grad: rows grad_stride >= experts apart; grad == logits (in place) is
+ *     allowed when grad_stride == stride (or rows == 1).
+ */
+CE_API int route_grad(const void *logits, int dtype, int64_t rows, int64_t experts, int64_t stride,
+                      const ce_route *route, const float *weights, const int64_t *chosen, const float *gates_grad,
+                      void *grad, int64_t grad_stride, ce_stream_t stream);
+
 /* Human-readable text of a status code (a static string). */
 CE_API const char *ce_status_string(int status);
 
@@ -505,8 +637,8 @@ CE_API int ce_last_cuda_error(void);
 
 /*
  * Device-side error counter of the current device, for tests and
- * diagnostics: *out = rows seen with a label outside [0, vocab), and bad
- * sequence ranges, since the last reset. This call WAITS for `stream` to
+ * diagnostics: *out = rows seen with a label outside [0, vocab), bad
+ * sequence ranges, and what the choices above count, since the last reset. This call WAITS for `stream` to
  * finish.
  */
 CE_API int ce_device_error_count(ce_stream_t stream, int64_t *out);

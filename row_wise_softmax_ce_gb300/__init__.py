@@ -4,8 +4,8 @@ GB300 (sm_103a).
 A thin binding over the C ABI of ``libcerows.so`` (declared in
 ``include/ce_rows.h``): each function checks the tensors it is given,
 passes their device pointers and the current CUDA stream to the entry point
-of the same name (the objectives' functions from C++, ``_binding.so``), and
-returns. Every step of the computation runs in the
+of the same name (the objectives' and the choices' functions from C++,
+``_binding.so``), and returns. Every step of the computation runs in the
 library's CUDA kernels; there is no other implementation to fall back to, so
 a missing library is an error.
 
@@ -42,6 +42,14 @@ may also be bfloat16 or float16 (formulas in ``include/ce_rows.h``):
 - ``preference_loss`` / ``preference_step``  the loss of pairs of sequences
                    (sigmoid, hinge, squared), and its gradient
 
+and the choices made from a row's softmax, of the same types, the random numbers
+given:
+
+- ``sample_rows``  a token drawn from each row at a temperature
+- ``verify_drafts``  drafted tokens accepted or replaced, request by request
+- ``route_rows`` / ``route_grad``  each row's experts and gates (softmax or sigmoid
+                   scores, a bias for balance, groups, top k), and the gates' gradient
+
 Logits are a CUDA float32 tensor ``[rows, cols]`` whose rows are contiguous
 (``stride(1) == 1``); its row stride ``stride(0)`` may exceed ``vocab``
 (padded rows), and ``vocab`` defaults to ``cols``. Labels are int64 ``[rows]``.
@@ -65,6 +73,8 @@ PATH_AUTO, PATH_STAGED, PATH_STREAM, PATH_STAGED_PER_ROW, PATH_FLAT, PATH_WARP, 
 OP_ROWS, OP_GRAD, OP_ARGMAX, OP_SOFTMAX, OP_LOG_SOFTMAX, OP_CANDIDATES = 0, 1, 2, 3, 4, 5
 # kinds of preference loss (enum ce_preference_kind)
 PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "squared": 2}
+# a router's scores (enum ce_route_score)
+ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
 # candidatesInto's workgroup, TOP_EACH and CANDIDATE_ROW (gizml:netops, Constants)
 CANDIDATE_THREADS, TOP_EACH, CANDIDATE_ROW = 256, 4, 2048
 
@@ -83,6 +93,12 @@ class Preference(ctypes.Structure):
     """struct ce_preference"""
     _fields_ = [(n, ctypes.c_double) for n in ("scale", "temperature", "beta", "label_smoothing", "margin")] + \
                [(n, ctypes.c_int) for n in ("kind", "average")]
+
+
+class Route(ctypes.Structure):
+    """struct ce_route"""
+    _fields_ = [(n, ctypes.c_int) for n in ("score", "k", "groups", "top_groups", "group_top", "renormalise")] + \
+               [("scale", ctypes.c_double)]
 
 
 class CeError(RuntimeError):
@@ -130,6 +146,10 @@ def _bind(lib):
         "policy_step": [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp],
         "preference_loss": [vp, i32, i64, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp],
         "preference_step": [vp, i32, i64, i64, i64, vp, vp, vp, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp],
+        "sample_rows": [vp, i32, i64, i64, i64, vp, ctypes.c_double, vp, vp, vp, vp],
+        "verify_drafts": [vp, i32, i64, i64, i64, vp, vp, i64, vp, i64, vp, ctypes.c_double, vp, vp, vp, vp, vp, vp],
+        "route_rows": [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp],
+        "route_grad": [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, i64, vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -549,7 +569,7 @@ def _bound():
             try:
                 from . import _binding as module  # an extension module beside this file
             except ImportError as e:
-                raise RuntimeError("the objectives' binding _binding.so is missing or does not fit this PyTorch: build it "
+                raise RuntimeError("the binding _binding.so is missing or does not fit this PyTorch: build it "
                                    "with `python -m row_wise_softmax_ce_gb300.build` (or __graft_entry__.build())") from e
             _objectives = module
         return _objectives
@@ -636,6 +656,76 @@ def preference_step(logits: torch.Tensor, labels: torch.Tensor, offsets: torch.T
     return _done("preference_step", (_objectives or _bound()).preference(
         True, logits, labels, offsets, scale, ref_logp, weights, _kind(kind), beta, label_smoothing, margin, average,
         temperature, vocab, grad))
+
+
+# -- the choices made from a row's softmax -------------------------------------------
+
+def sample_rows(logits: torch.Tensor, uniforms: torch.Tensor, temperature: float | torch.Tensor = 1.0,
+                vocab: int | None = None, logp: bool | torch.Tensor = False, out: torch.Tensor | None = None):
+    """A token drawn from softmax(logits / temperature) of each row, int64
+    ``[rows]``: the first column whose running sum of probabilities passes the
+    row's number in ``uniforms`` (f32 ``[rows]``, in [0, 1)). ``temperature``: a
+    number, or f32 ``[rows]``; 0 takes the argmax. With ``logp`` (True or a tensor)
+    the pair ``(tokens, logp)``, the tokens' log-probabilities at that temperature
+    (0 at temperature 0). A row that is no distribution gives -1."""
+    got = _done("sample_rows", (_objectives or _bound()).sample(logits, uniforms, temperature, vocab, logp, out))
+    return got if got[1] is not None else got[0]
+
+
+def verify_drafts(logits: torch.Tensor, drafts: torch.Tensor, offsets: torch.Tensor, uniforms: torch.Tensor,
+                  draft_logits: torch.Tensor | None = None, temperature: float | torch.Tensor = 1.0,
+                  vocab: int | None = None, logp: bool | torch.Tensor = False):
+    """Drafted tokens accepted or replaced so that what is emitted follows the
+    target's ``logits``: rows ``offsets[s]:offsets[s + 1]`` are request s
+    (``offsets`` int64 ``[requests + 1]`` on the device), ``drafts`` int64
+    ``[rows]`` the token each row is to accept, negative for none (the row behind
+    a request's last draft), ``draft_logits`` the logits that they were drawn
+    from, row by row, in the logits' type; None: they were looked up.
+    ``uniforms`` f32 ``[rows, 2]``: the number that accepts and the one that draws.
+    A row accepts where ``uniforms[0] * q < p``; a request emits its accepted
+    drafts and, at the first row that accepts none, a token drawn from the rest,
+    max(0, p - q), or from p where there is no draft. ``temperature`` as in
+    ``sample_rows``. Returns ``(accepted, tokens, logp)``: int64 ``[requests]``,
+    int64 ``[rows]`` (-1 where nothing is emitted), and with ``logp`` the tokens'
+    log-probabilities under the target, f32 ``[rows]``, else None. Request s's
+    last token is ``tokens[offsets[s] + accepted[s]]``."""
+    return _done("verify_drafts", (_objectives or _bound()).verify(
+        logits, drafts, offsets, uniforms, draft_logits, temperature, vocab, logp))
+
+
+def _score(score: str) -> int:
+    if score not in ROUTE_SCORES:
+        raise ValueError(f"score must be one of {sorted(ROUTE_SCORES)}")
+    return ROUTE_SCORES[score]
+
+
+def route_rows(logits: torch.Tensor, k: int, score: str = "softmax", bias: torch.Tensor | None = None,
+               groups: int = 1, top_groups: int | None = None, group_top: int = 2, renormalise: bool = True,
+               scale: float = 1.0, weights: torch.Tensor | None = None, counts: bool = False):
+    """Each row's k experts, best first, and their gates, from router logits
+    ``[rows, experts]`` (at most 1024 experts, k at most 32). The scores are
+    softmax(logits) or sigmoid(logits); ``bias`` (f32 ``[experts]``) is added for
+    the choice only. With ``groups``, only experts of the ``top_groups`` groups
+    with the largest sum of their ``group_top`` (1 or 2) best count. Gates are the
+    scores, renormalised to a sum of 1 unless told otherwise, times ``scale``.
+    Returns ``(chosen, gates, counts)``: int64 ``[rows, k]`` (-1: no expert left),
+    f32 ``[rows, k]``, and with ``counts`` int64 ``[experts]``, the rows that chose
+    each expert, else None. ``weights`` (f32 ``[rows]``): rows of weight 0 are
+    padding and choose nothing."""
+    return _done("route_rows", (_objectives or _bound()).route(
+        logits, k, _score(score), bias, groups, groups if top_groups is None else top_groups, group_top, renormalise,
+        scale, weights, counts))
+
+
+def route_grad(logits: torch.Tensor, chosen: torch.Tensor, gates_grad: torch.Tensor, score: str = "softmax",
+               renormalise: bool = True, scale: float = 1.0, weights: torch.Tensor | None = None,
+               grad: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of ``route_rows``' gates with respect to the logits, in their
+    type, from ``chosen`` (its choice; -1: none) and ``gates_grad``, f32 ``[rows,
+    k]``; ``score``, ``renormalise``, ``scale`` and ``weights`` as given there.
+    ``grad`` as in ``policy_step``."""
+    return _done("route_grad", (_objectives or _bound()).route_grad(
+        logits, chosen, gates_grad, _score(score), renormalise, scale, weights, grad))[0]
 
 
 # -- diagnostics and tuning ---------------------------------------------------

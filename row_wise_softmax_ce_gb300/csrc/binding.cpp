@@ -1,4 +1,4 @@
-// binding.cpp -- the objectives' calls for PyTorch tensors: the checks, the
+// binding.cpp -- the objectives' and the choices' calls for PyTorch tensors: the checks, the
 // outputs and the current stream, then the C ABI of libcerows.so. Marshalling
 // only, as the ctypes functions beside it are; it exists because these calls are
 // also made on batches whose kernels take a few microseconds, where checking
@@ -283,6 +283,155 @@ PyObject *preference(PyObject *const *a) {
     return step ? result(st, {grad, loss, pair_losses, seq, lp}) : result(st, {loss, pair_losses, seq, lp});
 }
 
+// -- the choices made from a row's softmax
+
+// A contiguous tensor of the given type and sizes on the logits' device.
+const at::Tensor &shaped(PyObject *o, at::ScalarType type, const char *type_name, at::IntArrayRef sizes, const Logits &x,
+                         const char *name) {
+    const at::Tensor &t = tensor(o, name);
+    if (t.scalar_type() != type || t.sizes() != sizes || t.device() != x.t.device() || !t.is_contiguous()) {
+        std::string shape;
+        for (int64_t n : sizes) shape += (shape.empty() ? "" : ", ") + std::to_string(n);
+        value_error(std::string(name) + " must be a contiguous " + type_name + " tensor [" + shape + "] on " +
+                    where(x.t.device()));
+    }
+    return t;
+}
+
+// A temperature: a number, or an f32 tensor with one for every row.
+struct Temperature {
+    double all = 1.0;
+    const float *rows = nullptr;
+};
+Temperature temperature_of(PyObject *o, const Logits &x) {
+    if (!THPVariable_Check(o)) return {number(o), nullptr};
+    return {1.0, f32_of(o, x.rows, x, "temperature")};
+}
+
+at::Tensor i64(const Logits &x, at::IntArrayRef sizes) { return empty(x, sizes, at::kLong); }
+int64_t *longs(const at::Tensor &t) { return t.defined() ? static_cast<int64_t *>(t.data_ptr()) : nullptr; }
+
+// sample(logits, uniforms, temperature, vocab, logp, out)
+PyObject *sample(PyObject *const *a) {
+    const Logits x = logits_of(a[0], a[3]);
+    const float *u = shaped(a[1], at::kFloat, "float32", {x.rows}, x, "uniforms").const_data_ptr<float>();
+    const Temperature t = temperature_of(a[2], x);
+    Wanted lp = wanted(a[4], x, "logp");
+    at::Tensor out;
+    if (a[5] != Py_None) out = shaped(a[5], at::kLong, "int64", {x.rows}, x, "out");
+    int st;
+    {
+        WithoutGil nogil;
+        c10::cuda::CUDAGuard guard(x.t.device());
+        if (!out.defined()) out = i64(x, {x.rows});
+        if (lp.any && !lp.t.defined()) lp.t = f32(x, {x.rows});
+        st = sample_rows(x.t.data_ptr(), x.dtype, x.rows, x.vocab, x.stride, u, t.all, t.rows, longs(out), data(lp.t),
+                         stream_of(x));
+    }
+    written(st, a[4]);
+    written(st, a[5]);
+    return result(st, {out, lp.t});
+}
+
+// verify(logits, drafts, offsets, uniforms, draft_logits, temperature, vocab, logp)
+PyObject *verify(PyObject *const *a) {
+    const Logits x = logits_of(a[0], a[6]);
+    const int64_t *drafts = shaped(a[1], at::kLong, "int64", {x.rows}, x, "drafts").const_data_ptr<int64_t>();
+    const at::Tensor &offsets = tensor(a[2], "offsets");
+    if (offsets.scalar_type() != at::kLong || offsets.dim() != 1 || offsets.size(0) < 1 ||
+        offsets.device() != x.t.device() || !offsets.is_contiguous())
+        value_error("offsets must be a contiguous int64 tensor [requests + 1] on the logits' device");
+    const int64_t requests = offsets.size(0) - 1;
+    const float *u = shaped(a[3], at::kFloat, "float32", {x.rows, 2}, x, "uniforms").const_data_ptr<float>();
+    const void *draft_logits = nullptr;
+    int64_t draft_stride = 0;
+    if (a[4] != Py_None) {
+        const at::Tensor &q = tensor(a[4], "draft_logits");
+        if (q.scalar_type() != x.t.scalar_type() || q.device() != x.t.device() || q.dim() != 2 || q.size(0) != x.rows ||
+            q.size(1) < x.vocab || (x.rows > 0 && q.size(1) > 1 && q.stride(1) != 1))
+            value_error("draft_logits must be a tensor of the logits' type, [rows=" + std::to_string(x.rows) + ", >= " +
+                        std::to_string(x.vocab) + "] with contiguous rows, on " + where(x.t.device()));
+        draft_logits = q.data_ptr();
+        draft_stride = x.rows > 1 ? q.stride(0) : x.vocab;
+        if (draft_stride < x.vocab) value_error("rows of draft_logits overlap (stride(0) < vocab)");
+    }
+    const Temperature t = temperature_of(a[5], x);
+    Wanted lp = wanted(a[7], x, "logp");
+    at::Tensor accepted, tokens, work;
+    int st;
+    {
+        WithoutGil nogil;
+        c10::cuda::CUDAGuard guard(x.t.device());
+        accepted = i64(x, {requests});
+        tokens = i64(x, {x.rows});
+        work = empty(x, {x.rows}, at::kByte);
+        if (lp.any && !lp.t.defined()) lp.t = f32(x, {x.rows});
+        st = verify_drafts(x.t.data_ptr(), x.dtype, x.rows, x.vocab, x.stride, drafts, draft_logits, draft_stride,
+                           offsets.const_data_ptr<int64_t>(), requests, u, t.all, t.rows, longs(accepted),
+                           longs(tokens), data(lp.t), work.data_ptr(), stream_of(x));
+    }
+    written(st, a[7]);
+    return result(st, {accepted, tokens, lp.t});
+}
+
+int int_of(PyObject *o) {
+    const long v = PyLong_AsLong(o);
+    if (v == -1 && PyErr_Occurred()) throw Raised{};
+    return v < INT32_MIN ? INT32_MIN : v > INT32_MAX ? INT32_MAX : static_cast<int>(v);
+}
+
+bool truth_of(PyObject *o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw Raised{};
+    return v != 0;
+}
+
+// route(logits, k, score, bias, groups, top_groups, group_top, renormalise, scale, weights, counts)
+PyObject *route(PyObject *const *a) {
+    const Logits x = logits_of(a[0], Py_None);
+    const ce_route par = {int_of(a[2]), int_of(a[1]), int_of(a[4]), int_of(a[5]), int_of(a[6]), truth_of(a[7]), number(a[8])};
+    const float *bias = f32_of(a[3], x.vocab, x, "bias"), *w = f32_of(a[9], x.rows, x, "weights");
+    const bool count = truth_of(a[10]);
+    const int64_t k = par.k > 0 && par.k <= x.vocab ? par.k : 0;  // else refused
+    at::Tensor chosen, gates, counts;
+    int st;
+    {
+        WithoutGil nogil;
+        c10::cuda::CUDAGuard guard(x.t.device());
+        chosen = i64(x, {x.rows, k});
+        gates = f32(x, {x.rows, k});
+        if (count) counts = i64(x, {x.vocab});
+        st = route_rows(x.t.data_ptr(), x.dtype, x.rows, x.vocab, x.stride, &par, bias, w, longs(chosen), data(gates),
+                        longs(counts), stream_of(x));
+    }
+    return result(st, {chosen, gates, counts});
+}
+
+// route_grad(logits, chosen, gates_grad, score, renormalise, scale, weights, grad)
+PyObject *route_gradient(PyObject *const *a) {
+    const Logits x = logits_of(a[0], Py_None);
+    const at::Tensor &c = tensor(a[1], "chosen");
+    if (c.dim() != 2) value_error("chosen must be int64 [rows, k]");
+    const int64_t k = c.size(1);
+    const int64_t *chosen = shaped(a[1], at::kLong, "int64", {x.rows, k}, x, "chosen").const_data_ptr<int64_t>();
+    const float *g = shaped(a[2], at::kFloat, "float32", {x.rows, k}, x, "gates_grad").const_data_ptr<float>();
+    const ce_route par = {int_of(a[3]), static_cast<int>(k > 1024 ? 1025 : k), 1, 1, 1, truth_of(a[4]), number(a[5])};
+    const float *w = f32_of(a[6], x.rows, x, "weights");
+    at::Tensor grad;
+    int64_t grad_stride = 0;
+    check_grad(a[7], x, &grad, &grad_stride);
+    int st;
+    {
+        WithoutGil nogil;
+        c10::cuda::CUDAGuard guard(x.t.device());
+        if (!grad.defined()) grad = empty(x, {x.rows, x.vocab}, x.t.scalar_type());
+        st = route_grad(x.t.data_ptr(), x.dtype, x.rows, x.vocab, x.stride, &par, w, chosen, g, grad.data_ptr(),
+                        grad_stride, stream_of(x));
+    }
+    written(st, a[7]);
+    return result(st, {grad});
+}
+
 // One entry point: the number of arguments, and every C++ exception as a Python error.
 template <PyObject *(*kFn)(PyObject *const *), Py_ssize_t kArgs>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -316,6 +465,10 @@ PyMethodDef methods[] = {
     {"logp_rows", fast<logp, 7>(), METH_FASTCALL, nullptr},
     {"policy", fast<policy, 16>(), METH_FASTCALL, nullptr},
     {"preference", fast<preference, 15>(), METH_FASTCALL, nullptr},
+    {"sample", fast<sample, 6>(), METH_FASTCALL, nullptr},
+    {"verify", fast<verify, 8>(), METH_FASTCALL, nullptr},
+    {"route", fast<route, 11>(), METH_FASTCALL, nullptr},
+    {"route_grad", fast<route_gradient, 8>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

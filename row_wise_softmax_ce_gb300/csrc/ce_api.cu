@@ -712,6 +712,11 @@ struct Bytes {
     int64_t n;
 };
 
+struct Rows {
+    const void *p;
+    int64_t rows, row_bytes, stride_bytes;
+};
+
 // Do `rows` rows of row_bytes, stride_bytes apart, and a flat array share a byte?
 // Not where the array lies in the rows' padding.
 static bool rows_meet(const void *base, int64_t rows, int64_t row_bytes, int64_t stride_bytes, const Bytes &flat) {
@@ -896,6 +901,191 @@ int preference_step(const void *logits, int dtype, int64_t rows, int64_t vocab, 
                            true, grad, grad_stride, logp, seq_logp, loss_pairs, loss, work, stream);
 }
 
+// -- the choices made from a row's softmax -----------------------------------------
+
+// What every choice checks of its rows: `cols` columns of a row, at most `most`.
+static int check_choice_rows(const void *logits, int dtype, int64_t rows, int64_t cols, int64_t stride, int64_t most) {
+    if (dtype != CE_F32 && dtype != CE_BF16 && dtype != CE_F16) return CE_EINVAL;
+    if (rows < 0 || cols < 1 || cols > most || stride < cols) return CE_EINVAL;
+    if (rows > 0 && logits == nullptr) return CE_EINVAL;
+    if (rows > 0 && stride > (INT64_MAX / 4) / rows) return CE_EINVAL;  // byte offsets fit int64
+    return misaligned(logits, dtype == CE_F32 ? 4 : 2) ? CE_EALIGN : CE_OK;
+}
+
+static int64_t current_grid_cap() {
+    std::lock_guard<std::mutex> lock(g_mu);
+    return g_force.grid_cap;
+}
+
+// The outputs share no byte with the rows, with another input or with one another.
+static int check_outputs_apart(std::initializer_list<Rows> rows, std::initializer_list<Bytes> inputs,
+                               std::initializer_list<Bytes> outputs) {
+    for (const Bytes *o = outputs.begin(); o != outputs.end(); ++o) {
+        if (o->p == nullptr || o->n <= 0) continue;
+        for (const Rows &r : rows)
+            if (rows_meet(r.p, r.rows, r.row_bytes, r.stride_bytes, *o)) return CE_EINVAL;
+        for (const Bytes &i : inputs)
+            if (i.p != nullptr && i.n > 0 && ranges_overlap(o->p, o->n, i.p, i.n)) return CE_EINVAL;
+        for (const Bytes *q = o + 1; q != outputs.end(); ++q)
+            if (q->p != nullptr && q->n > 0 && ranges_overlap(o->p, o->n, q->p, q->n)) return CE_EINVAL;
+    }
+    return CE_OK;
+}
+
+static bool good_temperature(double t) { return t == 0.0 || (t >= 1e-6 && t <= 1e6); }
+
+int sample_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride, const float *uniforms,
+                double temperature, const float *temperatures, int64_t *tokens, float *logp, ce_stream_t stream) {
+    int st = check_choice_rows(logits, dtype, rows, vocab, stride, kMaxVocab);
+    if (st) return st;
+    if (!good_temperature(temperature)) return CE_EINVAL;
+    if (rows > 0 && (uniforms == nullptr || tokens == nullptr)) return CE_EINVAL;
+    if (misaligned(uniforms, 4) || misaligned(temperatures, 4) || misaligned(tokens, 8) || misaligned(logp, 4))
+        return CE_EALIGN;
+    if (rows == 0) return CE_OK;
+    const int64_t size = dtype == CE_F32 ? 4 : 2;
+    if ((st = check_outputs_apart({{logits, rows, vocab * size, stride * size}},
+                                  {{uniforms, 4 * rows}, {temperatures, 4 * rows}},
+                                  {{tokens, 8 * rows}, {logp, 4 * rows}})))
+        return st;
+    DeviceInfo dev;
+    if ((st = current_device(&dev))) return st;
+    ChoiceArgs a{};
+    a.logits = logits;
+    a.rows = rows;
+    a.vocab = static_cast<int>(vocab);
+    a.stride = stride;
+    a.temperature = static_cast<float>(temperature);
+    a.temperatures = temperatures;
+    a.uniforms = uniforms;
+    a.tokens = tokens;
+    a.logp = logp;
+    a.grid_cap = current_grid_cap();
+    return cuda_status(launch_sample(static_cast<DType>(dtype), a, dev, stream));
+}
+
+int verify_drafts(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride, const int64_t *drafts,
+                  const void *draft_logits, int64_t draft_stride, const int64_t *offsets, int64_t requests,
+                  const float *uniforms, double temperature, const float *temperatures, int64_t *accepted,
+                  int64_t *tokens, float *logp, void *work, ce_stream_t stream) {
+    int st = check_choice_rows(logits, dtype, rows, vocab, stride, kMaxVocab);
+    if (st) return st;
+    if (!good_temperature(temperature)) return CE_EINVAL;
+    if (draft_logits != nullptr && (st = check_choice_rows(draft_logits, dtype, rows, vocab, draft_stride, kMaxVocab)))
+        return st;
+    if (requests < 0 || requests > (int64_t(1) << 40) || offsets == nullptr) return CE_EINVAL;
+    if (requests > 0 && accepted == nullptr) return CE_EINVAL;
+    if (rows > 0 && (drafts == nullptr || uniforms == nullptr || tokens == nullptr || work == nullptr))
+        return CE_EINVAL;
+    if (misaligned(drafts, 8) || misaligned(offsets, 8) || misaligned(uniforms, 4) || misaligned(temperatures, 4) ||
+        misaligned(accepted, 8) || misaligned(tokens, 8) || misaligned(logp, 4))
+        return CE_EALIGN;
+    const int64_t size = dtype == CE_F32 ? 4 : 2;
+    if ((st = check_outputs_apart(
+             {{logits, rows, vocab * size, stride * size}, {draft_logits, rows, vocab * size, draft_stride * size}},
+             {{drafts, 8 * rows}, {offsets, 8 * (requests + 1)}, {uniforms, 8 * rows}, {temperatures, 4 * rows}},
+             {{accepted, 8 * requests}, {tokens, 8 * rows}, {logp, 4 * rows}, {work, rows}})))
+        return st;
+    if (rows == 0 && requests == 0) return CE_OK;
+    DeviceInfo dev;
+    if ((st = current_device(&dev))) return st;
+    ChoiceArgs a{};
+    a.logits = logits;
+    a.rows = rows;
+    a.vocab = static_cast<int>(vocab);
+    a.stride = stride;
+    a.temperature = static_cast<float>(temperature);
+    a.temperatures = temperatures;
+    a.uniforms = uniforms;
+    a.tokens = tokens;
+    a.logp = logp;
+    a.draft_logits = draft_logits;
+    a.draft_stride = draft_stride;
+    a.drafts = drafts;
+    a.offsets = offsets;
+    a.requests = requests;
+    a.accepted = accepted;
+    a.accepts = static_cast<uint8_t *>(work);
+    a.grid_cap = current_grid_cap();
+    return cuda_status(launch_verify(static_cast<DType>(dtype), a, dev, stream));
+}
+
+static int check_route(const void *logits, int dtype, int64_t rows, int64_t experts, int64_t stride,
+                       const ce_route *route, const float *weights, RouteArgs *a) {
+    if (route == nullptr) return CE_EINVAL;
+    int st = check_choice_rows(logits, dtype, rows, experts, stride, kMaxExperts);
+    if (st) return st;
+    if (route->score != CE_ROUTE_SOFTMAX && route->score != CE_ROUTE_SIGMOID) return CE_EINVAL;
+    if (route->k < 1 || route->k > kMaxChosen || route->k > experts || !std::isfinite(route->scale)) return CE_EINVAL;
+    if (misaligned(weights, 4)) return CE_EALIGN;
+    *a = RouteArgs{};
+    a->logits = logits;
+    a->rows = rows;
+    a->experts = static_cast<int>(experts);
+    a->stride = stride;
+    a->k = route->k;
+    a->groups = a->top_groups = a->group_top = 1;
+    a->sigmoid = route->score == CE_ROUTE_SIGMOID;
+    a->renormalise = route->renormalise != 0;
+    a->scale = static_cast<float>(route->scale);
+    a->weights = weights;
+    a->grid_cap = current_grid_cap();
+    return CE_OK;
+}
+
+int route_rows(const void *logits, int dtype, int64_t rows, int64_t experts, int64_t stride, const ce_route *route,
+               const float *bias, const float *weights, int64_t *chosen, float *gates, int64_t *counts,
+               ce_stream_t stream) {
+    RouteArgs a;
+    int st = check_route(logits, dtype, rows, experts, stride, route, weights, &a);
+    if (st) return st;
+    if (route->groups < 1 || route->groups > kMaxGroups || experts % route->groups != 0) return CE_EINVAL;
+    if (route->top_groups < 1 || route->top_groups > route->groups) return CE_EINVAL;
+    if (route->group_top != 1 && route->group_top != 2) return CE_EINVAL;
+    if (route->k > route->top_groups * (experts / route->groups)) return CE_EINVAL;
+    if (rows > 0 && (chosen == nullptr || gates == nullptr)) return CE_EINVAL;
+    if (misaligned(bias, 4) || misaligned(chosen, 8) || misaligned(gates, 4) || misaligned(counts, 8))
+        return CE_EALIGN;
+    const int64_t size = dtype == CE_F32 ? 4 : 2, slots = rows * route->k;
+    if ((st = check_outputs_apart({{logits, rows, experts * size, stride * size}},
+                                  {{bias, 4 * experts}, {weights, 4 * rows}},
+                                  {{chosen, 8 * slots}, {gates, 4 * slots}, {counts, 8 * experts}})))
+        return st;
+    if (rows == 0 && counts == nullptr) return CE_OK;
+    DeviceInfo dev;
+    if ((st = current_device(&dev))) return st;
+    a.groups = route->groups;
+    a.top_groups = route->top_groups;
+    a.group_top = route->group_top;
+    a.bias = bias;
+    a.chosen = chosen;
+    a.gates = gates;
+    a.counts = reinterpret_cast<unsigned long long *>(counts);
+    return cuda_status(launch_route(static_cast<DType>(dtype), a, dev, stream));
+}
+
+int route_grad(const void *logits, int dtype, int64_t rows, int64_t experts, int64_t stride, const ce_route *route,
+               const float *weights, const int64_t *chosen, const float *gates_grad, void *grad, int64_t grad_stride,
+               ce_stream_t stream) {
+    RouteArgs a;
+    int st = check_route(logits, dtype, rows, experts, stride, route, weights, &a);
+    if (st) return st;
+    if (rows > 0 && (chosen == nullptr || gates_grad == nullptr)) return CE_EINVAL;
+    if (misaligned(chosen, 8) || misaligned(gates_grad, 4)) return CE_EALIGN;
+    if ((st = check_objective_grad(logits, dtype, rows, experts, stride, grad, grad_stride))) return st;
+    const int64_t size = dtype == CE_F32 ? 4 : 2, slots = rows * route->k;
+    for (const Bytes &i : {Bytes{weights, 4 * rows}, Bytes{chosen, 8 * slots}, Bytes{gates_grad, 4 * slots}})
+        if (rows_meet(grad, rows, experts * size, grad_stride * size, i)) return CE_EINVAL;
+    if (rows == 0) return CE_OK;
+    DeviceInfo dev;
+    if ((st = current_device(&dev))) return st;
+    a.chosen = const_cast<int64_t *>(chosen);
+    a.gates_grad = gates_grad;
+    a.grad = grad;
+    a.grad_stride = grad_stride;
+    return cuda_status(launch_route_grad(static_cast<DType>(dtype), a, dev, stream));
+}
+
 const char *ce_status_string(int status) {
     switch (status) {
     case CE_OK: return "ok";
@@ -980,10 +1170,11 @@ static int read_counter(ce_stream_t stream, int which, int64_t *out) {
     DeviceInfo dev;
     int st = current_device(&dev);
     if (st) return st;
-    unsigned long long v[2] = {0ull, 0ull}, o[2] = {0ull, 0ull};
+    unsigned long long v[2] = {0ull, 0ull}, o[2] = {0ull, 0ull}, c[2] = {0ull, 0ull};
     if ((st = cuda_status(read_status(v, stream)))) return st;
     if ((st = cuda_status(read_objective_status(o, dev, stream)))) return st;
-    *out = static_cast<int64_t>(v[which] + o[which]);
+    if ((st = cuda_status(read_choice_status(c, dev, stream)))) return st;
+    *out = static_cast<int64_t>(v[which] + o[which] + c[which]);
     return CE_OK;
 }
 
@@ -996,7 +1187,8 @@ int ce_device_error_reset(ce_stream_t stream) {
     int st = current_device(&dev);
     if (st) return st;
     if ((st = cuda_status(reset_status(stream)))) return st;
-    return cuda_status(reset_objective_status(dev, stream));
+    if ((st = cuda_status(reset_objective_status(dev, stream)))) return st;
+    return cuda_status(reset_choice_status(dev, stream));
 }
 
 int ce_debug_force(int path, int cluster, int threads) {

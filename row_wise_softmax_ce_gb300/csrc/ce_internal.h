@@ -149,6 +149,61 @@ cudaError_t launch_weighted_sum(const float *loss, const float *weights, int64_t
 cudaError_t read_objective_status(unsigned long long out[2], const DeviceInfo &dev, cudaStream_t s);
 cudaError_t reset_objective_status(const DeviceInfo &dev, cudaStream_t s);
 
+// -- the choices made from a row's softmax (ce_choices.cu) -----------------------
+// Arguments of sample_rows and verify_drafts; unused pointers are null.
+struct ChoiceArgs {
+    const void *logits;
+    int64_t rows;
+    int vocab;
+    int64_t stride;
+    float temperature;          // 0: greedy
+    const float *temperatures;  // [rows], or null: `temperature` for every row
+    const float *uniforms;      // [rows], of a verification [rows, 2]: accept, draw
+    int64_t *tokens;            // [rows]
+    float *logp;                // [rows] or null
+    // verification: request s is rows offsets[s] .. offsets[s + 1] - 1
+    const void *draft_logits;  // null: the drafts were not drawn by a model
+    int64_t draft_stride;
+    const int64_t *drafts;  // [rows], negative: none
+    const int64_t *offsets;
+    int64_t requests;
+    int64_t *accepted;  // [requests]
+    uint8_t *accepts;   // [rows] scratch
+    int64_t grid_cap;   // at most this many clusters (0: no cap)
+};
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxChosen = 32;  // experts of a row: a lane each
+constexpr int kMaxGroups = 32;  // a lane each
+
+// Arguments of route_rows and route_grad; unused pointers are null.
+struct RouteArgs {
+    const void *logits;
+    int64_t rows;
+    int experts;
+    int64_t stride;
+    int k, groups, top_groups, group_top;
+    bool sigmoid, renormalise;
+    float scale;
+    const float *bias;     // [experts]
+    const float *weights;  // [rows], 0: a padding row
+    int64_t *chosen;       // [rows, k]
+    float *gates;          // [rows, k]
+    unsigned long long *counts;  // [experts]
+    const float *gates_grad;     // [rows, k]
+    void *grad;
+    int64_t grad_stride;
+    int64_t grid_cap;
+};
+
+cudaError_t launch_sample(DType t, const ChoiceArgs &a, const DeviceInfo &dev, cudaStream_t s);
+cudaError_t launch_verify(DType t, const ChoiceArgs &a, const DeviceInfo &dev, cudaStream_t s);
+cudaError_t launch_route(DType t, const RouteArgs &a, const DeviceInfo &dev, cudaStream_t s);
+cudaError_t launch_route_grad(DType t, const RouteArgs &a, const DeviceInfo &dev, cudaStream_t s);
+// nothing to read or reset on a device that has launched no choice
+cudaError_t read_choice_status(unsigned long long out[2], const DeviceInfo &dev, cudaStream_t s);
+cudaError_t reset_choice_status(const DeviceInfo &dev, cudaStream_t s);
+
 cudaError_t set_kernel_attributes(const DeviceInfo &dev);
 cudaError_t max_active_clusters(const Plan &p, Op op, int *n);
 

@@ -19,10 +19,10 @@
 //   k_pair_grad      the gradient of a preference batch, the rows read again
 //   k_weighted_sum   the policy's loss, a fixed-shape tree of f32 pairs
 #include <algorithm>
-#include <atomic>
 #include <cstdint>
 
 #include "ce_internal.h"
+#include "ce_launch.h"
 #include "ce_objectives.cuh"
 
 namespace cerows {
@@ -904,64 +904,7 @@ __global__ void __launch_bounds__(kSumThreads) k_weighted_sum(const float *loss,
 // ---------------------------------------------------------------------------
 // launchers
 
-// cluster 0: a launch without cluster dimensions, for kernels that execute no
-// instruction on shared::cluster addresses (st.async is illegal there, to the
-// CTA's own shared memory too).
-struct LaunchConfig {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
-    LaunchConfig(int64_t ctas, int threads, int cluster, bool dependent, cudaStream_t s, int smem = 0) {
-        cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
-        cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
-        cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-        cfg.stream = s;
-        int n = 0;
-        if (cluster > 0) {
-            attr[n].id = cudaLaunchAttributeClusterDimension;
-            attr[n].val.clusterDim.x = static_cast<unsigned>(cluster);
-            attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
-            ++n;
-        }
-        if (dependent) {
-            attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-            attr[n].val.programmaticStreamSerializationAllowed = 1;
-            ++n;
-        }
-        cfg.attrs = attr;
-        cfg.numAttrs = n;
-    }
-};
-
-// Devices (a bit each) that have launched an objective. Touching a kernel or a
-// variable of this file loads all of its code, 10 ms once: no other function of
-// the library's does.
-std::atomic<uint64_t> g_launched{0};
-static_assert(kMaxDevices <= 64, "a bit per device");
-
-uint64_t bit_of(const DeviceInfo &dev) { return uint64_t(1) << dev.device; }
-bool launched(const DeviceInfo &dev) { return g_launched.load(std::memory_order_acquire) & bit_of(dev); }
-void launches(const DeviceInfo &dev) {
-    if (!launched(dev)) g_launched.fetch_or(bit_of(dev), std::memory_order_release);
-}
-
-// A kernel and the devices on which its attributes are set: clusters of up to 16
-// CTAs, and as much shared memory as a CTA may have. Set at the kernel's first
-// launch on a device.
-struct Kernel {
-    const void *fn;
-    bool smem;
-    std::atomic<uint64_t> set{0};
-    Kernel(const void *f, bool dynamic_smem) : fn(f), smem(dynamic_smem) {}
-};
-cudaError_t ready(Kernel &k, const DeviceInfo &dev) {
-    const uint64_t bit = bit_of(dev);
-    if (k.set.load(std::memory_order_acquire) & bit) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess && k.smem)
-        e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, dev.max_smem_optin);
-    if (e == cudaSuccess) k.set.fetch_or(bit, std::memory_order_release);
-    return e;
-}
+Launches g_launched;
 
 template <typename T, int kMode, bool kEnt>
 Kernel &rows_kernel_m(bool warp) {
@@ -1077,7 +1020,7 @@ int cols_of(int64_t vocab, int c) { return static_cast<int>(((vocab + c - 1) / c
 }  // namespace
 
 cudaError_t launch_obj_rows(DType t, ObjMode mode, const ObjArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-    launches(dev);
+    g_launched.note(dev);
     if (forward_warp(t, a.rows, a.vocab, dev)) {
         ObjArgs aa = a;
         void *args[] = {&aa};
@@ -1138,7 +1081,7 @@ static int staged_split(DType t, int64_t rows, int64_t vocab, const DeviceInfo &
 }
 
 cudaError_t launch_policy_grad(DType t, const ObjArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-    launches(dev);
+    g_launched.note(dev);
     const bool ent = wants_entropy(a);
     const int64_t clusters = capped(a.rows, a);
     ObjArgs aa = a;
@@ -1202,7 +1145,7 @@ cudaError_t launch_weighted_sum(const float *loss, const float *weights, int64_t
 
 cudaError_t read_objective_status(unsigned long long out[2], const DeviceInfo &dev, cudaStream_t s) {
     out[0] = out[1] = 0ull;
-    if (!launched(dev)) return cudaSuccess;
+    if (!g_launched.any(dev)) return cudaSuccess;
     cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_objective_status, sizeof(unsigned long long) * 2, 0,
                                               cudaMemcpyDeviceToHost, s);
     if (e != cudaSuccess) return e;
@@ -1210,7 +1153,7 @@ cudaError_t read_objective_status(unsigned long long out[2], const DeviceInfo &d
 }
 
 cudaError_t reset_objective_status(const DeviceInfo &dev, cudaStream_t s) {
-    if (!launched(dev)) return cudaSuccess;
+    if (!g_launched.any(dev)) return cudaSuccess;
     static const unsigned long long zero[2] = {0ull, 0ull};
     return cudaMemcpyToSymbolAsync(g_objective_status, zero, sizeof(zero), 0, cudaMemcpyHostToDevice, s);
 }
