@@ -499,8 +499,8 @@ CE_API int preference_step(const void *logits, int dtype, int64_t rows, int64_t 
 /*
  * The choices made from a row's softmax.
  *
- *  - Logits are CE_F32, CE_BF16 or CE_F16, rows as above; arithmetic is f32,
- *    sums over a row of 32 bits or more.
+ *  - Logits are CE_F32, CE_BF16 or CE_F16, rows as above, fewer than 2^31 of
+ *    them; arithmetic is f32, sums over a row of 32 bits or more.
  *  - The random numbers are inputs: f32 in [0, 1); a number outside counts as
  *    the nearest inside, NaN as 0.
  *  - Tokens and experts are int64; -1: none. Of equal columns the lowest wins.
@@ -515,6 +515,12 @@ CE_API int preference_step(const void *logits, int dtype, int64_t rows, int64_t 
  */
 
 /*
+ * Bytes of scratch (host only): of sample_rows with requests = -1, else of
+ * verify_drafts; negative for arguments that they refuse.
+ */
+CE_API int64_t choice_work(int dtype, int64_t rows, int64_t vocab, int64_t requests);
+
+/*
  * sample_rows: a token drawn from each row's softmax at a temperature. With
  * e_j = exp((x_j - m) / T), m = max_j x_j and S = sum_j e_j, row i's token is
  *     the first k with e_0 + ... + e_k > u_i S
@@ -527,10 +533,12 @@ CE_API int preference_step(const void *logits, int dtype, int64_t rows, int64_t 
  *     distribution.
  *   tokens: [rows] int64.   logp: [rows] f32, or NULL: the token's
  *     log-probability at that temperature (0 for T = 0), as logp_rows gives it.
+ *   work: scratch of choice_work(dtype, rows, vocab, -1) bytes, 16-byte
+ *     aligned; two calls that may run at the same time need one each.
  */
 CE_API int sample_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,
                        const float *uniforms, double temperature, const float *temperatures, int64_t *tokens,
-                       float *logp, ce_stream_t stream);
+                       float *logp, void *work, ce_stream_t stream);
 
 /*
  * verify_drafts: drafted tokens accepted or replaced so that what a request
@@ -564,8 +572,7 @@ CE_API int sample_rows(const void *logits, int dtype, int64_t rows, int64_t voca
  *     last, and for rows in no request.   logp: [rows] f32, or NULL: the
  *     token's log-probability under p (0 at temperature 0 and where none is
  *     emitted).
- *   work: rows bytes of scratch; two calls that may run at the same time need
- *     one each.
+ *   work: scratch of choice_work(dtype, rows, vocab, requests) bytes, as above.
  */
 CE_API int verify_drafts(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,
                          const int64_t *drafts, const void *draft_logits, int64_t draft_stride,
@@ -672,7 +679,8 @@ CE_API int ce_debug_force(int path, int cluster, int threads);
 
 /*
  * Grid override, for tests: at most `clusters` clusters (0: no cap) in every
- * later launch of a row kernel (not argmax_rows_noalloc's), so that each
+ * later launch of a row kernel (not argmax_rows_noalloc's, sample_rows' and
+ * verify_drafts'), so that each
  * cluster loops over several rows even when the rows are few. Results are
  * the same; only the schedule changes. Returns CE_EINVAL for clusters < 0.
  */

@@ -146,7 +146,8 @@ def _bind(lib):
         "policy_step": [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, i64, vp, vp, vp, vp, vp],
         "preference_loss": [vp, i32, i64, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp],
         "preference_step": [vp, i32, i64, i64, i64, vp, vp, vp, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp],
-        "sample_rows": [vp, i32, i64, i64, i64, vp, ctypes.c_double, vp, vp, vp, vp],
+        "choice_work": [i32, i64, i64, i64],
+        "sample_rows": [vp, i32, i64, i64, i64, vp, ctypes.c_double, vp, vp, vp, vp, vp],
         "verify_drafts": [vp, i32, i64, i64, i64, vp, vp, i64, vp, i64, vp, ctypes.c_double, vp, vp, vp, vp, vp, vp],
         "route_rows": [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp],
         "route_grad": [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, i64, vp],
@@ -155,6 +156,7 @@ def _bind(lib):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = i32
+    lib.choice_work.restype = i64
     lib.ce_status_string.argtypes = [i32]
     lib.ce_status_string.restype = ctypes.c_char_p
     return lib

@@ -17,6 +17,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <initializer_list>
 #include <string>
 
@@ -311,6 +312,11 @@ Temperature temperature_of(PyObject *o, const Logits &x) {
 at::Tensor i64(const Logits &x, at::IntArrayRef sizes) { return empty(x, sizes, at::kLong); }
 int64_t *longs(const at::Tensor &t) { return t.defined() ? static_cast<int64_t *>(t.data_ptr()) : nullptr; }
 
+// The work buffer of a choice (requests < 0: of a sampling).
+at::Tensor scratch(const Logits &x, int64_t requests) {
+    return empty(x, {std::max<int64_t>(16, choice_work(x.dtype, x.rows, x.vocab, requests))}, at::kByte);
+}
+
 // sample(logits, uniforms, temperature, vocab, logp, out)
 PyObject *sample(PyObject *const *a) {
     const Logits x = logits_of(a[0], a[3]);
@@ -325,8 +331,9 @@ PyObject *sample(PyObject *const *a) {
         c10::cuda::CUDAGuard guard(x.t.device());
         if (!out.defined()) out = i64(x, {x.rows});
         if (lp.any && !lp.t.defined()) lp.t = f32(x, {x.rows});
+        const at::Tensor work = scratch(x, -1);
         st = sample_rows(x.t.data_ptr(), x.dtype, x.rows, x.vocab, x.stride, u, t.all, t.rows, longs(out), data(lp.t),
-                         stream_of(x));
+                         work.data_ptr(), stream_of(x));
     }
     written(st, a[4]);
     written(st, a[5]);
@@ -364,7 +371,7 @@ PyObject *verify(PyObject *const *a) {
         c10::cuda::CUDAGuard guard(x.t.device());
         accepted = i64(x, {requests});
         tokens = i64(x, {x.rows});
-        work = empty(x, {x.rows}, at::kByte);
+        work = scratch(x, requests);
         if (lp.any && !lp.t.defined()) lp.t = f32(x, {x.rows});
         st = verify_drafts(x.t.data_ptr(), x.dtype, x.rows, x.vocab, x.stride, drafts, draft_logits, draft_stride,
                            offsets.const_data_ptr<int64_t>(), requests, u, t.all, t.rows, longs(accepted),

@@ -907,6 +907,7 @@ int preference_step(const void *logits, int dtype, int64_t rows, int64_t vocab, 
 static int check_choice_rows(const void *logits, int dtype, int64_t rows, int64_t cols, int64_t stride, int64_t most) {
     if (dtype != CE_F32 && dtype != CE_BF16 && dtype != CE_F16) return CE_EINVAL;
     if (rows < 0 || cols < 1 || cols > most || stride < cols) return CE_EINVAL;
+    if (rows > INT32_MAX) return CE_EINVAL;  // a launch's CTAs
     if (rows > 0 && logits == nullptr) return CE_EINVAL;
     if (rows > 0 && stride > (INT64_MAX / 4) / rows) return CE_EINVAL;  // byte offsets fit int64
     return misaligned(logits, dtype == CE_F32 ? 4 : 2) ? CE_EALIGN : CE_OK;
@@ -932,21 +933,32 @@ static int check_outputs_apart(std::initializer_list<Rows> rows, std::initialize
     return CE_OK;
 }
 
+int64_t choice_work(int dtype, int64_t rows, int64_t vocab, int64_t requests) {
+    if (dtype != CE_F32 && dtype != CE_BF16 && dtype != CE_F16) return CE_EINVAL;
+    if (rows < 0 || vocab < 1 || vocab > kMaxVocab || requests < -1 || requests > INT32_MAX) return CE_EINVAL;
+    if (rows > (INT64_MAX / 64) / (vocab / 512 + 2)) return CE_EINVAL;
+    return choice_bytes(static_cast<DType>(dtype), rows, vocab, requests);
+}
+
 static bool good_temperature(double t) { return t == 0.0 || (t >= 1e-6 && t <= 1e6); }
 
 int sample_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride, const float *uniforms,
-                double temperature, const float *temperatures, int64_t *tokens, float *logp, ce_stream_t stream) {
+                double temperature, const float *temperatures, int64_t *tokens, float *logp, void *work,
+                ce_stream_t stream) {
     int st = check_choice_rows(logits, dtype, rows, vocab, stride, kMaxVocab);
     if (st) return st;
     if (!good_temperature(temperature)) return CE_EINVAL;
-    if (rows > 0 && (uniforms == nullptr || tokens == nullptr)) return CE_EINVAL;
-    if (misaligned(uniforms, 4) || misaligned(temperatures, 4) || misaligned(tokens, 8) || misaligned(logp, 4))
+    if (rows > 0 && (uniforms == nullptr || tokens == nullptr || work == nullptr)) return CE_EINVAL;
+    if (misaligned(uniforms, 4) || misaligned(temperatures, 4) || misaligned(tokens, 8) || misaligned(logp, 4) ||
+        misaligned(work, 16))
         return CE_EALIGN;
     if (rows == 0) return CE_OK;
+    const int64_t scratch = choice_work(dtype, rows, vocab, -1);
+    if (scratch < 0) return CE_EINVAL;
     const int64_t size = dtype == CE_F32 ? 4 : 2;
     if ((st = check_outputs_apart({{logits, rows, vocab * size, stride * size}},
                                   {{uniforms, 4 * rows}, {temperatures, 4 * rows}},
-                                  {{tokens, 8 * rows}, {logp, 4 * rows}})))
+                                  {{tokens, 8 * rows}, {logp, 4 * rows}, {work, scratch}})))
         return st;
     DeviceInfo dev;
     if ((st = current_device(&dev))) return st;
@@ -960,8 +972,7 @@ int sample_rows(const void *logits, int dtype, int64_t rows, int64_t vocab, int6
     a.uniforms = uniforms;
     a.tokens = tokens;
     a.logp = logp;
-    a.grid_cap = current_grid_cap();
-    return cuda_status(launch_sample(static_cast<DType>(dtype), a, dev, stream));
+    return cuda_status(launch_sample(static_cast<DType>(dtype), a, work, dev, stream));
 }
 
 int verify_drafts(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride, const int64_t *drafts,
@@ -973,18 +984,19 @@ int verify_drafts(const void *logits, int dtype, int64_t rows, int64_t vocab, in
     if (!good_temperature(temperature)) return CE_EINVAL;
     if (draft_logits != nullptr && (st = check_choice_rows(draft_logits, dtype, rows, vocab, draft_stride, kMaxVocab)))
         return st;
-    if (requests < 0 || requests > (int64_t(1) << 40) || offsets == nullptr) return CE_EINVAL;
+    if (requests < 0 || requests > INT32_MAX || offsets == nullptr) return CE_EINVAL;
     if (requests > 0 && accepted == nullptr) return CE_EINVAL;
     if (rows > 0 && (drafts == nullptr || uniforms == nullptr || tokens == nullptr || work == nullptr))
         return CE_EINVAL;
     if (misaligned(drafts, 8) || misaligned(offsets, 8) || misaligned(uniforms, 4) || misaligned(temperatures, 4) ||
-        misaligned(accepted, 8) || misaligned(tokens, 8) || misaligned(logp, 4))
+        misaligned(accepted, 8) || misaligned(tokens, 8) || misaligned(logp, 4) || misaligned(work, 16))
         return CE_EALIGN;
-    const int64_t size = dtype == CE_F32 ? 4 : 2;
+    const int64_t size = dtype == CE_F32 ? 4 : 2, scratch = choice_work(dtype, rows, vocab, requests);
+    if (scratch < 0) return CE_EINVAL;
     if ((st = check_outputs_apart(
              {{logits, rows, vocab * size, stride * size}, {draft_logits, rows, vocab * size, draft_stride * size}},
              {{drafts, 8 * rows}, {offsets, 8 * (requests + 1)}, {uniforms, 8 * rows}, {temperatures, 4 * rows}},
-             {{accepted, 8 * requests}, {tokens, 8 * rows}, {logp, 4 * rows}, {work, rows}})))
+             {{accepted, 8 * requests}, {tokens, 8 * rows}, {logp, 4 * rows}, {work, scratch}})))
         return st;
     if (rows == 0 && requests == 0) return CE_OK;
     DeviceInfo dev;
@@ -1005,9 +1017,7 @@ int verify_drafts(const void *logits, int dtype, int64_t rows, int64_t vocab, in
     a.offsets = offsets;
     a.requests = requests;
     a.accepted = accepted;
-    a.accepts = static_cast<uint8_t *>(work);
-    a.grid_cap = current_grid_cap();
-    return cuda_status(launch_verify(static_cast<DType>(dtype), a, dev, stream));
+    return cuda_status(launch_verify(static_cast<DType>(dtype), a, work, dev, stream));
 }
 
 static int check_route(const void *logits, int dtype, int64_t rows, int64_t experts, int64_t stride,

@@ -7,10 +7,17 @@
 //   route_grad      the gradient of the gates
 //
 // Kernels (none uses tensor cores):
-//   k_sample        sample_rows: a row over a cluster of CTAs
-//   k_verify_rows   verify_drafts: every row by itself, a row over a cluster
-//   k_verify_join   its rows into requests: what is emitted ends at the first
-//                   draft that is not accepted
+//   k_states        every row in steps of 4 KB, a state (m, s) for each step: one
+//                   read of the logits, and of the draft rows, in parts of any
+//                   number of warps
+//   k_sample        sample_rows: a warp per row merges its states, draws a step by
+//                   their masses and re-reads that step
+//   k_decide        verify_drafts: a CTA per request merges its rows' states, finds
+//                   the first that accepts no draft and draws from p where the
+//                   token comes from p
+//   k_residual      the other requests' rows again: what max(0, p - q) leaves of
+//                   each step
+//   k_replace       their token: a warp per request draws a step and re-reads it
 //   k_route         route_rows, a warp per row
 //   k_route_grad    route_grad, a warp per row
 #include <algorithm>
@@ -31,7 +38,14 @@ __device__ unsigned long long g_choice_status[2];
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kScan = 8;  // 16-byte loads in flight per thread
-constexpr int kPartMin = 8192;  // bytes of a row per CTA, at least, when a row is split
+constexpr int kStep = 32 * kScan;  // vectors of a step, 4 KB
+constexpr int kDecideThreads = 256;
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+    return v;
+}
 
 __device__ __forceinline__ void count_bad() { atomicAdd(&g_choice_status[0], 1ull); }
 
@@ -88,6 +102,35 @@ __device__ __forceinline__ int warp_segment(Mass m, float w, Mass &t) {
     return top > 0.0f ? __ffs(__ballot_sync(kFullMask, w == top)) - 1 : -1;
 }
 
+// A row as 16-byte vectors on its own grid: vector q holds columns N q - off ..
+// N q - off + N - 1. Vectors [qa, qb) lie in the row; the columns of a partial
+// one at either end are loaded one by one, a lane each.
+template <typename T>
+struct RowGrid {
+    static constexpr int N = Vec<T>::kN;
+    const T *p;
+    int n, off;
+    int qa, qb, nq;  // nq vectors in all
+    __device__ RowGrid(const T *row, int columns) : p(row), n(columns) {
+        off = static_cast<int>((reinterpret_cast<uintptr_t>(p) / sizeof(T)) % N);
+        qa = off > 0 ? 1 : 0;
+        qb = (off + n) / N;
+        nq = (off + n + N - 1) / N;
+    }
+    __device__ int column(int q) const { return N * q - off; }
+    __device__ bool whole(int q) const { return q >= qa && q < qb; }
+    __device__ bool whole(int q, int end) const { return q >= qa && end <= qb; }
+    __device__ uint4 load(int q) const { return ld_stream_u4(reinterpret_cast<const uint4 *>(p - off) + q); }
+    // for vectors a lane apart by several: each line is asked for by several loads
+    __device__ uint4 load_cached(int q) const { return __ldg(reinterpret_cast<const uint4 *>(p - off) + q); }
+    // lane i's column of the partial vector q, -1 if it has none
+    __device__ int edge_column(int q, int lane) const {
+        const int j = column(q) + lane;
+        return lane < N && j >= 0 && j < n ? j : -1;
+    }
+    __device__ float at(int j) const { return Vec<T>::to_float(p[j]); }
+};
+
 // What a column weighs in a draw.
 enum Kind : int {
     kShare = 0,     // 2^((x - m) k)
@@ -101,374 +144,577 @@ struct Weigh {
     float rp, mq, rq;     // kResidual: 1 / s, and the draft row's max and 1 / s
     int skip;             // kOthers: the drafted column
     __device__ float unit() const { return kind == kResidual ? kUnitShares : kUnitWeights; }
+    __device__ float residual(float x, float y) const {
+        // two rounded products: rows that are the same leave exactly nothing
+        return fmaxf(0.0f, __fsub_rn(__fmul_rn(ex2_ftz((x - m) * k), rp), __fmul_rn(ex2_ftz((y - mq) * k), rq)));
+    }
     __device__ float operator()(float x, float y, int j) const {
         if (kind == kGreedy) return x == m ? 1.0f : 0.0f;
-        const float e = ex2_ftz((x - m) * k);
-        // two rounded products: rows that are the same leave exactly nothing
-        if (kind == kResidual) return fmaxf(0.0f, __fsub_rn(__fmul_rn(e, rp), __fmul_rn(ex2_ftz((y - mq) * k), rq)));
-        return kind == kOthers && j == skip ? 0.0f : e;
+        if (kind == kResidual) return residual(x, y);
+        return kind == kOthers && j == skip ? 0.0f : ex2_ftz((x - m) * k);
     }
 };
 
-// The weights of the columns [a, b) at p (and q, kResidual only), added in f32.
+// The columns of a draft row beside a row's: its vectors, or parts of two of
+// them where the two rows start at different phases of 16 bytes.
 template <typename T>
-__device__ float weight_of_run(const T *p, const T *q, int a, int b, const Weigh &w) {
-    constexpr int N = Vec<T>::kN;
-    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(p + a) / sizeof(T)) % N);
-    const bool same = q == nullptr || ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(q)) & 15) == 0;
-    float sum = 0.0f;
-    auto one = [&](int j) { sum += w(Vec<T>::to_float(p[j]), q ? Vec<T>::to_float(q[j]) : 0.0f, j); };
-    int j = a;
-    for (const int head = min(b, a + (N - off) % N); j < head; ++j) one(j);
-    if (same) {
-#pragma unroll 4
-        for (; j + N <= b; j += N) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(p + j);
-            uint4 y = make_uint4(0, 0, 0, 0);
-            if (q) y = *reinterpret_cast<const uint4 *>(q + j);
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) {
-                const float2 xx = Vec<T>::pair(x, i), yy = Vec<T>::pair(y, i);
-                sum += w(xx.x, yy.x, j + 2 * i) + w(xx.y, yy.y, j + 2 * i + 1);
-            }
-        }
+struct Beside {
+    static constexpr int N = Vec<T>::kN;
+    const RowGrid<T> &d;
+    int by, r;  // columns of vector q start at element r of the draft row's vector q + by
+    __device__ Beside(const RowGrid<T> &g, const RowGrid<T> &d_) : d(d_) {
+        r = (d.off - g.off + N) % N;
+        by = d.off < g.off ? -1 : 0;
     }
-    for (; j < b; ++j) one(j);
+    __device__ bool whole(int q, int end) const { return d.whole(q + by, end + by + (r ? 1 : 0)); }
+    __device__ uint4 load(int q) const {
+        const uint4 v = d.load(q + by);
+        return r == 0 ? v : shift_pair<T>(v, d.load(q + by + 1), r);
+    }
+    __device__ uint4 load_cached(int q) const {
+        const uint4 v = d.load_cached(q + by);
+        return r == 0 ? v : shift_pair<T>(v, d.load_cached(q + by + 1), r);
+    }
+};
+
+// N columns of a row from column j on, those outside it -inf, one by one.
+template <typename T>
+__device__ __noinline__ uint4 columns_from(const T *p, int n, int j) {
+    uint4 v = Vec<T>::lowest();
+#pragma unroll
+    for (int i = 0; i < Vec<T>::kN; i += 2) {
+        float2 f = make_float2(-INFINITY, -INFINITY);
+        if (j + i >= 0 && j + i < n) f.x = Vec<T>::to_float(p[j + i]);
+        if (j + i + 1 >= 0 && j + i + 1 < n) f.y = Vec<T>::to_float(p[j + i + 1]);
+        Vec<T>::set_pair(v, i / 2, f);
+    }
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ float weight_of(const uint4 &x, const uint4 &y, int j, const Weigh &w) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < Vec<T>::kN / 2; ++i) {
+        const float2 xx = Vec<T>::pair(x, i), yy = Vec<T>::pair(y, i);
+        sum += w(xx.x, yy.x, j + 2 * i) + w(xx.y, yy.y, j + 2 * i + 1);
+    }
     return sum;
 }
 
-// The column of [a, b) whose weight holds t: runs of columns, a lane each, until
-// a lane has one. All of a warp; -1 if nothing weighs anything.
-template <typename T>
-__device__ int column_of(const T *p, const T *q, int a, int b, const Weigh &w, Mass t) {
-    const int lane = threadIdx.x & 31;
-    while (true) {
-        const int n = b - a;
-        const int run = n <= 32 ? 1 : ((n + 31) / 32 + 7) & ~7;
-        const int lo = min(b, a + lane * run), hi = min(b, lo + run);
-        const float sum = weight_of_run(p, q, lo, hi, w);
-        const int at = warp_segment(mass_of(sum, w.unit()), sum, t);
-        if (at < 0) return -1;
-        if (run == 1) return a + at;
-        b = min(b, a + (at + 1) * run);
-        a += at * run;
-    }
-}
-
-// ---------------------------------------------------------------------------
-// A row over the warps of a cluster: CTA `rank` has `cols` columns, each of its
-// warps a quarter of them, in order.
-struct Part {
-    uint32_t rank, C;
-    int warp, lane;
-    int c0, n;  // this warp's columns
-    __device__ Part(int vocab, int cols) {
-        rank = cluster_rank();
-        C = cluster_size();
-        warp = static_cast<int>(threadIdx.x) >> 5;
-        lane = static_cast<int>(threadIdx.x) & 31;
-        c0 = min(vocab, static_cast<int>(rank) * cols + warp * (cols / kWarps));
-        n = min(vocab, c0 + cols / kWarps) - c0;
-    }
-    __device__ bool leads() const { return rank == 0 && warp == 0; }
-    __device__ int slot() const { return static_cast<int>(rank) * kWarps + warp; }
-};
-
-// Exchanges: every warp pushes 16 bytes into its slot in every CTA, and every
-// warp reads all of them (ce_objectives.cuh: WarpXchg). Lane l gets slots 2 l
-// and 2 l + 1: column order.
-struct Meeting {
-    WarpXchg<kWarps> &x;
-    const Part &part;
-    int64_t n = 0;  // exchanges so far
-    bool failed = false;
-    __device__ void push(float4 v) {
-        const int xs = static_cast<int>(n & 1);
-        if (part.lane < static_cast<int>(part.C))
-            st_async_peer(peer_smem(&x.slot[xs][part.slot()], part.lane), v, peer_smem(&x.bar[xs], part.lane));
-    }
-    __device__ void collect(float4 &a, float4 &b, const float4 &none) {
-        const int xs = static_cast<int>(n & 1), E = kWarps * static_cast<int>(part.C);
-        if (!failed)
-            failed = __any_sync(kFullMask, !mbar_wait_bounded(&x.bar[xs], static_cast<uint32_t>(n >> 1) & 1u));
-        a = 2 * part.lane < E ? x.slot[xs][2 * part.lane] : none;
-        b = 2 * part.lane + 1 < E ? x.slot[xs][2 * part.lane + 1] : none;
-        __syncwarp();
-        // its CTA's other warps may still be reading the slot: nobody pushes to
-        // it again before each of them has pushed the next exchange
-        if (threadIdx.x == 0) mbar_arrive_expect_tx(&x.bar[xs], 16u * kWarps * part.C);
-        ++n;
-    }
-};
-
-__device__ __forceinline__ float4 as_float4(Mass m) {
-    return make_float4(__uint_as_float(static_cast<uint32_t>(m)), __uint_as_float(static_cast<uint32_t>(m >> 32)), 0.0f,
-                       0.0f);
-}
-__device__ __forceinline__ Mass as_mass(const float4 &v) {
-    return static_cast<Mass>(__float_as_uint(v.x)) | static_cast<Mass>(__float_as_uint(v.y)) << 32;
-}
-
-// The slot among all warps' (masses a and b in lanes' slots 2 l and 2 l + 1)
-// that holds u of the total, and t from its start on; -1 if there is no mass.
-__device__ __forceinline__ int slot_of(Mass a, Mass b, float u, Mass &t) {
-    const Mass end = warp_running_sum(a + b);
-    t = part_of_total(u, __shfl_sync(kFullMask, end, 31));
-    const unsigned hit = __ballot_sync(kFullMask, t < end);
-    if (!hit) return -1;
-    const int at = __ffs(hit) - 1;
-    const Mass first = __shfl_sync(kFullMask, a, at);
-    t -= __shfl_sync(kFullMask, end - a - b, at);
-    if (t < first) return 2 * at;
-    t -= first;
-    return 2 * at + 1;
-}
-
-// A row's inputs.
-template <typename T>
-struct RowIn {
-    const T *p, *q;   // the row, and the draft model's (null: none)
-    int64_t draft;    // -1: none
-    float accept, u;  // the numbers that accept the draft and draw a token
-    float T_;         // temperature; 0: greedy
-};
-
-// The columns [c0, c0 + n) of a row into a state, without column `skip`.
-template <typename T>
-__device__ __forceinline__ TokState scan_part(const T *p, const Part &part, int skip, float k) {
-    auto nothing = [] {};
-    TokState st;
-    if (skip >= part.c0 && skip < part.c0 + part.n) {
-        st = tok_scan<T, false, kScan, 32, true>(p + part.c0, skip - part.c0, k, part.lane, nothing);
-        const TokState r = tok_scan<T, false, kScan, 32, true>(p + skip + 1, part.c0 + part.n - skip - 1, k, part.lane,
-                                                               nothing);
-        st = tok_merge<false>(st, r, k);
-    } else {
-        st = tok_scan<T, false, kScan, 32, true>(p + part.c0, part.n, k, part.lane, nothing);
-    }
-    return tok_warp_reduce<false>(st, k);
-}
-
-// One row, by all warps of the cluster: whether its draft was accepted, the same
-// in every warp. The token and its log-probability are written by one warp.
-template <typename T>
-__device__ bool choose_row(const RowIn<T> &in, int vocab, const Part &part, Meeting &meet, int64_t *token, float *logp) {
-    const bool greedy = in.T_ == 0.0f;
-    if (!greedy && !(in.T_ >= 1e-6f && in.T_ <= 1e6f)) {
-        if (part.leads() && part.lane == 0) {
-            *token = -1;
-            if (logp) *logp = nan_f();
-            count_bad();
-        }
-        return false;
-    }
-    // log2(e) / T to a last place: log2(e) in two parts
-    float k = 1.44269504f, inv_t = 1.0f;
-    if (!greedy) {
-        inv_t = 1.0f / in.T_;
-        k = 1.44269504f * inv_t;
-        k += __fmaf_rn(-k, in.T_, 1.44269504f) * inv_t + 1.92596299e-8f * inv_t;
-    }
-    const bool bad_draft = in.draft >= vocab;
-    const int d = in.draft >= 0 && !bad_draft ? static_cast<int>(in.draft) : -1;
-    const T *q = d >= 0 && !greedy ? in.q : nullptr;
-    const bool lookup = d >= 0 && !greedy && in.q == nullptr;  // a draft that no model drew
-    float xd = 0.0f, yd = 0.0f;
-    if (d >= 0) {
-        xd = Vec<T>::to_float(in.p[d]);
-        if (q) yd = Vec<T>::to_float(q[d]);
-    }
-    const TokState mine = scan_part(in.p, part, lookup ? d : -1, k);
-    TokState mine_q = tok_empty();
-    if (q) mine_q = scan_part(q, part, -1, k);
-    meet.push(make_float4(mine.m, mine.s, mine_q.m, mine_q.s));
-    float4 a, b;
-    meet.collect(a, b, make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f));
-    TokState P = tok_merge<false>(TokState{a.x, a.y, 0.0f}, TokState{b.x, b.y, 0.0f}, k);
-    P = tok_warp_reduce<false>(P, k);
-    if (lookup) tok_push1<false>(P, xd, k);
-    const bool leader = part.leads() && part.lane == 0;
-    if (bad_draft && leader) count_bad();
-    if (!isfinite(P.m) || isnan(P.s)) {  // no distribution
-        if (leader) {
-            *token = -1;
-            if (logp) *logp = nan_f();
-            count_bad();
-        }
-        return false;
-    }
-    Weigh w{};
-    w.kind = greedy ? kGreedy : lookup ? kOthers : kShare;
-    w.m = P.m;
-    w.k = k;
-    w.skip = d;
-    if (d >= 0 && !greedy) {
-        const float pd = ex2_ftz((xd - P.m) * k) / P.s;
-        float qd = 1.0f;
-        bool drawn = true;
-        if (q) {
-            TokState Q = tok_merge<false>(TokState{a.z, a.w, 0.0f}, TokState{b.z, b.w, 0.0f}, k);
-            Q = tok_warp_reduce<false>(Q, k);
-            drawn = isfinite(Q.m) && !isnan(Q.s);
-            qd = ex2_ftz((yd - Q.m) * k) / Q.s;
-            if (drawn) {
-                w.kind = kResidual;
-                w.rp = 1.0f / P.s;
-                w.mq = Q.m;
-                w.rq = 1.0f / Q.s;
-            } else if (leader) {
-                count_bad();  // no distribution: the draft is not accepted, the token drawn from p
-            }
-        }
-        if (drawn && in.accept * qd < pd) {
-            if (leader) {
-                *token = d;
-                if (logp) *logp = (xd - P.m) * inv_t - logf(P.s);
-            }
-            return true;
-        }
-    }
-    // the masses of the warps' parts
-    Mass ma, mb;
-    if (w.kind == kResidual) {
-        float sum = 0.0f;
-        const int run = ((part.n + 31) / 32 + 7) & ~7;
-        const int lo = min(part.n, part.lane * run), hi = min(part.n, lo + run);
-        sum = weight_of_run(in.p, q, part.c0 + lo, part.c0 + hi, w);
+// Walking kN segments of one lane: the one that holds t, and t from its start on;
+// for a t behind the last mass the last that weighs anything.
+template <int kN>
+__device__ __forceinline__ int walk(const float (&w)[kN], float unit, Mass &t) {
+    int at = 0;
+    bool found = false;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
-        float4 e, f;
-        meet.push(as_float4(mass_of(sum, kUnitShares)));
-        meet.collect(e, f, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
-        ma = as_mass(e);
-        mb = as_mass(f);
-        // nothing left: the two rows are the same, and the draw is from p
-        if (!__any_sync(kFullMask, (ma | mb) != 0)) w.kind = kShare;
+    for (int i = 0; i < kN; ++i) {
+        const Mass m = mass_of(w[i], unit);
+        if (!found && w[i] > 0.0f) at = i;
+        if (!found && t < m) found = true;
+        if (!found) t -= m;
     }
-    if (w.kind == kGreedy) {
-        ma = a.x == P.m;
-        mb = b.x == P.m;
-    } else if (w.kind != kResidual) {
-        ma = mass_of(a.y * ex2_ftz((a.x - P.m) * k), kUnitWeights);
-        mb = mass_of(b.y * ex2_ftz((b.x - P.m) * k), kUnitWeights);
-    }
-    Mass t;
-    const int slot = slot_of(ma, mb, greedy ? 0.0f : in.u, t);
-    int column = -1;
-    if (slot < 0) {
-        column = d;  // nothing but the drafted column weighs anything (kOthers)
-    } else if (slot == part.slot()) {
-        column = column_of(in.p, q, part.c0, part.c0 + part.n, w, t);
-    }
-    if (slot < 0 ? part.leads() : slot == part.slot()) {
-        if (part.lane == 0) {
-            *token = column;
-            if (logp)
-                *logp = greedy ? 0.0f : column < 0 ? nan_f() : (Vec<T>::to_float(in.p[column]) - P.m) * inv_t - logf(P.s);
-        }
-    }
-    if (!greedy || d < 0) return false;
-    // a greedy request accepts its draft where it is the row's first largest
-    meet.push(make_float4(__int_as_float(slot == part.slot() ? column : -1), 0.0f, 0.0f, 0.0f));
-    meet.collect(a, b, make_float4(__int_as_float(-1), 0.0f, 0.0f, 0.0f));
-    return __any_sync(kFullMask, __float_as_int(a.x) == d || __float_as_int(b.x) == d);
+    if (!found) t = ~Mass(0);
+    return at;
 }
 
+// The column of step `step` whose weight holds t, and its logit: eight vectors
+// next to one another in each lane, so one running sum over the lanes, then the
+// lane's vectors and the vector's columns. All of a warp; column -1 if nothing
+// weighs anything. kBeside: weights of p and q, else of p alone.
+struct Found {
+    int column;
+    float x;
+};
+template <typename T, bool kBeside>
+__device__ __forceinline__ Found column_of(const RowGrid<T> &g, const RowGrid<T> &d, int step, const Weigh &w, Mass t) {
+    constexpr int N = Vec<T>::kN;
+    const int lane = threadIdx.x & 31, q = step * kStep + kScan * lane;
+    const Beside<T> beside(g, d);
+    uint4 x[kScan], y[kBeside ? kScan : 1];
+#pragma unroll
+    for (int u = 0; u < kScan; ++u) {
+        x[u] = Vec<T>::lowest();
+        if (g.whole(q + u)) x[u] = g.load_cached(q + u);
+        if (kBeside) {
+            y[u] = Vec<T>::lowest();
+            if (beside.whole(q + u, q + u + 1)) y[u] = beside.load_cached(q + u);
+        }
+    }
+    // partial vectors, and columns that lie in one of the draft row's
+#pragma unroll
+    for (int u = 0; u < kScan; ++u)
+        if (q + u < g.nq) {
+            if (!g.whole(q + u)) x[u] = columns_from(g.p, g.n, g.column(q + u));
+            if (kBeside && !beside.whole(q + u, q + u + 1)) y[u] = columns_from(d.p, d.n, g.column(q + u));
+        }
+    float sum[kScan], all = 0.0f;
+    Mass m = 0;
+#pragma unroll
+    for (int u = 0; u < kScan; ++u) {
+        sum[u] = weight_of<T>(x[u], kBeside ? y[u] : x[u], g.column(q + u), w);
+        all += sum[u];
+        m += mass_of(sum[u], w.unit());
+    }
+    const int l = warp_segment(m, all, t);
+    if (l < 0) return Found{-1, 0.0f};
+    const int u = walk(sum, w.unit(), t);
+    uint4 xu = x[0], yu = y[0];
+#pragma unroll
+    for (int i = 1; i < kScan; ++i)
+        if (i == u) {
+            xu = x[i];
+            if (kBeside) yu = y[i];
+        }
+    float e[N], xs[N];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const float2 xx = Vec<T>::pair(xu, i), yy = Vec<T>::pair(kBeside ? yu : xu, i);
+        const int j = g.column(q + u) + 2 * i;
+        xs[2 * i] = xx.x, xs[2 * i + 1] = xx.y;
+        e[2 * i] = w(xx.x, yy.x, j), e[2 * i + 1] = w(xx.y, yy.y, j + 1);
+    }
+    const int at = walk(e, w.unit(), t);
+    float found = xs[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i)
+        if (i == at) found = xs[i];
+    return Found{__shfl_sync(kFullMask, g.column(q + u) + at, l), __shfl_sync(kFullMask, found, l)};
+}
+
+// One step of a scan: vectors q .. q + kStep - 1 (those below nq) into a state,
+// column `skip` (-1: none) left out.
 template <typename T>
+__device__ __forceinline__ void scan_step(TokState &st, const RowGrid<T> &g, int q, int skip, int lane, float k) {
+    constexpr int N = Vec<T>::kN;
+    uint4 v[kScan];
+    const bool whole = g.whole(q, q + kStep);
+    if (whole) {
+#pragma unroll
+        for (int u = 0; u < kScan; ++u) v[u] = g.load(q + 32 * u + lane);
+    } else {
+#pragma unroll
+        for (int u = 0; u < kScan; ++u) {
+            const int i = q + 32 * u + lane;
+            v[u] = g.whole(i) ? g.load(i) : Vec<T>::lowest();
+        }
+    }
+    const int skip_q = skip < 0 ? -1 : (skip + g.off) / N;
+    if (skip_q >= q && skip_q < q + kStep) {
+        const int at = skip + g.off - N * skip_q;
+#pragma unroll
+        for (int u = 0; u < kScan; ++u)
+            if (q + 32 * u + lane == skip_q) {
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    float2 f = Vec<T>::pair(v[u], i);
+                    if (2 * i == at) f.x = -INFINITY;
+                    if (2 * i + 1 == at) f.y = -INFINITY;
+                    Vec<T>::set_pair(v[u], i, f);
+                }
+            }
+    }
+    tok_push<T, false, kScan>(st, v, k);
+    if (!whole) {  // the row's partial vectors
+        const int head = q == 0 && g.qa > 0 ? g.edge_column(0, lane) : -1;
+        const int tail = g.qb < g.nq && g.qb >= max(q, g.qa) && g.qb < q + kStep ? g.edge_column(g.qb, lane) : -1;
+        if (head >= 0 && head != skip) tok_push1<false>(st, g.at(head), k);
+        if (tail >= 0 && tail != skip) tok_push1<false>(st, g.at(tail), k);
+    }
+}
+
+// A row's temperature as its arithmetic takes it; `ok`: 0 or in range.
+struct Heat {
+    float k, inv_t;
+    bool greedy, ok;
+    __device__ explicit Heat(float t) {
+        greedy = t == 0.0f;
+        ok = greedy || (t >= 1e-6f && t <= 1e6f);
+        inv_t = 1.0f;
+        k = 1.44269504f;
+        if (ok && !greedy) {
+            // log2(e) / T to a last place: log2(e) in two parts
+            inv_t = 1.0f / t;
+            k = 1.44269504f * inv_t;
+            k += __fmaf_rn(-k, t, 1.44269504f) * inv_t + 1.92596299e-8f * inv_t;
+        }
+    }
+};
 __device__ __forceinline__ float temperature_of(const ChoiceArgs &a, int64_t row) {
     return a.temperatures ? a.temperatures[row] : a.temperature;
 }
 
-// The exchange slots of a cluster exist before a peer pushes, and no CTA leaves
-// while a peer may still push to it.
-__device__ __forceinline__ void open_meeting(WarpXchg<kWarps> &x) {
-    if (threadIdx.x == 0) warp_xchg_init(x, 2, cluster_size());
-    __syncthreads();
-    cluster_arrive_release();
-    cluster_wait();
+template <typename T>
+__device__ __forceinline__ RowGrid<T> target_row(const ChoiceArgs &a, int64_t row) {
+    return RowGrid<T>(static_cast<const T *>(a.logits) + row * a.stride, a.vocab);
 }
-__device__ __forceinline__ void close_meeting(const Meeting &meet) {
-    cluster_arrive();
-    cluster_wait();
-    if (meet.failed && (threadIdx.x & 31) == 0) atomicAdd(&g_choice_status[1], 1ull);
+template <typename T>
+__device__ __forceinline__ RowGrid<T> draft_row(const ChoiceArgs &a, int64_t row) {
+    return RowGrid<T>(static_cast<const T *>(a.draft_logits) + row * a.draft_stride, a.vocab);
+}
+// Step states of a target row, and of a draft row (behind all target rows').
+__device__ __forceinline__ float2 *states_of(const ChoiceArgs &a, int64_t row) { return a.states + row * a.steps; }
+__device__ __forceinline__ float2 *draft_states_of(const ChoiceArgs &a, int64_t row) {
+    return a.states + (a.rows + row) * a.steps;
 }
 
-// k_sample: a cluster per row.
+// k_states: a warp per `unit` steps of a row: (m, s) of each step, its m the
+// largest value up to the step's end. Rows [0, rows) are the target's, and, of a
+// verification with draft logits, rows [rows, 2 rows) the drafts'; a row in no
+// request, and the draft row of a row without a draft, are not read.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 8) k_sample(ChoiceArgs a, int cols) {
-    __shared__ WarpXchg<kWarps> x;
-    const Part part(a.vocab, cols);
-    open_meeting(x);
-    Meeting meet{x, part};
-    for (int64_t row = cluster_id_x(); row < a.rows; row += cluster_count_x()) {
-        RowIn<T> in{};
-        in.p = static_cast<const T *>(a.logits) + row * a.stride;
-        in.draft = -1;
-        in.u = a.uniforms[row];
-        in.T_ = temperature_of<T>(a, row);
-        choose_row(in, a.vocab, part, meet, a.tokens + row, a.logp ? a.logp + row : nullptr);
-    }
-    close_meeting(meet);
-}
-
-// k_verify_rows: a cluster per row, each row as if all before it were accepted.
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 8) k_verify_rows(ChoiceArgs a, int cols) {
-    __shared__ WarpXchg<kWarps> x;
+__global__ void __launch_bounds__(kThreads, 8) k_states(ChoiceArgs a, int unit, int units, int64_t warps) {
     launch_dependents();
-    const Part part(a.vocab, cols);
-    open_meeting(x);
-    Meeting meet{x, part};
-    const int64_t first = a.offsets[0], last = a.offsets[a.requests];
-    for (int64_t row = cluster_id_x(); row < a.rows; row += cluster_count_x()) {
-        if (row < first || row >= last) {
-            if (part.leads() && part.lane == 0) {
-                a.tokens[row] = -1;
-                if (a.logp) a.logp[row] = 0.0f;
-                a.accepts[row] = 0;
-            }
-            continue;
-        }
-        RowIn<T> in{};
-        in.p = static_cast<const T *>(a.logits) + row * a.stride;
-        if (a.draft_logits) in.q = static_cast<const T *>(a.draft_logits) + row * a.draft_stride;
-        in.draft = a.drafts[row];
-        in.accept = a.uniforms[2 * row];
-        in.u = a.uniforms[2 * row + 1];
-        in.T_ = temperature_of<T>(a, row);
-        const bool yes = choose_row(in, a.vocab, part, meet, a.tokens + row, a.logp ? a.logp + row : nullptr);
-        if (part.leads() && part.lane == 0) a.accepts[row] = yes;
+    const int lane = threadIdx.x & 31;
+    const int64_t id = blockIdx.x * int64_t(kWarps) + (threadIdx.x >> 5);
+    if (id >= warps) return;
+    int64_t row = id / units;
+    const int first = static_cast<int>(id - row * units) * unit;
+    int skip = -1;
+    bool draft = false;
+    float temperature = a.temperature;
+    if (a.offsets) {
+        draft = row >= a.rows;
+        if (draft) row -= a.rows;
+        // asked for together: one latency before the row's own
+        const int64_t lo = a.offsets[0], hi = a.offsets[a.requests], d = a.drafts[row];
+        temperature = temperature_of(a, row);
+        const bool drafted = d >= 0 && d < a.vocab && temperature != 0.0f;
+        if (row < lo || row >= hi || (draft && !drafted)) return;
+        if (!a.draft_logits && drafted) skip = static_cast<int>(d);
+    } else {
+        temperature = temperature_of(a, row);
     }
-    close_meeting(meet);
+    const RowGrid<T> g = draft ? draft_row<T>(a, row) : target_row<T>(a, row);
+    const Heat heat(temperature);
+    const int n = min(unit, (g.nq + kStep - 1) / kStep - first);
+    TokState st = tok_empty();
+    float2 mine = make_float2(-INFINITY, 0.0f);
+    for (int i = 0; i < n; ++i) {
+        scan_step(st, g, (first + i) * kStep, skip, lane, heat.k);
+        st = tok_warp_reduce<false>(st, heat.k);
+        if (lane == i) mine = make_float2(st.m, st.s);
+        st.s = 0.0f;
+    }
+    // a row of another phase may have a step less: an empty one
+    if (lane < unit && first + lane < a.steps)
+        (draft ? draft_states_of(a, row) : states_of(a, row))[first + lane] = mine;
 }
 
-// k_verify_join: a warp per request: its accepted drafts, and nothing emitted
-// behind the first row that accepts none.
-__global__ void __launch_bounds__(kThreads) k_verify_join(ChoiceArgs a) {
-    wait_prerequisites();
+// A row's step states, by a warp: lane l holds steps l cnt .. l cnt + cnt - 1, the
+// first kHeld of them at hand (all of them up to 32 kHeld steps: 262144 f32
+// columns, or 524288 of 16 bits).
+constexpr int kHeld = 8;
+struct Steps {
+    const float2 *p;
+    int n, cnt, first;
+    float2 held[kHeld];
+    __device__ Steps(const float2 *states, int steps) : p(states), n(steps) {
+        cnt = (steps + 31) / 32;
+        first = static_cast<int>(threadIdx.x & 31) * cnt;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            held[i] = i < cnt && first + i < n ? p[first + i] : make_float2(-INFINITY, 0.0f);
+    }
+    // fn(state, i) for each of the lane's steps i, in order
+    template <typename Fn>
+    __device__ __forceinline__ void each(Fn fn) const {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) fn(held[i], i);
+        for (int i = kHeld; i < cnt; ++i)
+            if (first + i < n) fn(p[first + i], i);
+    }
+    __device__ TokState merged(float k) const {
+        float m = -INFINITY, s = 0.0f;
+        each([&](float2 v, int) { m = fmaxf(m, v.x); });
+        m = warp_max(m);
+        const float mm = m == -INFINITY ? 0.0f : m;
+        each([&](float2 v, int) { s += v.y * ex2_ftz((v.x - mm) * k); });
+        return TokState{m, warp_sum(s), 0.0f};
+    }
+    // The step that u of all steps' weights falls in, and t from its start on; -1
+    // if nothing weighs anything.
+    template <typename Weight>
+    __device__ __forceinline__ int draw(float unit, float u, Weight weight, Mass &t) const {
+        Mass mine = 0;
+        each([&](float2 v, int) { mine += mass_of(weight(v), unit); });
+        const Mass upto = warp_running_sum(mine), total = __shfl_sync(kFullMask, upto, 31);
+        t = part_of_total(u, total);
+        if (total == 0) return -1;
+        const int l = __ffs(__ballot_sync(kFullMask, t < upto)) - 1;
+        Mass rest = t - (upto - mine);  // lane l's
+        int at = 0;
+        bool found = false;
+        each([&](float2 v, int i) {
+            const Mass m = mass_of(weight(v), unit);
+            if (!found && rest < m) found = true, at = i;
+            if (!found) rest -= m;
+        });
+        t = __shfl_sync(kFullMask, rest, l);
+        return __shfl_sync(kFullMask, first + at, l);
+    }
+};
+__device__ __forceinline__ bool is_distribution(const TokState &st) { return isfinite(st.m) && !isnan(st.s); }
+
+// The column that u draws from a row by its own weights (greedy: its first
+// largest), without w.skip for kOthers; column -1 if nothing weighs anything.
+template <typename T>
+__device__ __forceinline__ Found draw_own(const RowGrid<T> &g, const Steps &steps, const Weigh &w, float u) {
+    Mass t;
+    const int step = steps.draw(kUnitWeights, w.kind == kGreedy ? 0.0f : u, [&](float2 v) {
+        return w.kind == kGreedy ? (v.x == w.m ? 1.0f : 0.0f) : v.y * ex2_ftz((v.x - w.m) * w.k);
+    }, t);
+    return step < 0 ? Found{-1, 0.0f} : column_of<T, false>(g, g, step, w, t);
+}
+
+__device__ __forceinline__ float logp_of(float x, const TokState &st, const Heat &heat) {
+    return heat.greedy ? 0.0f : (x - st.m) * heat.inv_t - logf(st.s);
+}
+
+// k_sample: a warp per row, behind k_states.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_sample(ChoiceArgs a) {
     const int lane = threadIdx.x & 31;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
-    for (int64_t s = blockIdx.x * int64_t(kWarps) + (threadIdx.x >> 5); s < a.requests; s += warps) {
-        const int64_t r0 = a.offsets[s], r1 = a.offsets[s + 1];
-        if (r0 < 0 || r1 < r0 || r1 > a.rows) {
-            if (lane == 0) {
-                a.accepted[s] = -1;
-                count_bad();
-            }
-            continue;
+    const int64_t row = blockIdx.x * int64_t(kWarps) + (threadIdx.x >> 5);
+    if (row >= a.rows) return;
+    const RowGrid<T> g = target_row<T>(a, row);
+    const Heat heat(temperature_of(a, row));
+    const float u = a.uniforms[row];
+    wait_prerequisites();
+    const Steps steps(states_of(a, row), a.steps);
+    const TokState st = steps.merged(heat.k);
+    Found f{-1, 0.0f};
+    if (heat.ok && is_distribution(st)) {
+        Weigh w{};
+        w.kind = heat.greedy ? kGreedy : kShare;
+        w.m = st.m;
+        w.k = heat.k;
+        f = draw_own(g, steps, w, u);
+    }
+    if (lane == 0) {
+        a.tokens[row] = f.column;
+        if (a.logp) a.logp[row] = f.column < 0 ? nan_f() : logp_of(f.x, st, heat);
+        if (f.column < 0) count_bad();
+    }
+}
+
+// k_decide: a CTA per request, behind k_states. Its warps judge a row each, in
+// order, until one accepts no draft; the token of that row is drawn here where
+// it comes from p, and left to k_residual and k_replace where it comes from what
+// q leaves of p.
+enum Verdict : int { kAccepted = 0, kDrawn = 1, kPending = 2 };
+
+// A row's own inputs, asked for before the states are there.
+struct RowNumbers {
+    int64_t draft;
+    float accept, u, temperature, xd, yd;
+    int d;  // the draft, -1: none
+};
+template <typename T>
+__device__ __forceinline__ RowNumbers row_numbers(const ChoiceArgs &a, int64_t row) {
+    RowNumbers r{};
+    r.draft = a.drafts[row];
+    r.accept = a.uniforms[2 * row];
+    r.u = a.uniforms[2 * row + 1];
+    r.temperature = temperature_of(a, row);
+    r.d = r.draft >= 0 && r.draft < a.vocab ? static_cast<int>(r.draft) : -1;
+    if (r.d >= 0) {
+        r.xd = target_row<T>(a, row).at(r.d);
+        if (a.draft_logits) r.yd = draft_row<T>(a, row).at(r.d);
+    }
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ Verdict judge(const ChoiceArgs &a, int64_t row, const RowNumbers &r) {
+    const int lane = threadIdx.x & 31;
+    const RowGrid<T> g = target_row<T>(a, row);
+    const Heat heat(r.temperature);
+    const bool drafted = r.d >= 0 && !heat.greedy, lookup = drafted && a.draft_logits == nullptr;
+    const Steps steps(states_of(a, row), a.steps);
+    TokState q{};
+    if (drafted && !lookup) q = Steps(draft_states_of(a, row), a.steps).merged(heat.k);
+    TokState p = steps.merged(heat.k);
+    if (lookup) tok_push1<false>(p, r.xd, heat.k);  // its column is not among the states
+    Weigh w{};
+    w.kind = heat.greedy ? kGreedy : lookup ? kOthers : kShare;
+    w.m = p.m;
+    w.k = heat.k;
+    w.skip = r.d;
+    bool odd = r.draft >= a.vocab, accepted = false, drawn = false;
+    Found f{-1, 0.0f};
+    float logp = 0.0f;
+    if (!heat.ok || !is_distribution(p)) {
+        odd = true;
+        logp = nan_f();
+    } else {
+        if (drafted) {
+            const bool from = lookup || is_distribution(q);  // else not accepted, the token drawn from p
+            odd |= !from;
+            const float qd = lookup ? 1.0f : ex2_ftz((r.yd - q.m) * heat.k) / q.s;
+            accepted = from && r.accept * qd < ex2_ftz((r.xd - p.m) * heat.k) / p.s;
+            drawn = from && !lookup && !accepted;
+            if (accepted) f = Found{r.d, r.xd};
         }
-        int64_t n = -1;  // rows before the first that accepts none
-        for (int64_t r = r0; r < r1; r += 32) {
-            const bool in = r + lane < r1;
-            const unsigned stop = __ballot_sync(kFullMask, in && n < 0 && a.accepts[r + lane] == 0);
-            const bool over = n >= 0;
-            if (n < 0 && stop) n = r - r0 + __ffs(stop) - 1;
-            if (in && n >= 0 && (over || r + lane > r0 + n)) {
-                a.tokens[r + lane] = -1;
-                if (a.logp) a.logp[r + lane] = 0.0f;
+        if (!accepted && !drawn) {
+            f = draw_own(g, steps, w, r.u);
+            if (f.column < 0) f = Found{r.d, r.xd};  // nothing but the draft weighs anything
+            accepted = heat.greedy && f.column == r.d;
+        }
+        if (!drawn) logp = logp_of(f.x, p, heat);
+    }
+    if (lane == 0) {
+        a.tokens[row] = f.column;
+        if (a.logp) a.logp[row] = logp;
+        if (drawn) a.row_states[row] = make_float4(p.m, p.s, q.m, q.s);
+        if (odd) count_bad();
+    }
+    return accepted ? kAccepted : drawn ? kPending : kDrawn;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kDecideThreads) k_decide(ChoiceArgs a) {
+    constexpr int kRows = kDecideThreads / 32;
+    __shared__ int verdicts[kRows];
+    launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t s = blockIdx.x, lo = a.offsets[0], hi = a.offsets[a.requests];
+    const int64_t r0 = s < a.requests ? a.offsets[s] : 0, r1 = s < a.requests ? a.offsets[s + 1] : 0;
+    const bool good = r0 >= 0 && r1 >= r0 && r1 <= a.rows;
+    auto silent = [&](int64_t row) {
+        a.tokens[row] = -1;
+        if (a.logp) a.logp[row] = 0.0f;
+    };
+    // a row outside [lo, hi) has no states: of a table that decreases
+    auto has_states = [&](int64_t row) { return good && row < r1 && row >= lo && row < hi; };
+    RowNumbers numbers{};
+    if (has_states(r0 + warp)) numbers = row_numbers<T>(a, r0 + warp);
+    wait_prerequisites();
+    if (s == 0)  // rows in no request
+        for (int64_t r = threadIdx.x; r < a.rows; r += kDecideThreads)
+            if (r < lo || r >= hi) silent(r);
+    if (s >= a.requests) return;
+    Pending pending{-1, 0.0f, 0.0f, 0.0f, 0.0f};
+    int64_t stop = good ? -1 : 0;
+    for (int64_t r = r0; good && r < r1 && stop < 0; r += kRows) {
+        const int64_t row = r + warp;
+        Verdict v = kDrawn;
+        if (has_states(row)) {
+            if (r > r0) numbers = row_numbers<T>(a, row);
+            v = judge<T>(a, row, numbers);
+        } else if (row < r1 && lane == 0) {
+            silent(row);
+        }
+        if (lane == 0) verdicts[warp] = v;
+        __syncthreads();
+        for (int i = 0; i < kRows && r + i < r1; ++i)
+            if (verdicts[i] != kAccepted) {
+                stop = r + i;
+                if (verdicts[i] == kPending) {
+                    const float4 st = a.row_states[stop];
+                    pending = Pending{stop, st.x, st.y, st.z, st.w};
+                }
+                break;
+            }
+        __syncthreads();
+    }
+    if (stop < 0) stop = r1;
+    if (threadIdx.x == 0) {
+        a.accepted[s] = good ? stop - r0 : -1;
+        if (a.pending) a.pending[s] = pending;
+        if (!good) count_bad();
+    }
+    for (int64_t r = stop + 1 + threadIdx.x; good && r < r1; r += kDecideThreads) silent(r);
+}
+
+__device__ __forceinline__ Weigh residual_of(const Pending &p, const Heat &heat) {
+    Weigh w{};
+    w.kind = kResidual;
+    w.m = p.m;
+    w.k = heat.k;
+    w.rp = 1.0f / p.s;
+    w.mq = p.mq;
+    w.rq = 1.0f / p.sq;
+    w.skip = -1;
+    return w;
+}
+
+// k_residual: a warp per `unit` steps of a pending request's row: the sum of
+// max(0, p - q) over each step, over the draft row's states, which have served.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 6) k_residual(ChoiceArgs a, int unit, int units, int64_t warps) {
+    constexpr int N = Vec<T>::kN, kU = kScan / 2, kHalf = 32 * kU;
+    launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const int64_t id = blockIdx.x * int64_t(kWarps) + (threadIdx.x >> 5);
+    wait_prerequisites();
+    if (id >= warps) return;
+    const int64_t s = id / units;
+    const int first = static_cast<int>(id - s * units) * unit;
+    const Pending p = a.pending[s];
+    if (p.row < 0) return;
+    const RowGrid<T> g = target_row<T>(a, p.row), d = draft_row<T>(a, p.row);
+    const Beside<T> beside(g, d);
+    const Weigh w = residual_of(p, Heat(temperature_of(a, p.row)));
+    float mine = 0.0f;
+    for (int i = 0; i < unit; ++i) {
+        float sum = 0.0f;
+        for (int q = (first + i) * kStep; q < min(g.nq, (first + i + 1) * kStep); q += kHalf) {
+            const int end = min(g.nq, q + kHalf);
+            if (g.whole(q, end) && beside.whole(q, end)) {
+                uint4 x[kU], y[kU];
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const int v = q + 32 * u + lane;
+                    x[u] = v < end ? g.load(v) : Vec<T>::lowest();
+                    y[u] = v < end ? beside.load(v) : Vec<T>::lowest();
+                }
+#pragma unroll
+                for (int u = 0; u < kU; ++u)
+#pragma unroll
+                    for (int h = 0; h < N / 2; ++h) {
+                        const float2 xx = Vec<T>::pair(x[u], h), yy = Vec<T>::pair(y[u], h);
+                        sum += w.residual(xx.x, yy.x) + w.residual(xx.y, yy.y);
+                    }
+            } else {
+                for (int v = q + lane; v < end; v += 32) {
+                    const int j = g.column(v);
+                    sum += weight_of<T>(columns_from(g.p, g.n, j), columns_from(d.p, d.n, j), j, w);
+                }
             }
         }
-        if (lane == 0) a.accepted[s] = n < 0 ? r1 - r0 : n;
+        sum = warp_sum(sum);
+        if (lane == i) mine = sum;
+    }
+    if (lane < unit && first + lane < a.steps) draft_states_of(a, p.row)[first + lane].x = mine;
+}
+
+// k_replace: a warp per request.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_replace(ChoiceArgs a) {
+    const int lane = threadIdx.x & 31;
+    const int64_t s = blockIdx.x * int64_t(kWarps) + (threadIdx.x >> 5);
+    wait_prerequisites();
+    if (s >= a.requests) return;
+    const Pending p = a.pending[s];
+    if (p.row < 0) return;
+    const RowGrid<T> g = target_row<T>(a, p.row), d = draft_row<T>(a, p.row);
+    const Heat heat(temperature_of(a, p.row));
+    Weigh w = residual_of(p, heat);
+    const float u = a.uniforms[2 * p.row + 1];
+    const Steps sums(draft_states_of(a, p.row), a.steps);
+    Mass t;
+    const int step = sums.draw(kUnitShares, u, [&](float2 v) { return v.x; }, t);
+    Found f{-1, 0.0f};
+    if (step >= 0) f = column_of<T, true>(g, d, step, w, t);
+    if (f.column < 0) {  // nothing left: the two rows are the same, and the draw is from p
+        w.kind = kShare;
+        f = draw_own(g, Steps(states_of(a, p.row), a.steps), w, u);
+    }
+    if (lane == 0) {
+        a.tokens[p.row] = f.column;
+        if (a.logp) a.logp[p.row] = f.column < 0 ? nan_f() : logp_of(f.x, TokState{p.m, p.s, 0.0f}, heat);
     }
 }
 
@@ -498,12 +744,6 @@ __device__ __forceinline__ void load_columns(float (&z)[V], const T *p, int j, i
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) z[i] = j + i < n ? Vec<T>::to_float(p[j + i]) : -INFINITY;
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
-    return v;
 }
 
 __device__ __forceinline__ float exp_of(float d) { return ex2_ftz(d * 1.44269504f); }
@@ -736,34 +976,54 @@ int64_t capped(int64_t clusters, int64_t cap) {
     return std::max<int64_t>(1, cap > 0 ? std::min(clusters, cap) : clusters);
 }
 
-// Columns of a CTA: its warps' parts are multiples of 8.
-int cols_of(int64_t vocab, int c) { return static_cast<int>(((vocab + c - 1) / c + 31) & ~int64_t(31)); }
-
-int split_of(DType t, int64_t rows, int64_t vocab, const DeviceInfo &dev) {
-    const int64_t fill = 6 * static_cast<int64_t>(dev.sms) / std::max<int64_t>(1, rows);
-    const int64_t parts = (vocab * elem_size(t) + kPartMin - 1) / kPartMin;
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fill, parts), kMaxCluster)));
+// Steps per warp: as many as keep the warps at `kWavesOfWarps` times what the GPU
+// holds, at most 32 (a lane each).
+int unit_of(int64_t steps, int64_t rows, const DeviceInfo &dev) {
+    const int64_t resident = 8 * kWarps * static_cast<int64_t>(dev.sms);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(8, steps), steps * rows / resident)));
 }
 
 template <typename T>
-Kernel &sample_kernel() {
-    static Kernel k(reinterpret_cast<const void *>(&k_sample<T>), false);
-    return k;
+struct Kernels {
+    static const void *states() { return reinterpret_cast<const void *>(&k_states<T>); }
+    static const void *sample() { return reinterpret_cast<const void *>(&k_sample<T>); }
+    static const void *decide() { return reinterpret_cast<const void *>(&k_decide<T>); }
+    static const void *residual() { return reinterpret_cast<const void *>(&k_residual<T>); }
+    static const void *replace() { return reinterpret_cast<const void *>(&k_replace<T>); }
+};
+
+cudaError_t launch(const void *fn, int64_t ctas, bool dependent, cudaStream_t s, void **args, int threads = kThreads) {
+    LaunchConfig l(ctas, threads, 0, dependent, s);
+    return cudaLaunchKernelExC(&l.cfg, fn, args);
 }
-template <typename T>
-Kernel &verify_kernel() {
-    static Kernel k(reinterpret_cast<const void *>(&k_verify_rows<T>), false);
-    return k;
+int64_t ctas_of(int64_t warps) { return (warps + kWarps - 1) / kWarps; }
+
+// A pass of a warp per unit of steps over `rows` rows.
+cudaError_t launch_steps(const void *fn, ChoiceArgs &a, int64_t rows, bool dependent, const DeviceInfo &dev, cudaStream_t s) {
+    int unit = unit_of(a.steps, rows, dev);
+    int units = (a.steps + unit - 1) / unit;
+    int64_t warps = rows * units;
+    void *args[] = {&a, &unit, &units, &warps};
+    return launch(fn, ctas_of(warps), dependent, s, args);
 }
 
-cudaError_t launch_rows(Kernel &k, DType t, const ChoiceArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-    if (cudaError_t e = ready(k, dev); e != cudaSuccess) return e;
-    const int c = split_of(t, a.rows, a.vocab, dev);
-    ChoiceArgs aa = a;
-    int cols = cols_of(a.vocab, c);
-    void *args[] = {&aa, &cols};
-    LaunchConfig l(capped(a.rows, a.grid_cap) * c, kThreads, c, false, s);
-    return cudaLaunchKernelExC(&l.cfg, k.fn, args);
+template <typename T>
+cudaError_t sample_as(ChoiceArgs a, const DeviceInfo &dev, cudaStream_t s) {
+    if (cudaError_t e = launch_steps(Kernels<T>::states(), a, a.rows, false, dev, s); e != cudaSuccess) return e;
+    void *args[] = {&a};
+    return launch(Kernels<T>::sample(), ctas_of(a.rows), true, s, args);
+}
+
+template <typename T>
+cudaError_t verify_as(ChoiceArgs a, const DeviceInfo &dev, cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
+    const bool drawn = a.draft_logits != nullptr;
+    if (a.rows > 0 && (e = launch_steps(Kernels<T>::states(), a, drawn ? 2 * a.rows : a.rows, false, dev, s))) return e;
+    void *args[] = {&a};
+    if ((e = launch(Kernels<T>::decide(), std::max<int64_t>(1, a.requests), a.rows > 0, s, args, kDecideThreads))) return e;
+    if (!drawn || a.rows == 0 || a.requests == 0) return e;
+    if ((e = launch_steps(Kernels<T>::residual(), a, a.requests, true, dev, s))) return e;
+    return launch(Kernels<T>::replace(), ctas_of(a.requests), true, s, args);
 }
 
 template <typename T>
@@ -798,28 +1058,39 @@ cudaError_t launch_route_any(DType t, const RouteArgs &a, bool grad, const Devic
 
 }  // namespace
 
-cudaError_t launch_sample(DType t, const ChoiceArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-    g_launched.note(dev);
-    Kernel &k = t == kF32    ? sample_kernel<float>()
-                : t == kBF16 ? sample_kernel<__nv_bfloat16>()
-                             : sample_kernel<__half>();
-    return launch_rows(k, t, a, dev, s);
+// The scratch: step states of the target rows, then of the draft rows, then the
+// rows' and the requests' own.
+int64_t choice_steps(DType t, int64_t vocab) {
+    const int N = 16 / elem_size(t);
+    return ((vocab + 2 * N - 2) / N + kStep - 1) / kStep;
+}
+int64_t choice_bytes(DType t, int64_t rows, int64_t vocab, int64_t requests) {
+    const int64_t states = 8 * rows * choice_steps(t, vocab);
+    return requests < 0 ? states : 2 * states + 16 * rows + static_cast<int64_t>(sizeof(Pending)) * requests;
+}
+static void lay_out(DType t, ChoiceArgs &a, void *work) {
+    a.steps = static_cast<int>(choice_steps(t, a.vocab));
+    a.states = static_cast<float2 *>(work);
+    a.row_states = reinterpret_cast<float4 *>(a.states + 2 * a.rows * a.steps);
+    a.pending = a.draft_logits ? reinterpret_cast<Pending *>(a.row_states + a.rows) : nullptr;
 }
 
-cudaError_t launch_verify(DType t, const ChoiceArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+cudaError_t launch_sample(DType t, const ChoiceArgs &a, void *work, const DeviceInfo &dev, cudaStream_t s) {
     g_launched.note(dev);
-    Kernel &k = t == kF32    ? verify_kernel<float>()
-                : t == kBF16 ? verify_kernel<__nv_bfloat16>()
-                             : verify_kernel<__half>();
-    if (a.rows > 0) {
-        if (cudaError_t e = launch_rows(k, t, a, dev, s); e != cudaSuccess) return e;
-    }
-    if (a.requests == 0) return cudaSuccess;
     ChoiceArgs aa = a;
-    void *args[] = {&aa};
-    const int64_t ctas = std::min<int64_t>((a.requests + kWarps - 1) / kWarps, 8 * static_cast<int64_t>(dev.sms));
-    LaunchConfig l(ctas, kThreads, 0, a.rows > 0, s);
-    return cudaLaunchKernelExC(&l.cfg, reinterpret_cast<const void *>(&k_verify_join), args);
+    lay_out(t, aa, work);
+    return t == kF32    ? sample_as<float>(aa, dev, s)
+           : t == kBF16 ? sample_as<__nv_bfloat16>(aa, dev, s)
+                        : sample_as<__half>(aa, dev, s);
+}
+
+cudaError_t launch_verify(DType t, const ChoiceArgs &a, void *work, const DeviceInfo &dev, cudaStream_t s) {
+    g_launched.note(dev);
+    ChoiceArgs aa = a;
+    lay_out(t, aa, work);
+    return t == kF32    ? verify_as<float>(aa, dev, s)
+           : t == kBF16 ? verify_as<__nv_bfloat16>(aa, dev, s)
+                        : verify_as<__half>(aa, dev, s);
 }
 
 cudaError_t launch_route(DType t, const RouteArgs &a, const DeviceInfo &dev, cudaStream_t s) {

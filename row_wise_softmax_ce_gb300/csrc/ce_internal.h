@@ -150,6 +150,12 @@ cudaError_t read_objective_status(unsigned long long out[2], const DeviceInfo &d
 cudaError_t reset_objective_status(const DeviceInfo &dev, cudaStream_t s);
 
 // -- the choices made from a row's softmax (ce_choices.cu) -----------------------
+// A request whose token is drawn from what its draft row leaves of a row (-1: none).
+struct Pending {
+    int64_t row;
+    float m, s, mq, sq;
+};
+
 // Arguments of sample_rows and verify_drafts; unused pointers are null.
 struct ChoiceArgs {
     const void *logits;
@@ -168,8 +174,11 @@ struct ChoiceArgs {
     const int64_t *offsets;
     int64_t requests;
     int64_t *accepted;  // [requests]
-    uint8_t *accepts;   // [rows] scratch
-    int64_t grid_cap;   // at most this many clusters (0: no cap)
+    // scratch
+    int steps;           // of a row
+    float2 *states;      // [2 rows, steps] (m, s)
+    float4 *row_states;  // [rows] (m, s) of a row and of its draft row
+    Pending *pending;    // [requests], or null: drafts that were not drawn
 };
 
 constexpr int kMaxExperts = 1024;
@@ -196,8 +205,10 @@ struct RouteArgs {
     int64_t grid_cap;
 };
 
-cudaError_t launch_sample(DType t, const ChoiceArgs &a, const DeviceInfo &dev, cudaStream_t s);
-cudaError_t launch_verify(DType t, const ChoiceArgs &a, const DeviceInfo &dev, cudaStream_t s);
+// bytes of scratch; requests < 0: of a sampling
+int64_t choice_bytes(DType t, int64_t rows, int64_t vocab, int64_t requests);
+cudaError_t launch_sample(DType t, const ChoiceArgs &a, void *work, const DeviceInfo &dev, cudaStream_t s);
+cudaError_t launch_verify(DType t, const ChoiceArgs &a, void *work, const DeviceInfo &dev, cudaStream_t s);
 cudaError_t launch_route(DType t, const RouteArgs &a, const DeviceInfo &dev, cudaStream_t s);
 cudaError_t launch_route_grad(DType t, const RouteArgs &a, const DeviceInfo &dev, cudaStream_t s);
 // nothing to read or reset on a device that has launched no choice

@@ -112,6 +112,20 @@ struct Vec<__half> {
     }
 };
 
+// Elements r .. r + N - 1 of the 2 N of two neighbouring vectors.
+template <typename T>
+__device__ __forceinline__ uint4 shift_pair(const uint4 &a, const uint4 &b, int r) {
+    const int bytes = r * static_cast<int>(sizeof(T));
+    const bool two = bytes & 8, one = bytes & 4;
+    const uint32_t w0 = two ? a.z : a.x, w1 = two ? a.w : a.y, w2 = two ? b.x : a.z, w3 = two ? b.y : a.w,
+                   w4 = two ? b.z : b.x, w5 = two ? b.w : b.y;
+    const uint32_t v0 = one ? w1 : w0, v1 = one ? w2 : w1, v2 = one ? w3 : w2, v3 = one ? w4 : w3, v4 = one ? w5 : w4;
+    if (sizeof(T) == 4) return make_uint4(v0, v1, v2, v3);
+    const int half = (bytes & 2) * 8;
+    return make_uint4(__funnelshift_r(v0, v1, half), __funnelshift_r(v1, v2, half), __funnelshift_r(v2, v3, half),
+                      __funnelshift_r(v3, v4, half));
+}
+
 // read-only 16 bytes read once: skip L1
 __device__ __forceinline__ uint4 ld_stream_u4(const uint4 *p) {
     uint4 v;

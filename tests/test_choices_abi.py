@@ -21,8 +21,8 @@ def lib():
 
 
 def sample(lib, logits=V(4096), dtype=0, rows=4, cols=10, stride=10, uniforms=V(512), t=1.0, temps=None,
-           tokens=V(1 << 20), logp=None):
-    return lib.sample_rows(logits, dtype, rows, cols, stride, uniforms, t, temps, tokens, logp, None)
+           tokens=V(1 << 20), logp=None, work=V(1 << 22)):
+    return lib.sample_rows(logits, dtype, rows, cols, stride, uniforms, t, temps, tokens, logp, work, None)
 
 
 def verify(lib, logits=V(4096), dtype=0, rows=4, cols=10, stride=10, drafts=V(512), q=V(8192), qs=10, offsets=V(1024),
@@ -75,14 +75,27 @@ def test_temperatures(lib, call):
         assert call(lib, t=0.0) == ce.CE_EDEVICE
 
 
-@pytest.mark.parametrize("bad", [dict(uniforms=None), dict(tokens=None)], ids=str)
+@pytest.mark.parametrize("bad", [dict(uniforms=None), dict(tokens=None), dict(work=None)], ids=str)
 def test_sample_arguments_refused(lib, bad):
     assert sample(lib, **bad) == ce.CE_EINVAL
 
 
-@pytest.mark.parametrize("bad", [dict(uniforms=V(514)), dict(tokens=V((1 << 20) + 4)), dict(logp=V(1026))], ids=str)
+@pytest.mark.parametrize("bad", [dict(uniforms=V(514)), dict(tokens=V((1 << 20) + 4)), dict(logp=V(1026)), dict(work=V(1032))],
+                         ids=str)
 def test_sample_alignment_refused(lib, bad):
     assert sample(lib, **bad) == ce.CE_EALIGN
+
+
+def test_scratch(lib):
+    """Enough for a row's steps of 256 vectors of 16 bytes at any phase, 8 bytes each."""
+    for dtype, n in ((0, 4), (1, 8), (2, 8)):
+        for vocab in (1, n, 256 * n, 256 * n + 1, 50257, 1 << 24):
+            steps = -(-((vocab + n - 1 + n - 1) // n) // 256)
+            assert lib.choice_work(dtype, 3, vocab, -1) >= 24 * steps
+            assert lib.choice_work(dtype, 3, vocab, 5) >= 48 * steps + 48 + 5 * 24
+    assert lib.choice_work(1, 0, 10, -1) == 0
+    for bad in ((3, 1, 10, 0), (0, -1, 10, 0), (0, 1, 0, 0), (0, 1, HUGE, 0), (0, 1, 10, -2), (0, 1 << 61, 1 << 20, 0)):
+        assert lib.choice_work(*bad) == ce.CE_EINVAL
 
 
 @pytest.mark.parametrize("bad", [dict(drafts=None), dict(offsets=None), dict(uniforms=None), dict(accepted=None),
@@ -94,7 +107,7 @@ def test_verify_arguments_refused(lib, bad):
 
 @pytest.mark.parametrize("bad", [dict(drafts=V(516)), dict(offsets=V(1028)), dict(uniforms=V(2050)),
                                  dict(accepted=V((1 << 20) + 4)), dict(tokens=V((1 << 21) + 4)), dict(logp=V(1026)),
-                                 dict(q=V(8194))], ids=str)
+                                 dict(q=V(8194)), dict(work=V(1032))], ids=str)
 def test_verify_alignment_refused(lib, bad):
     assert verify(lib, **bad) == ce.CE_EALIGN
 
@@ -141,10 +154,11 @@ def test_outputs_over_the_rest_refused(lib):
         assert sample(lib, temps=V(1024), tokens=V(where)) == ce.CE_EINVAL
     assert sample(lib, logp=V((1 << 20) + 16)) == ce.CE_EINVAL
     for name in ("accepted", "tokens", "logp", "work"):
-        for where in (512 + 8, 1024 + 16, 2048 + 24, 4096 + 80, 8192 + 80, 16384 + 8):
+        for where in (512 + 16, 1024 + 16, 2048 + 16, 4096 + 80, 8192 + 80, 16384):
             assert verify(lib, temps=V(16384), **{name: V(where)}) == ce.CE_EINVAL, (name, where)
     assert verify(lib, logp=V((1 << 21) + 16)) == ce.CE_EINVAL
-    assert verify(lib, work=V((1 << 20) + 8)) == ce.CE_EINVAL
+    assert verify(lib, work=V((1 << 20) - 16)) == ce.CE_EINVAL
+    assert sample(lib, work=V((1 << 20) - 16)) == ce.CE_EINVAL and sample(lib, work=V(4096 + 160 - 16)) == ce.CE_EINVAL
     for name in ("chosen", "gates", "counts"):
         for where in (512 + 8, 1024 + 8, 4096 + 96):
             assert route(lib, bias=V(512), weights=V(1024), **{name: V(where)}) == ce.CE_EINVAL, (name, where)
@@ -164,7 +178,7 @@ def test_accepted_calls_reach_the_device_check(lib):
     assert verify(lib, q=None, qs=0) == ce.CE_EDEVICE                                 # drafts that were looked up
     assert route(lib, groups=4, top_groups=2, k=6) == ce.CE_EDEVICE
     # nothing to do
-    assert sample(lib, rows=0, logits=None, uniforms=None, tokens=None) == ce.CE_OK
+    assert sample(lib, rows=0, logits=None, uniforms=None, tokens=None, work=None) == ce.CE_OK
     assert verify(lib, rows=0, requests=0, logits=None, drafts=None, q=None, uniforms=None, accepted=None, tokens=None,
                   work=None) == ce.CE_OK
     assert verify(lib, rows=0, logits=None, drafts=None, q=None, uniforms=None, tokens=None, work=None) == ce.CE_EDEVICE
