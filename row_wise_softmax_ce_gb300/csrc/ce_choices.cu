@@ -12,12 +12,9 @@
 //                   number of warps
 //   k_sample        sample_rows: a warp per row merges its states, draws a step by
 //                   their masses and re-reads that step
-//   k_decide        verify_drafts: a CTA per request merges its rows' states, finds
-//                   the first that accepts no draft and draws from p where the
-//                   token comes from p
-//   k_residual      the other requests' rows again: what max(0, p - q) leaves of
-//                   each step
-//   k_replace       their token: a warp per request draws a step and re-reads it
+//   k_decide        verify_drafts: a cluster per request merges its rows' states,
+//                   finds the first that accepts no draft, and draws its token: from
+//                   p, or from max(0, p - q), which reads the two rows once more
 //   k_route         route_rows, a warp per row
 //   k_route_grad    route_grad, a warp per row
 #include <algorithm>
@@ -39,7 +36,7 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kScan = 8;  // 16-byte loads in flight per thread
 constexpr int kStep = 32 * kScan;  // vectors of a step, 4 KB
-constexpr int kDecideThreads = 256;
+constexpr int kDrawThreads = 32 * kScan;
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -131,29 +128,42 @@ struct RowGrid {
     __device__ float at(int j) const { return Vec<T>::to_float(p[j]); }
 };
 
-// What a column weighs in a draw.
-enum Kind : int {
-    kShare = 0,     // 2^((x - m) k)
-    kGreedy = 1,    // 1 where x is the row's largest value, else 0
-    kResidual = 2,  // max(0, p - q)
-    kOthers = 3,    // 2^((x - m) k), the drafted column 0
-};
+// What a column weighs in a draw: 2^((x - m) k), a looked-up draft's column
+// (skip) 0; or, kResidual, what its draft row leaves of it, max(0, p - q).
 struct Weigh {
-    Kind kind;
-    float m, k;           // the row's
-    float rp, mq, rq;     // kResidual: 1 / s, and the draft row's max and 1 / s
-    int skip;             // kOthers: the drafted column
-    __device__ float unit() const { return kind == kResidual ? kUnitShares : kUnitWeights; }
-    __device__ float residual(float x, float y) const {
-        // two rounded products: rows that are the same leave exactly nothing
-        return fmaxf(0.0f, __fsub_rn(__fmul_rn(ex2_ftz((x - m) * k), rp), __fmul_rn(ex2_ftz((y - mq) * k), rq)));
-    }
-    __device__ float operator()(float x, float y, int j) const {
-        if (kind == kGreedy) return x == m ? 1.0f : 0.0f;
-        if (kind == kResidual) return residual(x, y);
-        return kind == kOthers && j == skip ? 0.0f : ex2_ftz((x - m) * k);
-    }
+    float m, k;        // the row's
+    int skip;          // -1: none
+    float c, mq, cq;   // kResidual: -log2 s, the draft row's max and its -log2 s
 };
+
+// The weights of a vector's columns, from column j on; x - m first, as the
+// row's states take it.
+template <typename T, bool kResidual>
+__device__ __forceinline__ void weights_of(float (&e)[Vec<T>::kN], const uint4 &x, const uint4 &y, int j, const Weigh &w) {
+    const float2 nm = make_float2(-w.m, -w.m), kk = make_float2(w.k, w.k);
+#pragma unroll
+    for (int i = 0; i < Vec<T>::kN / 2; ++i) {
+        const float2 dx = __fadd2_rn(Vec<T>::pair(x, i), nm);
+        if (kResidual) {
+            // both by the same instructions: rows that are the same leave exactly nothing
+            const float2 dy = __fadd2_rn(Vec<T>::pair(y, i), make_float2(-w.mq, -w.mq));
+            const float2 p = __ffma2_rn(dx, kk, make_float2(w.c, w.c)), q = __ffma2_rn(dy, kk, make_float2(w.cq, w.cq));
+            e[2 * i] = fmaxf(0.0f, ex2_ftz(p.x) - ex2_ftz(q.x));
+            e[2 * i + 1] = fmaxf(0.0f, ex2_ftz(p.y) - ex2_ftz(q.y));
+        } else {
+            const float2 p = __fmul2_rn(dx, kk);
+            e[2 * i] = j + 2 * i == w.skip ? 0.0f : ex2_ftz(p.x);
+            e[2 * i + 1] = j + 2 * i + 1 == w.skip ? 0.0f : ex2_ftz(p.y);
+        }
+    }
+}
+template <int kN>
+__device__ __forceinline__ float sum_of(const float (&e)[kN]) {
+    float2 s = make_float2(e[0], e[1]);
+#pragma unroll
+    for (int i = 2; i < kN; i += 2) s = __fadd2_rn(s, make_float2(e[i], e[i + 1]));
+    return s.x + s.y;
+}
 
 // The columns of a draft row beside a row's: its vectors, or parts of two of
 // them where the two rows start at different phases of 16 bytes.
@@ -191,17 +201,6 @@ __device__ __noinline__ uint4 columns_from(const T *p, int n, int j) {
     return v;
 }
 
-template <typename T>
-__device__ __forceinline__ float weight_of(const uint4 &x, const uint4 &y, int j, const Weigh &w) {
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < Vec<T>::kN / 2; ++i) {
-        const float2 xx = Vec<T>::pair(x, i), yy = Vec<T>::pair(y, i);
-        sum += w(xx.x, yy.x, j + 2 * i) + w(xx.y, yy.y, j + 2 * i + 1);
-    }
-    return sum;
-}
-
 // Walking kN segments of one lane: the one that holds t, and t from its start on;
 // for a t behind the last mass the last that weighs anything.
 template <int kN>
@@ -219,68 +218,84 @@ __device__ __forceinline__ int walk(const float (&w)[kN], float unit, Mass &t) {
     return at;
 }
 
-// The column of step `step` whose weight holds t, and its logit: eight vectors
-// next to one another in each lane, so one running sum over the lanes, then the
-// lane's vectors and the vector's columns. All of a warp; column -1 if nothing
-// weighs anything. kBeside: weights of p and q, else of p alone.
+// The column of step `step` whose weight holds t, and its logit, by a CTA of
+// kScan warps: a warp weighs 32 of the step's vectors, a lane one; every warp
+// finds the warp that holds t, and that one the lane and the lane the column:
+// one latency, and eight weights a lane where a warp alone would take 64 (a
+// draw of a step by one warp: 4 us, of a residual 6 us). `mine` in that warp
+// only; its column is -1 if nothing weighs anything.
 struct Found {
+    bool mine;
     int column;
     float x;
 };
-template <typename T, bool kBeside>
-__device__ __forceinline__ Found column_of(const RowGrid<T> &g, const RowGrid<T> &d, int step, const Weigh &w, Mass t) {
+template <typename T, bool kResidual>
+__device__ __forceinline__ Found column_of(const RowGrid<T> &g, const RowGrid<T> &d, int step, const Weigh &w, Mass t,
+                                           float *sums) {
     constexpr int N = Vec<T>::kN;
-    const int lane = threadIdx.x & 31, q = step * kStep + kScan * lane;
+    constexpr float kUnit = kResidual ? kUnitShares : kUnitWeights;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = step * kStep + 32 * warp + lane;
     const Beside<T> beside(g, d);
-    uint4 x[kScan], y[kBeside ? kScan : 1];
-#pragma unroll
-    for (int u = 0; u < kScan; ++u) {
-        x[u] = Vec<T>::lowest();
-        if (g.whole(q + u)) x[u] = g.load_cached(q + u);
-        if (kBeside) {
-            y[u] = Vec<T>::lowest();
-            if (beside.whole(q + u, q + u + 1)) y[u] = beside.load_cached(q + u);
-        }
+    uint4 x = Vec<T>::lowest(), y = x;
+    if (g.whole(q))
+        x = g.load(q);
+    else if (q < g.nq)
+        x = columns_from(g.p, g.n, g.column(q));
+    if (kResidual) {
+        if (beside.whole(q, q + 1))
+            y = beside.load(q);
+        else if (q < g.nq)
+            y = columns_from(d.p, d.n, g.column(q));
     }
-    // partial vectors, and columns that lie in one of the draft row's
+    float e[N];
+    weights_of<T, kResidual>(e, x, y, g.column(q), w);
+    const float mine = sum_of(e), all = warp_sum(mine);
+    if (lane == 0) sums[warp] = all;
+    __syncthreads();
+    float of[kScan];
 #pragma unroll
-    for (int u = 0; u < kScan; ++u)
-        if (q + u < g.nq) {
-            if (!g.whole(q + u)) x[u] = columns_from(g.p, g.n, g.column(q + u));
-            if (kBeside && !beside.whole(q + u, q + u + 1)) y[u] = columns_from(d.p, d.n, g.column(q + u));
-        }
-    float sum[kScan], all = 0.0f;
-    Mass m = 0;
-#pragma unroll
-    for (int u = 0; u < kScan; ++u) {
-        sum[u] = weight_of<T>(x[u], kBeside ? y[u] : x[u], g.column(q + u), w);
-        all += sum[u];
-        m += mass_of(sum[u], w.unit());
-    }
-    const int l = warp_segment(m, all, t);
-    if (l < 0) return Found{-1, 0.0f};
-    const int u = walk(sum, w.unit(), t);
-    uint4 xu = x[0], yu = y[0];
-#pragma unroll
-    for (int i = 1; i < kScan; ++i)
-        if (i == u) {
-            xu = x[i];
-            if (kBeside) yu = y[i];
-        }
-    float e[N], xs[N];
+    for (int i = 0; i < kScan; ++i) of[i] = sums[i];
+    if (walk(of, kUnit, t) != warp) return Found{false, -1, 0.0f};
+    const int l = warp_segment(mass_of(mine, kUnit), mine, t);
+    if (l < 0) return Found{true, -1, 0.0f};
+    const int at = walk(e, kUnit, t);
+    float found = 0.0f;
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
-        const float2 xx = Vec<T>::pair(xu, i), yy = Vec<T>::pair(kBeside ? yu : xu, i);
-        const int j = g.column(q + u) + 2 * i;
-        xs[2 * i] = xx.x, xs[2 * i + 1] = xx.y;
-        e[2 * i] = w(xx.x, yy.x, j), e[2 * i + 1] = w(xx.y, yy.y, j + 1);
+        const float2 xx = Vec<T>::pair(x, i);
+        if (2 * i == at) found = xx.x;
+        if (2 * i + 1 == at) found = xx.y;
     }
-    const int at = walk(e, w.unit(), t);
-    float found = xs[0];
+    return Found{true, __shfl_sync(kFullMask, g.column(q) + at, l), __shfl_sync(kFullMask, found, l)};
+}
+
+// The first column of step `step` that holds m, by a warp.
+template <typename T>
+__device__ __forceinline__ int first_of(const RowGrid<T> &g, int step, float m) {
+    constexpr int N = Vec<T>::kN;
+    const int lane = threadIdx.x & 31;
+    uint4 x[kScan];
 #pragma unroll
-    for (int i = 1; i < N; ++i)
-        if (i == at) found = xs[i];
-    return Found{__shfl_sync(kFullMask, g.column(q + u) + at, l), __shfl_sync(kFullMask, found, l)};
+    for (int u = 0; u < kScan; ++u) {
+        const int q = step * kStep + 32 * u + lane;
+        x[u] = g.whole(q) ? g.load(q) : Vec<T>::lowest();
+    }
+#pragma unroll 1
+    for (int u = 0; u < kScan; ++u) {
+        const int q = step * kStep + 32 * u + lane;
+        if (q < g.nq && !g.whole(q)) x[0] = columns_from(g.p, g.n, g.column(q));
+        unsigned at = 0;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const float2 xx = Vec<T>::pair(x[0], i);
+            at |= (xx.x == m ? 1u : 0u) << (2 * i) | (xx.y == m ? 2u : 0u) << (2 * i);
+        }
+        const unsigned some = __ballot_sync(kFullMask, at != 0);
+        if (some) return __shfl_sync(kFullMask, g.column(q) + __ffs(at) - 1, __ffs(some) - 1);
+#pragma unroll
+        for (int i = 0; i + 1 < kScan; ++i) x[i] = x[i + 1];
+    }
+    return -1;
 }
 
 // One step of a scan: vectors q .. q + kStep - 1 (those below nq) into a state,
@@ -410,20 +425,22 @@ struct Steps {
     const float2 *p;
     int n, cnt, first;
     float2 held[kHeld];
+    // past L1: another SM has written them, and may write over them
     __device__ Steps(const float2 *states, int steps) : p(states), n(steps) {
         cnt = (steps + 31) / 32;
         first = static_cast<int>(threadIdx.x & 31) * cnt;
 #pragma unroll
         for (int i = 0; i < kHeld; ++i)
-            held[i] = i < cnt && first + i < n ? p[first + i] : make_float2(-INFINITY, 0.0f);
+            held[i] = i < cnt && first + i < n ? __ldcg(p + first + i) : make_float2(-INFINITY, 0.0f);
     }
     // fn(state, i) for each of the lane's steps i, in order
     template <typename Fn>
     __device__ __forceinline__ void each(Fn fn) const {
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) fn(held[i], i);
+        for (int i = 0; i < kHeld; ++i)
+            if (i < cnt) fn(held[i], i);
         for (int i = kHeld; i < cnt; ++i)
-            if (first + i < n) fn(p[first + i], i);
+            if (first + i < n) fn(__ldcg(p + first + i), i);
     }
     __device__ TokState merged(float k) const {
         float m = -INFINITY, s = 0.0f;
@@ -457,53 +474,82 @@ struct Steps {
 };
 __device__ __forceinline__ bool is_distribution(const TokState &st) { return isfinite(st.m) && !isnan(st.s); }
 
-// The column that u draws from a row by its own weights (greedy: its first
-// largest), without w.skip for kOthers; column -1 if nothing weighs anything.
+// The row's first largest column: the first step that comes to it.
 template <typename T>
-__device__ __forceinline__ Found draw_own(const RowGrid<T> &g, const Steps &steps, const Weigh &w, float u) {
-    Mass t;
-    const int step = steps.draw(kUnitWeights, w.kind == kGreedy ? 0.0f : u, [&](float2 v) {
-        return w.kind == kGreedy ? (v.x == w.m ? 1.0f : 0.0f) : v.y * ex2_ftz((v.x - w.m) * w.k);
-    }, t);
-    return step < 0 ? Found{-1, 0.0f} : column_of<T, false>(g, g, step, w, t);
+__device__ __forceinline__ int first_largest(const RowGrid<T> &g, const Steps &steps, float m) {
+    int mine = -1;
+    steps.each([&](float2 v, int i) {
+        if (mine < 0 && v.x == m) mine = steps.first + i;
+    });
+    const unsigned some = __ballot_sync(kFullMask, mine >= 0);
+    return some ? first_of(g, __shfl_sync(kFullMask, mine, __ffs(some) - 1), m) : -1;
+}
+
+// The step that u of a row's own weights falls in.
+__device__ __forceinline__ int own_step(const Steps &steps, const Weigh &w, float u, Mass &t) {
+    return steps.draw(kUnitWeights, u, [&](float2 v) { return v.y * ex2_ftz((v.x - w.m) * w.k); }, t);
 }
 
 __device__ __forceinline__ float logp_of(float x, const TokState &st, const Heat &heat) {
     return heat.greedy ? 0.0f : (x - st.m) * heat.inv_t - logf(st.s);
 }
 
-// k_sample: a warp per row, behind k_states.
+// k_sample: a CTA of kScan warps per row, behind k_states. The first warp merges
+// the row's states and finds the step.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_sample(ChoiceArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t row = blockIdx.x * int64_t(kWarps) + (threadIdx.x >> 5);
-    if (row >= a.rows) return;
+__global__ void __launch_bounds__(kDrawThreads) k_sample(ChoiceArgs a) {
+    __shared__ float sums[kScan];
+    __shared__ TokState row_state;
+    __shared__ int row_step;
+    __shared__ Mass row_t;
+    const int64_t row = blockIdx.x;
     const RowGrid<T> g = target_row<T>(a, row);
     const Heat heat(temperature_of(a, row));
     const float u = a.uniforms[row];
     wait_prerequisites();
-    const Steps steps(states_of(a, row), a.steps);
-    const TokState st = steps.merged(heat.k);
-    Found f{-1, 0.0f};
-    if (heat.ok && is_distribution(st)) {
-        Weigh w{};
-        w.kind = heat.greedy ? kGreedy : kShare;
-        w.m = st.m;
-        w.k = heat.k;
-        f = draw_own(g, steps, w, u);
+    Weigh w{0.0f, heat.k, -1, 0.0f, 0.0f, 0.0f};
+    if (threadIdx.x < 32) {
+        const Steps steps(states_of(a, row), a.steps);
+        const TokState st = steps.merged(heat.k);
+        int step = -1, column = -1;
+        Mass t = 0;
+        if (heat.ok && is_distribution(st)) {
+            w.m = st.m;
+            if (heat.greedy)
+                column = first_largest(g, steps, st.m);
+            else
+                step = own_step(steps, w, u, t);
+        }
+        if (threadIdx.x == 0) {
+            row_state = st;
+            row_step = step;
+            row_t = t;
+            if (step < 0) {
+                a.tokens[row] = column;
+                if (a.logp) a.logp[row] = column < 0 ? nan_f() : 0.0f;
+                if (column < 0) count_bad();
+            }
+        }
     }
-    if (lane == 0) {
-        a.tokens[row] = f.column;
-        if (a.logp) a.logp[row] = f.column < 0 ? nan_f() : logp_of(f.x, st, heat);
-        if (f.column < 0) count_bad();
-    }
+    __syncthreads();
+    if (row_step < 0) return;
+    const TokState st = row_state;
+    w.m = st.m;
+    const Found f = column_of<T, false>(g, g, row_step, w, row_t, sums);
+    if (!f.mine || (threadIdx.x & 31) != 0) return;
+    a.tokens[row] = f.column;
+    if (a.logp) a.logp[row] = f.column < 0 ? nan_f() : logp_of(f.x, st, heat);
 }
 
-// k_decide: a CTA per request, behind k_states. Its warps judge a row each, in
-// order, until one accepts no draft; the token of that row is drawn here where
-// it comes from p, and left to k_residual and k_replace where it comes from what
-// q leaves of p.
-enum Verdict : int { kAccepted = 0, kDrawn = 1, kPending = 2 };
+// What becomes of a row: its draft is accepted; or it ends its request, with a
+// token that is known, that comes from p, or that comes from what q leaves of p.
+enum Verdict : int { kAccepted = 0, kKnown = 1, kFromOwn = 2, kFromRest = 3 };
+struct Open {  // of a row whose token is still to be drawn
+    Weigh w;
+    float inv_t, s, u;
+    int step;  // kFromOwn: the step it lies in, and t from its start on
+    Mass t;
+};
 
 // A row's own inputs, asked for before the states are there.
 struct RowNumbers {
@@ -527,9 +573,8 @@ __device__ __forceinline__ RowNumbers row_numbers(const ChoiceArgs &a, int64_t r
 }
 
 template <typename T>
-__device__ __forceinline__ Verdict judge(const ChoiceArgs &a, int64_t row, const RowNumbers &r) {
+__device__ __forceinline__ Verdict judge(const ChoiceArgs &a, int64_t row, const RowNumbers &r, bool writes, Open *open) {
     const int lane = threadIdx.x & 31;
-    const RowGrid<T> g = target_row<T>(a, row);
     const Heat heat(r.temperature);
     const bool drafted = r.d >= 0 && !heat.greedy, lookup = drafted && a.draft_logits == nullptr;
     const Steps steps(states_of(a, row), a.steps);
@@ -537,51 +582,102 @@ __device__ __forceinline__ Verdict judge(const ChoiceArgs &a, int64_t row, const
     if (drafted && !lookup) q = Steps(draft_states_of(a, row), a.steps).merged(heat.k);
     TokState p = steps.merged(heat.k);
     if (lookup) tok_push1<false>(p, r.xd, heat.k);  // its column is not among the states
-    Weigh w{};
-    w.kind = heat.greedy ? kGreedy : lookup ? kOthers : kShare;
-    w.m = p.m;
-    w.k = heat.k;
-    w.skip = r.d;
-    bool odd = r.draft >= a.vocab, accepted = false, drawn = false;
-    Found f{-1, 0.0f};
+    Verdict v = kKnown;
+    bool odd = r.draft >= a.vocab;
+    int token = -1;
     float logp = 0.0f;
     if (!heat.ok || !is_distribution(p)) {
         odd = true;
         logp = nan_f();
+    } else if (heat.greedy) {
+        token = first_largest(target_row<T>(a, row), steps, p.m);
+        if (token == r.d) v = kAccepted;
     } else {
-        if (drafted) {
-            const bool from = lookup || is_distribution(q);  // else not accepted, the token drawn from p
-            odd |= !from;
-            const float qd = lookup ? 1.0f : ex2_ftz((r.yd - q.m) * heat.k) / q.s;
-            accepted = from && r.accept * qd < ex2_ftz((r.xd - p.m) * heat.k) / p.s;
-            drawn = from && !lookup && !accepted;
-            if (accepted) f = Found{r.d, r.xd};
+        Open o{};
+        o.w = Weigh{p.m, heat.k, lookup ? r.d : -1, -log2f(p.s), q.m, -log2f(q.s)};
+        o.inv_t = heat.inv_t;
+        o.s = p.s;
+        o.u = r.u;
+        o.step = -1;
+        const bool from = drafted && (lookup || is_distribution(q));  // else not accepted, the token drawn from p
+        odd |= drafted && !from;
+        const float qd = lookup ? 1.0f : ex2_ftz((r.yd - q.m) * heat.k) / q.s;
+        if (from && r.accept * qd < ex2_ftz((r.xd - p.m) * heat.k) / p.s) {
+            v = kAccepted;
+        } else if (from && !lookup) {
+            v = kFromRest;
+        } else {
+            o.step = own_step(steps, o.w, r.u, o.t);
+            if (o.step >= 0) v = kFromOwn;  // else nothing but the draft weighs anything
         }
-        if (!accepted && !drawn) {
-            f = draw_own(g, steps, w, r.u);
-            if (f.column < 0) f = Found{r.d, r.xd};  // nothing but the draft weighs anything
-            accepted = heat.greedy && f.column == r.d;
+        if (v == kAccepted || v == kKnown) {
+            token = r.d;
+            logp = logp_of(r.xd, p, heat);
+        } else if (lane == 0) {
+            *open = o;
         }
-        if (!drawn) logp = logp_of(f.x, p, heat);
     }
-    if (lane == 0) {
-        a.tokens[row] = f.column;
-        if (a.logp) a.logp[row] = logp;
-        if (drawn) a.row_states[row] = make_float4(p.m, p.s, q.m, q.s);
+    if (lane == 0 && writes) {
+        if (v == kAccepted || v == kKnown) {
+            a.tokens[row] = token;
+            if (a.logp) a.logp[row] = logp;
+        }
         if (odd) count_bad();
     }
-    return accepted ? kAccepted : drawn ? kPending : kDrawn;
+    return v;
 }
 
+// max(0, p - q) added over the columns of a step; all of a warp.
 template <typename T>
-__global__ void __launch_bounds__(kDecideThreads) k_decide(ChoiceArgs a) {
-    constexpr int kRows = kDecideThreads / 32;
+__device__ __forceinline__ float residual_of_step(const RowGrid<T> &g, const RowGrid<T> &d, const Beside<T> &beside, int step,
+                                                  const Weigh &w) {
+    constexpr int kU = kScan / 2;
+    const int lane = threadIdx.x & 31, end = min(g.nq, (step + 1) * kStep);
+    float sum = 0.0f;
+    float e[Vec<T>::kN];
+#pragma unroll 1
+    for (int q = step * kStep; q < end; q += 32 * kU) {
+        const int to = min(end, q + 32 * kU);
+        if (g.whole(q, to) && beside.whole(q, to)) {
+            uint4 x[kU], y[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int v = q + 32 * u + lane;
+                x[u] = v < to ? g.load(v) : Vec<T>::lowest();
+                y[u] = v < to ? beside.load(v) : Vec<T>::lowest();
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                weights_of<T, true>(e, x[u], y[u], 0, w);
+                sum += sum_of(e);
+            }
+        } else {
+            for (int v = q + lane; v < to; v += 32) {
+                const int j = g.column(v);
+                weights_of<T, true>(e, columns_from(g.p, g.n, j), columns_from(d.p, d.n, j), 0, w);
+                sum += sum_of(e);
+            }
+        }
+    }
+    return warp_sum(sum);
+}
+
+// k_decide: a cluster per request, behind k_states. Every CTA's warps judge a row
+// each, in order, until one accepts no draft (the CTAs of a cluster come to the
+// same; the first writes). That row's token is then drawn: from p by the first
+// CTA; where it comes from what q leaves of p, the cluster's warps add that up
+// over the row's steps first.
+template <typename T>
+__global__ void __launch_bounds__(kDrawThreads, 4) k_decide(ChoiceArgs a) {
+    constexpr int kRows = kDrawThreads / 32;
     __shared__ int verdicts[kRows];
-    launch_dependents();
+    __shared__ Open opens[kRows];
+    __shared__ float sums[kScan];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t s = blockIdx.x, lo = a.offsets[0], hi = a.offsets[a.requests];
+    const uint32_t rank = cluster_rank(), C = cluster_size();
+    const int64_t s = cluster_id_x(), lo = a.offsets[0], hi = a.offsets[a.requests];
     const int64_t r0 = s < a.requests ? a.offsets[s] : 0, r1 = s < a.requests ? a.offsets[s + 1] : 0;
-    const bool good = r0 >= 0 && r1 >= r0 && r1 <= a.rows;
+    const bool good = r0 >= 0 && r1 >= r0 && r1 <= a.rows, writes = rank == 0;
     auto silent = [&](int64_t row) {
         a.tokens[row] = -1;
         if (a.logp) a.logp[row] = 0.0f;
@@ -591,19 +687,20 @@ __global__ void __launch_bounds__(kDecideThreads) k_decide(ChoiceArgs a) {
     RowNumbers numbers{};
     if (has_states(r0 + warp)) numbers = row_numbers<T>(a, r0 + warp);
     wait_prerequisites();
-    if (s == 0)  // rows in no request
-        for (int64_t r = threadIdx.x; r < a.rows; r += kDecideThreads)
+    if (s == 0 && writes)  // rows in no request
+        for (int64_t r = threadIdx.x; r < a.rows; r += kDrawThreads)
             if (r < lo || r >= hi) silent(r);
     if (s >= a.requests) return;
-    Pending pending{-1, 0.0f, 0.0f, 0.0f, 0.0f};
     int64_t stop = good ? -1 : 0;
+    int by = -1;  // the warp that judged a row whose token is still to be drawn
     for (int64_t r = r0; good && r < r1 && stop < 0; r += kRows) {
         const int64_t row = r + warp;
-        Verdict v = kDrawn;
+        Verdict v = kKnown;
+        if (r > r0) __syncthreads();  // the verdicts before have been read
         if (has_states(row)) {
             if (r > r0) numbers = row_numbers<T>(a, row);
-            v = judge<T>(a, row, numbers);
-        } else if (row < r1 && lane == 0) {
+            v = judge<T>(a, row, numbers, writes, &opens[warp]);
+        } else if (row < r1 && writes && lane == 0) {
             silent(row);
         }
         if (lane == 0) verdicts[warp] = v;
@@ -611,115 +708,65 @@ __global__ void __launch_bounds__(kDecideThreads) k_decide(ChoiceArgs a) {
         for (int i = 0; i < kRows && r + i < r1; ++i)
             if (verdicts[i] != kAccepted) {
                 stop = r + i;
-                if (verdicts[i] == kPending) {
-                    const float4 st = a.row_states[stop];
-                    pending = Pending{stop, st.x, st.y, st.z, st.w};
-                }
+                if (verdicts[i] != kKnown) by = i;
                 break;
             }
-        __syncthreads();
     }
     if (stop < 0) stop = r1;
-    if (threadIdx.x == 0) {
-        a.accepted[s] = good ? stop - r0 : -1;
-        if (a.pending) a.pending[s] = pending;
-        if (!good) count_bad();
-    }
-    for (int64_t r = stop + 1 + threadIdx.x; good && r < r1; r += kDecideThreads) silent(r);
-}
-
-__device__ __forceinline__ Weigh residual_of(const Pending &p, const Heat &heat) {
-    Weigh w{};
-    w.kind = kResidual;
-    w.m = p.m;
-    w.k = heat.k;
-    w.rp = 1.0f / p.s;
-    w.mq = p.mq;
-    w.rq = 1.0f / p.sq;
-    w.skip = -1;
-    return w;
-}
-
-// k_residual: a warp per `unit` steps of a pending request's row: the sum of
-// max(0, p - q) over each step, over the draft row's states, which have served.
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 6) k_residual(ChoiceArgs a, int unit, int units, int64_t warps) {
-    constexpr int N = Vec<T>::kN, kU = kScan / 2, kHalf = 32 * kU;
-    launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int64_t id = blockIdx.x * int64_t(kWarps) + (threadIdx.x >> 5);
-    wait_prerequisites();
-    if (id >= warps) return;
-    const int64_t s = id / units;
-    const int first = static_cast<int>(id - s * units) * unit;
-    const Pending p = a.pending[s];
-    if (p.row < 0) return;
-    const RowGrid<T> g = target_row<T>(a, p.row), d = draft_row<T>(a, p.row);
-    const Beside<T> beside(g, d);
-    const Weigh w = residual_of(p, Heat(temperature_of(a, p.row)));
-    float mine = 0.0f;
-    for (int i = 0; i < unit; ++i) {
-        float sum = 0.0f;
-        for (int q = (first + i) * kStep; q < min(g.nq, (first + i + 1) * kStep); q += kHalf) {
-            const int end = min(g.nq, q + kHalf);
-            if (g.whole(q, end) && beside.whole(q, end)) {
-                uint4 x[kU], y[kU];
-#pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    const int v = q + 32 * u + lane;
-                    x[u] = v < end ? g.load(v) : Vec<T>::lowest();
-                    y[u] = v < end ? beside.load(v) : Vec<T>::lowest();
-                }
-#pragma unroll
-                for (int u = 0; u < kU; ++u)
-#pragma unroll
-                    for (int h = 0; h < N / 2; ++h) {
-                        const float2 xx = Vec<T>::pair(x[u], h), yy = Vec<T>::pair(y[u], h);
-                        sum += w.residual(xx.x, yy.x) + w.residual(xx.y, yy.y);
-                    }
-            } else {
-                for (int v = q + lane; v < end; v += 32) {
-                    const int j = g.column(v);
-                    sum += weight_of<T>(columns_from(g.p, g.n, j), columns_from(d.p, d.n, j), j, w);
-                }
-            }
+    if (writes) {
+        if (threadIdx.x == 0) {
+            a.accepted[s] = good ? stop - r0 : -1;
+            if (!good) count_bad();
         }
-        sum = warp_sum(sum);
-        if (lane == i) mine = sum;
+        for (int64_t r = stop + 1 + threadIdx.x; good && r < r1; r += kDrawThreads) silent(r);
     }
-    if (lane < unit && first + lane < a.steps) draft_states_of(a, p.row)[first + lane].x = mine;
-}
-
-// k_replace: a warp per request.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) k_replace(ChoiceArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t s = blockIdx.x * int64_t(kWarps) + (threadIdx.x >> 5);
-    wait_prerequisites();
-    if (s >= a.requests) return;
-    const Pending p = a.pending[s];
-    if (p.row < 0) return;
-    const RowGrid<T> g = target_row<T>(a, p.row), d = draft_row<T>(a, p.row);
-    const Heat heat(temperature_of(a, p.row));
-    Weigh w = residual_of(p, heat);
-    const float u = a.uniforms[2 * p.row + 1];
-    const Steps sums(draft_states_of(a, p.row), a.steps);
-    Mass t;
-    const int step = sums.draw(kUnitShares, u, [&](float2 v) { return v.x; }, t);
-    Found f{-1, 0.0f};
-    if (step >= 0) f = column_of<T, true>(g, d, step, w, t);
-    if (f.column < 0) {  // nothing left: the two rows are the same, and the draw is from p
-        w.kind = kShare;
-        f = draw_own(g, Steps(states_of(a, p.row), a.steps), w, u);
+    if (by < 0) return;
+    const Open o = opens[by];
+    const bool rest = verdicts[by] == kFromRest;
+    const RowGrid<T> g = target_row<T>(a, stop);
+    Found f{};
+    int step = o.step;
+    Mass t = o.t;
+    bool own = !rest;
+    if (rest) {
+        const RowGrid<T> d = draft_row<T>(a, stop);
+        const Beside<T> beside(g, d);
+        float2 *states = draft_states_of(a, stop);  // the draft row's have served: the steps' sums go over them
+        if (C > 1) {  // every CTA has read them
+            cluster_arrive();
+            cluster_wait();
+        }
+        for (int i = static_cast<int>(rank) * kRows + warp; i < a.steps; i += static_cast<int>(C) * kRows) {
+            const float sum = residual_of_step(g, d, beside, i, o.w);
+            if (lane == 0) __stcg(&states[i].x, sum);
+        }
+        if (C > 1) {
+            cluster_arrive_release();
+            cluster_wait();
+        } else {
+            __syncthreads();
+        }
+        if (!writes) return;
+        step = Steps(states, a.steps).draw(kUnitShares, o.u, [&](float2 v) { return v.x; }, t);
+        if (step >= 0) {
+            f = column_of<T, true>(g, d, step, o.w, t, sums);
+        } else {  // nothing left: the two rows are the same, and the draw is from p
+            step = own_step(Steps(states_of(a, stop), a.steps), o.w, o.u, t);
+            own = true;
+        }
+    } else if (!writes) {
+        return;
     }
-    if (lane == 0) {
-        a.tokens[p.row] = f.column;
-        if (a.logp) a.logp[p.row] = f.column < 0 ? nan_f() : logp_of(f.x, TokState{p.m, p.s, 0.0f}, heat);
+    if (own) f = column_of<T, false>(g, g, step, o.w, t, sums);
+    if (f.mine && lane == 0) {
+        a.tokens[stop] = f.column;
+        if (a.logp) a.logp[stop] = f.column < 0 ? nan_f() : (f.x - o.w.m) * o.inv_t - logf(o.s);
     }
 }
 
 // ---------------------------------------------------------------------------
-// Routing. A warp per row; lane l holds columns l V .. l V + V - 1.
+// Routing. L lanes per row (32 / L rows per warp side by side), lane i of a row
+// holding columns i V .. i V + V - 1 in registers.
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWarps = kRouteThreads / 32;
 
@@ -727,149 +774,283 @@ constexpr int kRouteWarps = kRouteThreads / 32;
 template <typename T, int V>
 __device__ __forceinline__ void load_columns(float (&z)[V], const T *p, int j, int n) {
     constexpr int N = Vec<T>::kN;
-    if constexpr (V >= N) {
-        if (j + V <= n && (reinterpret_cast<uintptr_t>(p + j) & 15) == 0) {
+    static_assert(V % N == 0, "whole vectors");
+    if (j + V <= n && (reinterpret_cast<uintptr_t>(p + j) & 15) == 0) {
 #pragma unroll
-            for (int i = 0; i < V / N; ++i) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(p + j + N * i);
+        for (int i = 0; i < V / N; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p + j + N * i);
 #pragma unroll
-                for (int h = 0; h < N / 2; ++h) {
-                    const float2 f = Vec<T>::pair(v, h);
-                    z[N * i + 2 * h] = f.x;
-                    z[N * i + 2 * h + 1] = f.y;
-                }
+            for (int h = 0; h < N / 2; ++h) {
+                const float2 f = Vec<T>::pair(v, h);
+                z[N * i + 2 * h] = f.x;
+                z[N * i + 2 * h + 1] = f.y;
             }
-            return;
         }
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) z[i] = j + i < n ? Vec<T>::to_float(p[j + i]) : -INFINITY;
+        for (int i = 0; i < V; ++i) z[i] = j + i < n ? Vec<T>::to_float(p[j + i]) : -INFINITY;
+    }
 }
 
+template <typename T, int V>
+__device__ __forceinline__ void store_columns(T *p, int j, int n, const float (&z)[V]) {
+    constexpr int N = Vec<T>::kN;
+    if (j + V <= n && (reinterpret_cast<uintptr_t>(p + j) & 15) == 0) {
+#pragma unroll
+        for (int i = 0; i < V / N; ++i) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int h = 0; h < N / 2; ++h) Vec<T>::set_pair(v, h, make_float2(z[N * i + 2 * h], z[N * i + 2 * h + 1]));
+            *reinterpret_cast<uint4 *>(p + j + N * i) = v;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (j + i < n) p[j + i] = Vec<T>::from_float(z[i]);
+    }
+}
+
+// The L lanes of a row: their largest value (no NaN among them), their sum.
+template <int L>
+__device__ __forceinline__ float row_max(float v) {
+    if constexpr (L == 32) {
+        return warp_max(v);
+    } else {
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullMask, v, o));
+        return v;
+    }
+}
+template <int L>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFullMask, v, o);
+    return v;
+}
+template <int L>
+__device__ __forceinline__ unsigned row_ballot(bool b) {
+    const unsigned all = __ballot_sync(kFullMask, b);
+    return L == 32 ? all : (all >> (threadIdx.x & 31 & ~(L - 1))) & ((1u << (L & 31)) - 1u);
+}
+// a NaN wins
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// 1 / x to a last place or two
+__device__ __forceinline__ float rcp_of(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 __device__ __forceinline__ float exp_of(float d) { return ex2_ftz(d * 1.44269504f); }
 // 1 / (1 + e^-z) without a difference from 1, for any z
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
+__device__ __forceinline__ float sigmoid(float z) { return rcp_of(1.0f + exp_of(-z)); }
 
 // A score over a factor that those of a row (or of its chosen) have in common,
 // `top` the largest of their logits: nothing overflows, and what is next to
 // nothing beside 1 is not so beside the others.
 __device__ __forceinline__ float relative_score(float z, float top, bool sigmoid_scores) {
-    if (!sigmoid_scores) return expf(z - top);
-    return z > 0.0f ? sigmoid(z) : expf(z - fminf(0.0f, top)) / (1.0f + expf(z));
+    if (!sigmoid_scores) return exp_of(z - top);
+    return (z > 0.0f ? 1.0f : exp_of(z - fminf(0.0f, top))) * rcp_of(1.0f + exp_of(-fabsf(z)));
 }
 
-// The chosen experts' share of their sum from their logits (-inf: none), the sum
-// over the warp's lanes.
+// The chosen experts' share of their sum from their logits (-inf: none), over the
+// row's lanes.
+template <int L>
 __device__ __forceinline__ float share_of(float z, bool sigmoid_scores) {
-    const float top = warp_max(z);
-    if (top == -INFINITY) return 0.0f;
-    const float e = relative_score(z, top, sigmoid_scores);
-    return e / warp_sum(e);
+    const float top = row_max<L>(z);
+    const float e = z > -INFINITY || isnan(z) ? relative_score(z, top, sigmoid_scores) : 0.0f;
+    const float all = row_sum<L>(e);
+    return e / (all > 0.0f || isnan(all) ? all : 1.0f);
 }
 
-template <typename T, int V>
+// The two largest of a lane's values that are not taken, the lower of equals first.
+template <int V>
+struct Best {
+    float b1, b2;
+    int i1, i2;
+    __device__ __forceinline__ void find(const float (&by)[V], unsigned taken) {
+        b1 = b2 = -INFINITY;
+        i1 = i2 = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float v = taken >> i & 1u ? -INFINITY : by[i];
+            const bool first = v > b1, second = v > b2;
+            b2 = first ? b1 : second ? v : b2;
+            i2 = first ? i1 : second ? i : i2;
+            b1 = first ? v : b1;
+            i1 = first ? i : i1;
+        }
+    }
+};
+
+// k_route: bound by the instructions of the choice. Each lane keeps its two best
+// at hand: a row's k best are mostly of as many lanes, so a lane is searched
+// again only when it gives a third.
+template <typename T, int L, int V>
 __global__ void __launch_bounds__(kRouteThreads) k_route(RouteArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
+    constexpr int R = 32 / L;  // rows of a warp
     int *counts = reinterpret_cast<int *>(smem);  // [experts], if wanted
-    float *mine = reinterpret_cast<float *>(smem + (a.counts ? 4 * ((a.experts + 3) & ~3) : 0)) +
-                  (threadIdx.x >> 5) * a.experts;  // this warp's row: what its groups are ranked by
-    const int lane = threadIdx.x & 31, E = a.experts, j0 = lane * V;
+    const int lane = threadIdx.x & 31, sub = lane & (L - 1), E = a.experts, j0 = sub * V;
     const int per = E / a.groups;
     const bool grouped = a.top_groups < a.groups;
+    // groups of whole lanes, a power of two of them
+    const int wide = per / V;
+    const bool by_lanes = grouped && per % V == 0 && (wide & (wide - 1)) == 0 && wide <= L;
+    // else their scores by way of shared memory: [rows of the CTA, experts]
+    float *mine = reinterpret_cast<float *>(smem + (a.counts ? 4 * ((E + 3) & ~3) : 0)) +
+                  ((threadIdx.x >> 5) * R + lane / L) * E;
     if (a.counts) {
         for (int j = threadIdx.x; j < E; j += kRouteThreads) counts[j] = 0;
         __syncthreads();
     }
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * kRouteWarps;
-    for (int64_t row = blockIdx.x * int64_t(kRouteWarps) + (threadIdx.x >> 5); row < a.rows; row += warps) {
-        int64_t *chosen = a.chosen + row * a.k;
-        float *gates = a.gates + row * a.k;
-        if (a.weights && a.weights[row] == 0.0f) {
-            if (lane < a.k) chosen[lane] = -1, gates[lane] = 0.0f;
-            continue;
-        }
+    float bias[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) bias[i] = a.bias && j0 + i < E ? a.bias[j0 + i] : 0.0f;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteWarps * R;
+    for (int64_t first = (blockIdx.x * int64_t(kRouteWarps) + (threadIdx.x >> 5)) * R; first < a.rows; first += step) {
+        const int64_t row = first + lane / L;
+        const bool live = row < a.rows && !(a.weights && a.weights[row] == 0.0f);
         const T *p = static_cast<const T *>(a.logits) + row * a.stride;
-        float z[V], by[V];
-        load_columns<T, V>(z, p, j0, E);
-        bool odd = false;
-        float m = -INFINITY;
+        float z[V];
+        if (live) {
+            load_columns<T, V>(z, p, j0, E);
+        } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            odd |= isnan(z[i]) || z[i] == INFINITY;
-            m = fmaxf(m, z[i]);
+            for (int i = 0; i < V; ++i) z[i] = -INFINITY;
         }
-        if (__any_sync(kFullMask, odd)) {
-            if (lane < a.k) chosen[lane] = -1, gates[lane] = nan_f();
-            if (lane == 0) count_bad();
-            continue;
+        float m = z[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) m = max_nan(m, z[i]);
+        const bool odd = row_ballot<L>(!(m < INFINITY)) != 0;  // a NaN or +inf
+        if (odd) m = -INFINITY;
+        m = row_max<L>(m);
+        if (odd) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) z[i] = -INFINITY;
         }
-        m = warp_max(m);
-        float rs = 0.0f;
-        if (!a.sigmoid) {
+        float rs = 0.0f;  // softmax: 1 / s, where the scores themselves are asked for
+        if (!a.sigmoid && (a.bias || !a.renormalise)) {
             float s = 0.0f;
+            const float mm = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-            for (int i = 0; i < V; ++i) s += exp_of(z[i] - m);
-            rs = 1.0f / warp_sum(s);
+            for (int i = 0; i < V; ++i) s += exp_of(z[i] - mm);
+            rs = rcp_of(row_sum<L>(s));
         }
         auto score = [&](float x) { return a.sigmoid ? sigmoid(x) : exp_of(x - m) * rs; };
         // what the choice goes by: the biased score, or, without a bias, the logit,
         // which orders the experts as their scores do and is exact
+        float by[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            by[i] = z[i];
-            if (a.bias && j0 + i < E && z[i] > -INFINITY) {
-                by[i] = score(z[i]) + a.bias[j0 + i];
-                if (isnan(by[i])) by[i] = -INFINITY;
+        for (int i = 0; i < V; ++i) by[i] = z[i];
+        if (a.bias) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float c = score(z[i]) + bias[i];
+                by[i] = z[i] > -INFINITY && c > -INFINITY ? c : -INFINITY;
             }
         }
-        if (grouped) {
+        Best<V> best;
+        best.find(by, 0u);
+        unsigned taken = 0;
+        if (by_lanes) {
+            float g1 = best.b1, g2 = best.b2;
+            if (!a.bias) {
+                if (g1 > -INFINITY) g1 = relative_score(g1, m, a.sigmoid);
+                if (g2 > -INFINITY) g2 = relative_score(g2, m, a.sigmoid);
+            }
+            for (int o = 1; o < wide; o <<= 1) {
+                const float o1 = __shfl_xor_sync(kFullMask, g1, o), o2 = __shfl_xor_sync(kFullMask, g2, o);
+                g2 = fmaxf(fminf(g1, o1), fmaxf(g2, o2));
+                g1 = fmaxf(g1, o1);
+            }
+            const float rank_by = a.group_top == 2 && g2 > -INFINITY ? g1 + g2 : g1;
+            const int own = sub / wide;
+            int before = 0;
+            for (int g = 0; g < a.groups; ++g) {
+                const float o = __shfl_sync(kFullMask, rank_by, (lane & ~(L - 1)) + g * wide);
+                before += o > rank_by || (o == rank_by && g < own);
+            }
+            if (before >= a.top_groups || own >= a.groups) {
+                taken = ~0u;
+                best.b1 = best.b2 = -INFINITY;
+            }
+        } else if (grouped) {
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (j0 + i < E) mine[j0 + i] = a.bias || z[i] == -INFINITY ? by[i] : relative_score(z[i], m, a.sigmoid);
             __syncwarp();
-            float best = -INFINITY, second = -INFINITY;
-            if (lane < a.groups) {
+            auto group_score = [&](int g) {
+                float g1 = -INFINITY, g2 = -INFINITY;
                 for (int i = 0; i < per; ++i) {
-                    const float v = mine[lane * per + i];
-                    second = fmaxf(second, fminf(v, best));
-                    best = fmaxf(best, v);
+                    const float v = mine[g * per + i];
+                    g2 = fmaxf(g2, fminf(v, g1));
+                    g1 = fmaxf(g1, v);
                 }
+                return a.group_top == 2 && g2 > -INFINITY ? g1 + g2 : g1;
+            };
+            // lane i of the row has groups i, i + L, ..: their scores first, over
+            // their first members, then how many come before each
+            constexpr int kMost = kMaxGroups / L;
+            float rank_by[kMost];
+#pragma unroll
+            for (int h = 0; h < kMost; ++h) rank_by[h] = sub + h * L < a.groups ? group_score(sub + h * L) : -INFINITY;
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < kMost; ++h)
+                if (sub + h * L < a.groups) mine[sub + h * L] = rank_by[h];
+            __syncwarp();
+            unsigned kept = 0;
+#pragma unroll
+            for (int h = 0; h < kMost; ++h) {
+                const int own = sub + h * L;
+                int before = 0;
+                for (int g = 0; g < a.groups; ++g) before += mine[g] > rank_by[h] || (mine[g] == rank_by[h] && g < own);
+                if (own < a.groups && before < a.top_groups) kept |= 1u << own;
             }
-            const float rank_by = a.group_top == 2 && second > -INFINITY ? best + second : best;
-            int before = 0;
-            for (int g = 0; g < a.groups; ++g) {
-                const float o = __shfl_sync(kFullMask, rank_by, g);
-                before += o > rank_by || (o == rank_by && g < lane);
-            }
-            const unsigned kept = __ballot_sync(kFullMask, lane < a.groups && before < a.top_groups);
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) kept |= __shfl_xor_sync(kFullMask, kept, o);
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (j0 + i < E && !(kept >> ((j0 + i) / per) & 1u)) by[i] = -INFINITY;
+                if (j0 + i >= E || !(kept >> ((j0 + i) / per) & 1u)) by[i] = -INFINITY;
+            best.find(by, 0u);
         }
         // the k best, one after another: the largest, the lowest column of equals
-        unsigned taken = 0;
-        int expert = -1;  // lane i: the i-th
+        int expert = -1;  // lane i of the row: the i-th
         for (int n = 0; n < a.k; ++n) {
-            float best = -INFINITY;
-            int at = 0;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (!(taken >> i & 1u) && by[i] > best) best = by[i], at = i;
-            const float top = warp_max(best);
-            if (top == -INFINITY) break;
-            const int owner = __ffs(__ballot_sync(kFullMask, best == top)) - 1;
-            if (lane == owner) taken |= 1u << at;
-            const int j = __shfl_sync(kFullMask, j0 + at, owner);
-            if (lane == n) expert = j;
+            const float top = row_max<L>(best.b1);
+            const unsigned holds = row_ballot<L>(best.b1 == top);
+            const int owner = __ffs(holds) - 1;
+            const int j = __shfl_sync(kFullMask, j0 + best.i1, (lane & ~(L - 1)) + owner);
+            if (sub == n && top > -INFINITY) expert = j;
+            if (sub == owner) {
+                taken |= 1u << best.i1;
+                best.b1 = best.b2;
+                best.i1 = best.i2;
+                best.b2 = -INFINITY;
+            }
+            // a lane that has given both and may hold more
+            const bool empty = best.b1 == -INFINITY && taken != 0u && taken != ~0u;
+            if (__any_sync(kFullMask, empty)) {
+                if (empty) {
+                    best.find(by, taken);
+                    if (best.b1 == -INFINITY) taken = ~0u;
+                }
+            }
         }
         const float zc = expert >= 0 ? Vec<T>::to_float(p[expert]) : -INFINITY;
-        float g = a.renormalise ? share_of(zc, a.sigmoid) : expert >= 0 ? score(zc) : 0.0f;
-        if (expert < 0) g = 0.0f;
-        if (lane < a.k) {
-            chosen[lane] = expert;
-            gates[lane] = g * a.scale;
+        float g = a.renormalise ? share_of<L>(zc, a.sigmoid) : expert >= 0 ? score(zc) : 0.0f;
+        g = odd ? nan_f() : g * a.scale;
+        if (row < a.rows && sub < a.k) {
+            a.chosen[row * a.k + sub] = expert;
+            a.gates[row * a.k + sub] = g;
         }
+        if (odd && sub == 0) count_bad();
         if (a.counts && expert >= 0) atomicAdd(&counts[expert], 1);
     }
     if (a.counts) {
@@ -887,80 +1068,85 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(RouteArgs a) {
 //                 sigmoid: dz_c = s_c (1 - s_c) G, 0 elsewhere
 // Only the softmax scores themselves need the whole row; the others read the
 // chosen experts' logits.
-template <typename T, int V>
+template <typename T, int L, int V>
 __global__ void __launch_bounds__(kRouteThreads) k_route_grad(RouteArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
-    const int lane = threadIdx.x & 31, E = a.experts, j0 = lane * V;
-    float *mine = reinterpret_cast<float *>(smem) + (threadIdx.x >> 5) * E;  // this warp's row of the gradient
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * kRouteWarps;
-    for (int64_t row = blockIdx.x * int64_t(kRouteWarps) + (threadIdx.x >> 5); row < a.rows; row += warps) {
-        T *grad = static_cast<T *>(a.grad) + row * a.grad_stride;
+    constexpr int R = 32 / L, kRow = L * V;
+    const int lane = threadIdx.x & 31, sub = lane & (L - 1), E = a.experts, j0 = sub * V;
+    float *mine = reinterpret_cast<float *>(smem) + ((threadIdx.x >> 5) * R + lane / L) * kRow;  // this row's gradient
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteWarps * R;
+    for (int64_t first = (blockIdx.x * int64_t(kRouteWarps) + (threadIdx.x >> 5)) * R; first < a.rows; first += step) {
+        const int64_t row = first + lane / L;
+        const bool live = row < a.rows && !(a.weights && a.weights[row] == 0.0f);
+        const T *p = static_cast<const T *>(a.logits) + row * a.stride;
+        int c = -1;
+        float G = 0.0f;
+        if (live && sub < a.k) {
+            const int64_t at = a.chosen[row * a.k + sub];
+            G = a.gates_grad[row * a.k + sub] * a.scale;
+            if (at >= E || at < -1)
+                count_bad();
+            else
+                c = static_cast<int>(at);
+        }
+        const float z = c >= 0 ? Vec<T>::to_float(p[c]) : -INFINITY;
         float out[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) out[i] = 0.0f;
-        if (!a.weights || a.weights[row] != 0.0f) {
-            const T *p = static_cast<const T *>(a.logits) + row * a.stride;
-            int64_t c = lane < a.k ? a.chosen[row * a.k + lane] : -1;
-            if (c >= E || c < -1) {
-                count_bad();
-                c = -1;
-            }
-            const float z = c >= 0 ? Vec<T>::to_float(p[c]) : -INFINITY;
-            const float G = c >= 0 ? a.gates_grad[row * a.k + lane] * a.scale : 0.0f;
-            float v = 0.0f;  // the gradient at the chosen expert
-            if (a.renormalise) {
-                const float f = share_of(z, a.sigmoid);
-                const float D = warp_sum(f > 0.0f || isnan(f) ? f * G : 0.0f);
-                if (c >= 0) v = f * (G - D);
-                if (a.sigmoid && c >= 0) v *= sigmoid(-z);
-            } else if (a.sigmoid) {
-                if (c >= 0) v = sigmoid(z) * sigmoid(-z) * G;
+        float v = 0.0f;  // the gradient at the chosen expert
+        if (a.renormalise) {
+            const float f = share_of<L>(z, a.sigmoid);
+            const float D = row_sum<L>(c >= 0 ? f * G : 0.0f);
+            if (c >= 0) v = f * (G - D);
+            if (a.sigmoid && c >= 0) v *= sigmoid(-z);
+        } else if (a.sigmoid) {
+            if (c >= 0) v = sigmoid(z) * sigmoid(-z) * G;
+        } else {
+            float m = -INFINITY, s = 0.0f;
+            if (live) {
+                load_columns<T, V>(out, p, j0, E);
             } else {
-                float x[V];
-                load_columns<T, V>(x, p, j0, E);
-                float m = -INFINITY, s = 0.0f;
 #pragma unroll
-                for (int i = 0; i < V; ++i) m = fmaxf(m, x[i]);
-                m = warp_max(m);
-                if (m == -INFINITY) m = 0.0f;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    out[i] = exp_of(x[i] - m);
-                    s += out[i];
-                }
-                s = warp_sum(s);
-                const float rs = s > 0.0f || isnan(s) ? 1.0f / s : 0.0f;
-                const float sc = c >= 0 ? exp_of(z - m) * rs : 0.0f;
-                v = sc * G;
-                const float D = warp_sum(v);
-#pragma unroll
-                for (int i = 0; i < V; ++i) out[i] *= -rs * D;
+                for (int i = 0; i < V; ++i) out[i] = -INFINITY;
             }
-            // add v to its column: through shared memory, the same column twice one
-            // after the other, in the order of the slots
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (j0 + i < E) mine[j0 + i] = out[i];
-            __syncwarp();
-            const unsigned same = __match_any_sync(kFullMask, c >= 0 ? static_cast<int>(c) : -1 - lane);
-            const unsigned others = __ballot_sync(kFullMask, (same & (same - 1)) != 0);
-            if (others == 0) {
-                if (c >= 0) mine[c] += v;
-            } else {
-                for (int i = 0; i < a.k; ++i) {
-                    if (lane == i && c >= 0) mine[c] += v;
-                    __syncwarp();
-                }
+            for (int i = 0; i < V; ++i) m = fmaxf(m, out[i]);
+            m = row_max<L>(m);
+            if (m == -INFINITY) m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                out[i] = exp_of(out[i] - m);
+                s += out[i];
             }
-            __syncwarp();
+            s = row_sum<L>(s);
+            const float rs = s > 0.0f || isnan(s) ? 1.0f / s : 0.0f;
+            v = c >= 0 ? exp_of(z - m) * rs * G : 0.0f;
+            const float D = row_sum<L>(v);
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (j0 + i < E) out[i] = mine[j0 + i];
-            __syncwarp();
+            for (int i = 0; i < V; ++i) out[i] *= -rs * D;
         }
+        // add v to its column: through shared memory; a column that a row names
+        // twice one after the other, in the order of the slots
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (j0 + i < E) grad[j0 + i] = Vec<T>::from_float(out[i]);
+        for (int i = 0; i < V; i += 4) *reinterpret_cast<float4 *>(mine + j0 + i) = make_float4(out[i], out[i + 1], out[i + 2], out[i + 3]);
+        __syncwarp();
+        const unsigned same = __match_any_sync(kFullMask, c >= 0 ? (lane / L) * kRow + c : -1 - lane);
+        if (!__any_sync(kFullMask, (same & (same - 1)) != 0)) {
+            if (c >= 0) mine[c] += v;
+        } else {
+            for (int i = 0; i < a.k; ++i) {
+                if (sub == i && c >= 0) mine[c] += v;
+                __syncwarp();
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+            const float4 o = *reinterpret_cast<const float4 *>(mine + j0 + i);
+            out[i] = o.x, out[i + 1] = o.y, out[i + 2] = o.z, out[i + 3] = o.w;
+        }
+        __syncwarp();
+        if (row < a.rows) store_columns<T, V>(static_cast<T *>(a.grad) + row * a.grad_stride, j0, E, out);
     }
 }
 
@@ -976,11 +1162,13 @@ int64_t capped(int64_t clusters, int64_t cap) {
     return std::max<int64_t>(1, cap > 0 ? std::min(clusters, cap) : clusters);
 }
 
-// Steps per warp: as many as keep the warps at `kWavesOfWarps` times what the GPU
-// holds, at most 32 (a lane each).
+// Steps per warp: two where that leaves more warps than the GPU holds at once.
+// Measured (us, whole calls, 1 / 2 / 3 / 4 / 6 / 8 / 12 steps): sample_rows 1 x
+// 32000 bf16 5.7 / 6.3 / 6.9 / 7.6 / 8.8 / 9.9 / 12; 256 x 151936 19.2 / 19.1 /
+// 19.4 / 18.7 / 19.2 / 20.2 / 22.3; verify_drafts 256 requests of up to 7 drafts
+// of 128256 119.5 / 115.1 / 115.5 / 115.7 / 116.7 / 115.8 / 118.
 int unit_of(int64_t steps, int64_t rows, const DeviceInfo &dev) {
-    const int64_t resident = 8 * kWarps * static_cast<int64_t>(dev.sms);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(8, steps), steps * rows / resident)));
+    return steps * rows > 2 * 8 * kWarps * static_cast<int64_t>(dev.sms) ? 2 : 1;
 }
 
 template <typename T>
@@ -988,8 +1176,6 @@ struct Kernels {
     static const void *states() { return reinterpret_cast<const void *>(&k_states<T>); }
     static const void *sample() { return reinterpret_cast<const void *>(&k_sample<T>); }
     static const void *decide() { return reinterpret_cast<const void *>(&k_decide<T>); }
-    static const void *residual() { return reinterpret_cast<const void *>(&k_residual<T>); }
-    static const void *replace() { return reinterpret_cast<const void *>(&k_replace<T>); }
 };
 
 cudaError_t launch(const void *fn, int64_t ctas, bool dependent, cudaStream_t s, void **args, int threads = kThreads) {
@@ -1011,7 +1197,7 @@ template <typename T>
 cudaError_t sample_as(ChoiceArgs a, const DeviceInfo &dev, cudaStream_t s) {
     if (cudaError_t e = launch_steps(Kernels<T>::states(), a, a.rows, false, dev, s); e != cudaSuccess) return e;
     void *args[] = {&a};
-    return launch(Kernels<T>::sample(), ctas_of(a.rows), true, s, args);
+    return launch(Kernels<T>::sample(), a.rows, true, s, args, kDrawThreads);
 }
 
 template <typename T>
@@ -1019,37 +1205,40 @@ cudaError_t verify_as(ChoiceArgs a, const DeviceInfo &dev, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
     const bool drawn = a.draft_logits != nullptr;
     if (a.rows > 0 && (e = launch_steps(Kernels<T>::states(), a, drawn ? 2 * a.rows : a.rows, false, dev, s))) return e;
+    // CTAs per request: as many as an SM holds, four, with a step for each of their warps
+    int c = 1;
+    while (drawn && c < 8 && 2 * c * a.requests <= 4 * dev.sms && 2 * c * (kDrawThreads / 32) <= a.steps) c *= 2;
     void *args[] = {&a};
-    if ((e = launch(Kernels<T>::decide(), std::max<int64_t>(1, a.requests), a.rows > 0, s, args, kDecideThreads))) return e;
-    if (!drawn || a.rows == 0 || a.requests == 0) return e;
-    if ((e = launch_steps(Kernels<T>::residual(), a, a.requests, true, dev, s))) return e;
-    return launch(Kernels<T>::replace(), ctas_of(a.requests), true, s, args);
+    LaunchConfig l(std::max<int64_t>(1, a.requests) * c, kDrawThreads, c, a.rows > 0, s);
+    return cudaLaunchKernelExC(&l.cfg, Kernels<T>::decide(), args);
 }
 
+template <typename T, int L, int V>
+const void *route_kernel_v(bool grad) {
+    return grad ? reinterpret_cast<const void *>(&k_route_grad<T, L, V>) : reinterpret_cast<const void *>(&k_route<T, L, V>);
+}
 template <typename T>
-const void *route_kernel_t(int v, bool grad) {
-#define CE_ROUTE(V)                                                           \
-    return grad ? reinterpret_cast<const void *>(&k_route_grad<T, V>) : reinterpret_cast<const void *>(&k_route<T, V>)
-    switch (v) {
-    case 2: CE_ROUTE(2);
-    case 4: CE_ROUTE(4);
-    case 8: CE_ROUTE(8);
-    case 16: CE_ROUTE(16);
-    default: CE_ROUTE(32);
-    }
-#undef CE_ROUTE
+const void *route_kernel_t(int lanes, int v, bool grad) {
+    if (v == 32) return route_kernel_v<T, 32, 32>(grad);
+    if (v == 16) return route_kernel_v<T, 32, 16>(grad);
+    if (lanes == 32) return route_kernel_v<T, 32, 8>(grad);
+    return lanes == 16 ? route_kernel_v<T, 16, 8>(grad) : route_kernel_v<T, 8, 8>(grad);
 }
 
 cudaError_t launch_route_any(DType t, const RouteArgs &a, bool grad, const DeviceInfo &dev, cudaStream_t s) {
     g_launched.note(dev);
-    int v = 2;
-    while (32 * v < a.experts) v *= 2;
-    const void *fn = t == kF32    ? route_kernel_t<float>(v, grad)
-                     : t == kBF16 ? route_kernel_t<__nv_bfloat16>(v, grad)
-                                  : route_kernel_t<__half>(v, grad);
-    const int64_t need = (a.rows + kRouteWarps - 1) / kRouteWarps;
+    // eight columns a lane, as few lanes as hold the row and its k slots
+    int lanes = 8, v = 8;
+    while (lanes < 32 && (lanes * v < a.experts || lanes < a.k)) lanes *= 2;
+    while (lanes * v < a.experts) v *= 2;
+    const void *fn = t == kF32    ? route_kernel_t<float>(lanes, v, grad)
+                     : t == kBF16 ? route_kernel_t<__nv_bfloat16>(lanes, v, grad)
+                                  : route_kernel_t<__half>(lanes, v, grad);
+    const int per = kRouteWarps * (32 / lanes);  // rows of a CTA
+    const int64_t need = (a.rows + per - 1) / per;
     const int64_t ctas = capped(std::min<int64_t>(need, 8 * static_cast<int64_t>(dev.sms)), a.grid_cap);
-    const int smem = (a.counts ? 4 * ((a.experts + 3) & ~3) : 0) + 4 * kRouteWarps * a.experts;
+    const int smem = grad ? 4 * per * lanes * v
+                          : (a.counts ? 4 * ((a.experts + 3) & ~3) : 0) + (a.top_groups < a.groups ? 4 * per * a.experts : 0);
     RouteArgs aa = a;
     void *args[] = {&aa};
     LaunchConfig l(ctas, kRouteThreads, 0, false, s, smem);
@@ -1058,21 +1247,18 @@ cudaError_t launch_route_any(DType t, const RouteArgs &a, bool grad, const Devic
 
 }  // namespace
 
-// The scratch: step states of the target rows, then of the draft rows, then the
-// rows' and the requests' own.
+// The scratch: step states of the target rows, then of the draft rows.
 int64_t choice_steps(DType t, int64_t vocab) {
     const int N = 16 / elem_size(t);
     return ((vocab + 2 * N - 2) / N + kStep - 1) / kStep;
 }
 int64_t choice_bytes(DType t, int64_t rows, int64_t vocab, int64_t requests) {
     const int64_t states = 8 * rows * choice_steps(t, vocab);
-    return requests < 0 ? states : 2 * states + 16 * rows + static_cast<int64_t>(sizeof(Pending)) * requests;
+    return requests < 0 ? states : 2 * states;
 }
 static void lay_out(DType t, ChoiceArgs &a, void *work) {
     a.steps = static_cast<int>(choice_steps(t, a.vocab));
     a.states = static_cast<float2 *>(work);
-    a.row_states = reinterpret_cast<float4 *>(a.states + 2 * a.rows * a.steps);
-    a.pending = a.draft_logits ? reinterpret_cast<Pending *>(a.row_states + a.rows) : nullptr;
 }
 
 cudaError_t launch_sample(DType t, const ChoiceArgs &a, void *work, const DeviceInfo &dev, cudaStream_t s) {

@@ -150,12 +150,6 @@ cudaError_t read_objective_status(unsigned long long out[2], const DeviceInfo &d
 cudaError_t reset_objective_status(const DeviceInfo &dev, cudaStream_t s);
 
 // -- the choices made from a row's softmax (ce_choices.cu) -----------------------
-// A request whose token is drawn from what its draft row leaves of a row (-1: none).
-struct Pending {
-    int64_t row;
-    float m, s, mq, sq;
-};
-
 // Arguments of sample_rows and verify_drafts; unused pointers are null.
 struct ChoiceArgs {
     const void *logits;
@@ -177,8 +171,6 @@ struct ChoiceArgs {
     // scratch
     int steps;           // of a row
     float2 *states;      // [2 rows, steps] (m, s)
-    float4 *row_states;  // [rows] (m, s) of a row and of its draft row
-    Pending *pending;    // [requests], or null: drafts that were not drawn
 };
 
 constexpr int kMaxExperts = 1024;

@@ -167,12 +167,13 @@ def check_verified(logits, drafts, offsets, uniforms, draft_logits, temperatures
 # -- routing ----------------------------------------------------------------------
 
 def scores64(x, score):
-    """Scores and the bounds of their errors: sigmoid, one expf (4 U), a sum and a division;
-    softmax, (3 |y| + 4) U, the sum's (6 + 32 + 5) U and the product's."""
+    """Scores and the bounds of their errors. sigmoid: e^-z by base 2, its exponent's product and constant
+    rounded (2 U |z| of e^-z, of which the score has its part 1 - s), ex2 (4 U), a sum, a reciprocal (2 U);
+    softmax, (3 |y| + 4) U, the sum's (6 + 32 + 5) U, a reciprocal and the product."""
     z = x.double()
     if score == "sigmoid":
         s = torch.sigmoid(z)
-        return s, s * 8 * U
+        return s, s * (8 + 2 * z.clamp(-1e4, 1e4).abs() * (1 - s)) * U
     d = z - z.amax(1, keepdim=True)
     s = torch.softmax(z, 1)
     y = d.clamp(min=-200).abs() * 1.4426950408889634
@@ -262,12 +263,13 @@ def gates64(x, chosen, score, renormalise):
     s, es = s[0][chosen], es[0][chosen]
     if not renormalise or not chosen:
         return s, es
-    # exp(z - top) by CUDA's expf (2 ulp = 4 U; U |z - top| for the rounded difference), a sum, a division
+    # exp(z - top) by base 2: 2 U |z - top| for the exponent's roundings and U |z - top| for the difference's, ex2
+    # 4 U; 1 / (1 + e^-|z|): at most 7 U, since |z| e^-|z| < 1; the sum's 5 levels and a division
     zc = z[chosen]
     ls = torch.nn.functional.logsigmoid(zc) if score == "sigmoid" else zc
     f = torch.softmax(ls, 0)
     d = (zc - zc.max()).clamp(min=-200).abs()
-    rel = (d + 16) * U
+    rel = (3 * d + 20) * U
     return f, f * (rel + (f * rel).sum() + 8 * U)
 
 
@@ -286,7 +288,7 @@ def route_grad64(x, chosen, gates_grad, score="softmax", renormalise=True, scale
         G = gates_grad[r].double()[[i for _, i in at]] * scale
         eG = G.abs() * U
         s, es = scores64(x[r][None], score)
-        sc, esc = s[0][cols], es[0][cols]
+        sc, esc, zc = s[0][cols], es[0][cols], x[r].double()[cols].clamp(-1e4, 1e4)
         if renormalise:
             f, ef = gates64(x[r], cols, score, True)
             D = (f * G).sum()
@@ -294,11 +296,11 @@ def route_grad64(x, chosen, gates_grad, score="softmax", renormalise=True, scale
             v = f * (G - D)
             ev = ef * (G - D).abs() + f * (eG + eD + U * (G - D).abs()) + 2 * U * v.abs()
             if score == "sigmoid":
-                ev = ev * (1 - sc) + v.abs() * (1 - sc) * 10 * U
+                ev = ev * (1 - sc) + v.abs() * (1 - sc) * (10 + 2 * zc.abs()) * U
                 v = v * (1 - sc)
         elif score == "sigmoid":
             v = sc * (1 - sc) * G
-            ev = v.abs() * 20 * U
+            ev = v.abs() * (20 + 4 * zc.abs()) * U
         else:
             v = sc * G
             ev = esc * G.abs() + sc * eG + 2 * U * v.abs()
