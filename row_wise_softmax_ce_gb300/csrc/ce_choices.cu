@@ -770,26 +770,36 @@ __global__ void __launch_bounds__(kDrawThreads, 4) k_decide(ChoiceArgs a) {
 constexpr int kRouteThreads = 256;
 constexpr int kRouteWarps = kRouteThreads / 32;
 
-// V consecutive columns from j on (those below n), -inf elsewhere.
+// V consecutive columns from j on (those below n), -inf elsewhere, as vectors.
 template <typename T, int V>
-__device__ __forceinline__ void load_columns(float (&z)[V], const T *p, int j, int n) {
+__device__ __forceinline__ void load_columns(uint4 (&v)[V / Vec<T>::kN], const T *p, int j, int n) {
     constexpr int N = Vec<T>::kN;
     static_assert(V % N == 0, "whole vectors");
     if (j + V <= n && (reinterpret_cast<uintptr_t>(p + j) & 15) == 0) {
 #pragma unroll
-        for (int i = 0; i < V / N; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(p + j + N * i);
-#pragma unroll
-            for (int h = 0; h < N / 2; ++h) {
-                const float2 f = Vec<T>::pair(v, h);
-                z[N * i + 2 * h] = f.x;
-                z[N * i + 2 * h + 1] = f.y;
-            }
-        }
+        for (int i = 0; i < V / N; ++i) v[i] = *reinterpret_cast<const uint4 *>(p + j + N * i);
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) z[i] = j + i < n ? Vec<T>::to_float(p[j + i]) : -INFINITY;
+        for (int i = 0; i < V / N; ++i)
+#pragma unroll
+            for (int h = 0; h < N / 2; ++h) {
+                const int c = j + N * i + 2 * h;
+                Vec<T>::set_pair(v[i], h, make_float2(c < n ? Vec<T>::to_float(p[c]) : -INFINITY,
+                                                      c + 1 < n ? Vec<T>::to_float(p[c + 1]) : -INFINITY));
+            }
     }
+}
+template <typename T, int V>
+__device__ __forceinline__ void unpack_columns(float (&z)[V], const uint4 (&v)[V / Vec<T>::kN]) {
+    constexpr int N = Vec<T>::kN;
+#pragma unroll
+    for (int i = 0; i < V / N; ++i)
+#pragma unroll
+        for (int h = 0; h < N / 2; ++h) {
+            const float2 f = Vec<T>::pair(v[i], h);
+            z[N * i + 2 * h] = f.x;
+            z[N * i + 2 * h + 1] = f.y;
+        }
 }
 
 template <typename T, int V>
@@ -867,123 +877,126 @@ __device__ __forceinline__ float share_of(float z, bool sigmoid_scores) {
     return e / (all > 0.0f || isnan(all) ? all : 1.0f);
 }
 
-// The two largest of a lane's values that are not taken, the lower of equals first.
+// The two largest of a lane's values that are not taken, the lower of equals
+// first, and the value of the third.
 template <int V>
 struct Best {
-    float b1, b2;
+    float b1, b2, b3;
     int i1, i2;
     __device__ __forceinline__ void find(const float (&by)[V], unsigned taken) {
-        b1 = b2 = -INFINITY;
+        b1 = b2 = b3 = -INFINITY;
         i1 = i2 = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const float v = taken >> i & 1u ? -INFINITY : by[i];
             const bool first = v > b1, second = v > b2;
-            b2 = first ? b1 : second ? v : b2;
             i2 = first ? i1 : second ? i : i2;
-            b1 = first ? v : b1;
             i1 = first ? i : i1;
+            b3 = fmaxf(b3, fminf(b2, v));
+            b2 = fmaxf(b2, fminf(b1, v));
+            b1 = fmaxf(b1, v);
         }
     }
+    // the largest is given away; the third's column is looked for when it is asked for
+    __device__ __forceinline__ void give() {
+        b1 = b2, i1 = i2;
+        b2 = b3, i2 = -1;
+        b3 = -INFINITY;
+    }
+    __device__ __forceinline__ void none() { b1 = b2 = b3 = -INFINITY; }
 };
 
-// k_route: bound by the instructions of the choice. Each lane keeps its two best
-// at hand: a row's k best are mostly of as many lanes, so a lane is searched
-// again only when it gives a third.
+// The counts are zeroed by a kernel that k_route, launched as its programmatic
+// dependent, runs beside and waits for before it adds to them (a memset before
+// k_route: 4 us more).
+__global__ void __launch_bounds__(kRouteThreads) k_zero(unsigned long long *counts, int n) {
+    launch_dependents();
+    for (int j = threadIdx.x; j < n; j += kRouteThreads) counts[j] = 0;
+}
+
+// CTAs of an SM, by the columns a lane holds.
+__host__ __device__ constexpr int route_ctas(int v) { return v > 16 ? 1 : v > 8 ? 2 : 4; }
+
+// k_route: bound by the instructions of the choice, so several rows share a
+// warp's instructions, and each lane keeps its two best columns at hand, and the
+// value of the third: a lane is searched again only when its third is chosen.
 template <typename T, int L, int V>
-__global__ void __launch_bounds__(kRouteThreads) k_route(RouteArgs a) {
+__global__ void __launch_bounds__(kRouteThreads, route_ctas(V)) k_route(RouteArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
-    constexpr int R = 32 / L;  // rows of a warp
-    int *counts = reinterpret_cast<int *>(smem);  // [experts], if wanted
-    const int lane = threadIdx.x & 31, sub = lane & (L - 1), E = a.experts, j0 = sub * V;
+    constexpr int R = 32 / L, kVecs = V / Vec<T>::kN;  // rows of a warp
+    const int lane = threadIdx.x & 31, sub = lane & (L - 1), row0 = lane & ~(L - 1), E = a.experts, j0 = sub * V;
     const int per = E / a.groups;
     const bool grouped = a.top_groups < a.groups;
     // groups of whole lanes, a power of two of them
     const int wide = per / V;
     const bool by_lanes = grouped && per % V == 0 && (wide & (wide - 1)) == 0 && wide <= L;
-    // else their scores by way of shared memory: [rows of the CTA, experts]
-    float *mine = reinterpret_cast<float *>(smem + (a.counts ? 4 * ((E + 3) & ~3) : 0)) +
-                  ((threadIdx.x >> 5) * R + lane / L) * E;
-    if (a.counts) {
-        for (int j = threadIdx.x; j < E; j += kRouteThreads) counts[j] = 0;
+    float *bias = reinterpret_cast<float *>(smem);           // [L V], if there is one
+    int *counts = reinterpret_cast<int *>(bias + (a.bias ? L * V : 0));  // [experts], if wanted
+    // group scores by way of shared memory: [rows of the CTA, experts]
+    float *mine = reinterpret_cast<float *>(counts + (a.counts ? E : 0)) + ((threadIdx.x >> 5) * R + lane / L) * E;
+    if (a.bias || a.counts) {
+        if (a.bias)
+            for (int j = threadIdx.x; j < L * V; j += kRouteThreads) bias[j] = j < E ? a.bias[j] : 0.0f;
+        if (a.counts)
+            for (int j = threadIdx.x; j < E; j += kRouteThreads) counts[j] = 0;
         __syncthreads();
     }
-    float bias[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) bias[i] = a.bias && j0 + i < E ? a.bias[j0 + i] : 0.0f;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteWarps * R;
-    for (int64_t first = (blockIdx.x * int64_t(kRouteWarps) + (threadIdx.x >> 5)) * R; first < a.rows; first += step) {
-        const int64_t row = first + lane / L;
-        const bool live = row < a.rows && !(a.weights && a.weights[row] == 0.0f);
-        const T *p = static_cast<const T *>(a.logits) + row * a.stride;
-        float z[V];
-        if (live) {
-            load_columns<T, V>(z, p, j0, E);
+    uint4 next[kVecs];
+    // a row's logits, asked for a row ahead: -inf for a padding row or none
+    auto load = [&](int64_t row) {
+        if (row < a.rows && !(a.weights && a.weights[row] == 0.0f)) {
+            load_columns<T, V>(next, static_cast<const T *>(a.logits) + row * a.stride, j0, E);
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) z[i] = -INFINITY;
+            for (int i = 0; i < kVecs; ++i) next[i] = Vec<T>::lowest();
         }
+    };
+    int64_t first = (blockIdx.x * int64_t(kRouteWarps) + (threadIdx.x >> 5)) * R;
+    load(first + lane / L);
+    for (; first < a.rows; first += step) {
+        const int64_t row = first + lane / L;
+        float z[V];
+        unpack_columns<T, V>(z, next);
+        if (first + step < a.rows) load(row + step);
         float m = z[0];
 #pragma unroll
         for (int i = 1; i < V; ++i) m = max_nan(m, z[i]);
         const bool odd = row_ballot<L>(!(m < INFINITY)) != 0;  // a NaN or +inf
-        if (odd) m = -INFINITY;
-        m = row_max<L>(m);
         if (odd) {
+            m = -INFINITY;
 #pragma unroll
             for (int i = 0; i < V; ++i) z[i] = -INFINITY;
         }
+        m = row_max<L>(m);
         float rs = 0.0f;  // softmax: 1 / s, where the scores themselves are asked for
         if (!a.sigmoid && (a.bias || !a.renormalise)) {
-            float s = 0.0f;
             const float mm = m == -INFINITY ? 0.0f : m;
+            float s = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) s += exp_of(z[i] - mm);
             rs = rcp_of(row_sum<L>(s));
         }
-        auto score = [&](float x) { return a.sigmoid ? sigmoid(x) : exp_of(x - m) * rs; };
-        // what the choice goes by: the biased score, or, without a bias, the logit,
-        // which orders the experts as their scores do and is exact
-        float by[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) by[i] = z[i];
+        // what the choice goes by, from here on in z: the biased score, or, without a
+        // bias, the logit, which orders the experts as their scores do and is exact
         if (a.bias) {
+            auto biased = [&](float c, int i) { return z[i] > -INFINITY && c > -INFINITY ? c : -INFINITY; };
+            if (a.sigmoid) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float c = score(z[i]) + bias[i];
-                by[i] = z[i] > -INFINITY && c > -INFINITY ? c : -INFINITY;
+                for (int i = 0; i < V; ++i) z[i] = biased(sigmoid(z[i]) + bias[j0 + i], i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) z[i] = biased(exp_of(z[i] - m) * rs + bias[j0 + i], i);
             }
         }
+        auto ranked = [&](float v) { return a.bias || v == -INFINITY ? v : relative_score(v, m, a.sigmoid); };
         Best<V> best;
-        best.find(by, 0u);
         unsigned taken = 0;
-        if (by_lanes) {
-            float g1 = best.b1, g2 = best.b2;
-            if (!a.bias) {
-                if (g1 > -INFINITY) g1 = relative_score(g1, m, a.sigmoid);
-                if (g2 > -INFINITY) g2 = relative_score(g2, m, a.sigmoid);
-            }
-            for (int o = 1; o < wide; o <<= 1) {
-                const float o1 = __shfl_xor_sync(kFullMask, g1, o), o2 = __shfl_xor_sync(kFullMask, g2, o);
-                g2 = fmaxf(fminf(g1, o1), fmaxf(g2, o2));
-                g1 = fmaxf(g1, o1);
-            }
-            const float rank_by = a.group_top == 2 && g2 > -INFINITY ? g1 + g2 : g1;
-            const int own = sub / wide;
-            int before = 0;
-            for (int g = 0; g < a.groups; ++g) {
-                const float o = __shfl_sync(kFullMask, rank_by, (lane & ~(L - 1)) + g * wide);
-                before += o > rank_by || (o == rank_by && g < own);
-            }
-            if (before >= a.top_groups || own >= a.groups) {
-                taken = ~0u;
-                best.b1 = best.b2 = -INFINITY;
-            }
-        } else if (grouped) {
+        if (grouped && !by_lanes) {
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (j0 + i < E) mine[j0 + i] = a.bias || z[i] == -INFINITY ? by[i] : relative_score(z[i], m, a.sigmoid);
+                if (j0 + i < E) mine[j0 + i] = ranked(z[i]);
             __syncwarp();
             auto group_score = [&](int g) {
                 float g1 = -INFINITY, g2 = -INFINITY;
@@ -1017,34 +1030,47 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(RouteArgs a) {
             for (int o = L / 2; o > 0; o >>= 1) kept |= __shfl_xor_sync(kFullMask, kept, o);
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                if (j0 + i >= E || !(kept >> ((j0 + i) / per) & 1u)) by[i] = -INFINITY;
-            best.find(by, 0u);
+                if (j0 + i >= E || !(kept >> ((j0 + i) / per) & 1u)) z[i] = -INFINITY;
+        }
+        best.find(z, 0u);
+        if (by_lanes) {
+            float g1 = ranked(best.b1), g2 = ranked(best.b2);
+            for (int o = 1; o < wide; o <<= 1) {
+                const float o1 = __shfl_xor_sync(kFullMask, g1, o), o2 = __shfl_xor_sync(kFullMask, g2, o);
+                g2 = fmaxf(fminf(g1, o1), fmaxf(g2, o2));
+                g1 = fmaxf(g1, o1);
+            }
+            const float rank_by = a.group_top == 2 && g2 > -INFINITY ? g1 + g2 : g1;
+            const int own = sub / wide;
+            int before = 0;
+            for (int g = 0; g < a.groups; ++g) {
+                const float o = __shfl_sync(kFullMask, rank_by, row0 + g * wide);
+                before += o > rank_by || (o == rank_by && g < own);
+            }
+            if (before >= a.top_groups || own >= a.groups) best.none();
         }
         // the k best, one after another: the largest, the lowest column of equals
         int expert = -1;  // lane i of the row: the i-th
         for (int n = 0; n < a.k; ++n) {
             const float top = row_max<L>(best.b1);
-            const unsigned holds = row_ballot<L>(best.b1 == top);
-            const int owner = __ffs(holds) - 1;
-            const int j = __shfl_sync(kFullMask, j0 + best.i1, (lane & ~(L - 1)) + owner);
-            if (sub == n && top > -INFINITY) expert = j;
-            if (sub == owner) {
-                taken |= 1u << best.i1;
-                best.b1 = best.b2;
-                best.i1 = best.i2;
-                best.b2 = -INFINITY;
+            const int owner = __ffs(row_ballot<L>(best.b1 == top)) - 1;
+            const bool gives = sub == owner && top > -INFINITY, unknown = gives && best.i1 < 0;
+            if (__any_sync(kFullMask, unknown)) {
+                if (unknown) best.find(z, taken);
             }
-            // a lane that has given both and may hold more
-            const bool empty = best.b1 == -INFINITY && taken != 0u && taken != ~0u;
-            if (__any_sync(kFullMask, empty)) {
-                if (empty) {
-                    best.find(by, taken);
-                    if (best.b1 == -INFINITY) taken = ~0u;
-                }
+            const int j = __shfl_sync(kFullMask, best.i1, row0 + owner);
+            if (sub == n && top > -INFINITY) expert = owner * V + j;
+            if (gives) {
+                taken |= 1u << best.i1;
+                best.give();
             }
         }
+        const T *p = static_cast<const T *>(a.logits) + row * a.stride;
         const float zc = expert >= 0 ? Vec<T>::to_float(p[expert]) : -INFINITY;
-        float g = a.renormalise ? share_of<L>(zc, a.sigmoid) : expert >= 0 ? score(zc) : 0.0f;
+        float g = a.renormalise ? share_of<L>(zc, a.sigmoid)
+                  : expert < 0  ? 0.0f
+                  : a.sigmoid   ? sigmoid(zc)
+                                : exp_of(zc - m) * rs;
         g = odd ? nan_f() : g * a.scale;
         if (row < a.rows && sub < a.k) {
             a.chosen[row * a.k + sub] = expert;
@@ -1055,6 +1081,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route(RouteArgs a) {
     }
     if (a.counts) {
         __syncthreads();
+        wait_prerequisites();  // k_zero is done
         for (int j = threadIdx.x; j < E; j += kRouteThreads)
             if (counts[j]) atomicAdd(&a.counts[j], static_cast<unsigned long long>(counts[j]));
     }
@@ -1104,7 +1131,9 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(RouteArgs a) {
         } else {
             float m = -INFINITY, s = 0.0f;
             if (live) {
-                load_columns<T, V>(out, p, j0, E);
+                uint4 raw[V / Vec<T>::kN];
+                load_columns<T, V>(raw, p, j0, E);
+                unpack_columns<T, V>(out, raw);
             } else {
 #pragma unroll
                 for (int i = 0; i < V; ++i) out[i] = -INFINITY;
@@ -1236,12 +1265,14 @@ cudaError_t launch_route_any(DType t, const RouteArgs &a, bool grad, const Devic
                                   : route_kernel_t<__half>(lanes, v, grad);
     const int per = kRouteWarps * (32 / lanes);  // rows of a CTA
     const int64_t need = (a.rows + per - 1) / per;
-    const int64_t ctas = capped(std::min<int64_t>(need, 8 * static_cast<int64_t>(dev.sms)), a.grid_cap);
+    const int resident = grad ? 8 : route_ctas(v);
+    const int64_t ctas = capped(std::min<int64_t>(need, resident * static_cast<int64_t>(dev.sms)), a.grid_cap);
     const int smem = grad ? 4 * per * lanes * v
-                          : (a.counts ? 4 * ((a.experts + 3) & ~3) : 0) + (a.top_groups < a.groups ? 4 * per * a.experts : 0);
+                          : 4 * ((a.bias ? lanes * v : 0) + (a.counts ? a.experts : 0) +
+                                 (a.top_groups < a.groups ? per * a.experts : 0));
     RouteArgs aa = a;
     void *args[] = {&aa};
-    LaunchConfig l(ctas, kRouteThreads, 0, false, s, smem);
+    LaunchConfig l(ctas, kRouteThreads, 0, a.counts != nullptr, s, smem);
     return cudaLaunchKernelExC(&l.cfg, fn, args);
 }
 
@@ -1280,8 +1311,10 @@ cudaError_t launch_verify(DType t, const ChoiceArgs &a, void *work, const Device
 }
 
 cudaError_t launch_route(DType t, const RouteArgs &a, const DeviceInfo &dev, cudaStream_t s) {
+    g_launched.note(dev);
     if (a.counts) {
-        const cudaError_t e = cudaMemsetAsync(a.counts, 0, sizeof(unsigned long long) * a.experts, s);
+        LaunchConfig l(1, kRouteThreads, 0, false, s);
+        const cudaError_t e = cudaLaunchKernelEx(&l.cfg, k_zero, a.counts, a.experts);
         if (e != cudaSuccess || a.rows == 0) return e;
     }
     return launch_route_any(t, a, false, dev, s);

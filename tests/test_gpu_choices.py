@@ -668,3 +668,48 @@ def test_changed_in_place():
     out = torch.zeros(4, dtype=torch.int64, device=DEV)
     ce.sample_rows(torch.randn(4, 8, device=DEV), torch.rand(4, device=DEV), out=out)
     assert out._version == 1
+
+
+def test_behind_other_work():
+    """Each call behind a kernel, a copy, another stream's event and the calls themselves, eager and
+    captured: their inputs are made right before them, on the same memory, and their outputs used right after."""
+    x = torch.randn(4, 64, 30000, device=DEV)
+    u = torch.rand(4, 64, device=DEV)
+    want = [ce.sample_rows(x[i] * 2, u[i]) for i in range(4)]
+    routed = [ce.route_rows(x[i][:, :64].contiguous(), 4, counts=True) for i in range(4)]
+    torch.cuda.synchronize()
+    buf, num, cols = torch.empty_like(x[0]), torch.empty_like(u[0]), torch.empty(64, 64, device=DEV)
+    side = torch.cuda.Stream()
+
+    def chain():
+        out = []
+        for i in range(4):
+            buf.copy_(x[i])
+            buf.mul_(2)
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                num.copy_(u[i])
+            torch.cuda.current_stream().wait_stream(side)
+            tokens = ce.sample_rows(buf, num)
+            again = ce.sample_rows(buf, num)
+            buf.fill_(0)
+            cols.copy_(x[i][:, :64])
+            chosen, gates, counts = ce.route_rows(cols, 4, counts=True)
+            cols.fill_(math.nan)
+            out.append((tokens + 0, again, chosen, gates * 1, counts))
+        return out
+
+    def check(out):
+        for i in range(4):
+            tokens, again, chosen, gates, counts = out[i]
+            assert torch.equal(tokens, want[i]) and torch.equal(again, want[i])
+            assert all(torch.equal(p, q) for p, q in zip((chosen, gates, counts), routed[i]))
+    for _ in range(5):
+        check(chain())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain()
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    check(out)
