@@ -572,6 +572,7 @@ CE_API int sample_rows(const void *logits, int dtype, int64_t rows, int64_t voca
  *     last, and for rows in no request.   logp: [rows] f32, or NULL: the
  *     token's log-probability under p (0 at temperature 0 and where none is
  *     emitted).
+ * What is counted, is so once for a request that it ends.
  *   work: scratch of choice_work(dtype, rows, vocab, requests) bytes, as above.
  */
 CE_API int verify_drafts(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t stride,

@@ -543,7 +543,8 @@ __global__ void __launch_bounds__(kDrawThreads) k_sample(ChoiceArgs a) {
 
 // What becomes of a row: its draft is accepted; or it ends its request, with a
 // token that is known, that comes from p, or that comes from what q leaves of p.
-enum Verdict : int { kAccepted = 0, kKnown = 1, kFromOwn = 2, kFromRest = 3 };
+// Of a row that ends its request kOdd: something of it is to be counted.
+enum Verdict : int { kAccepted = 0, kKnown = 1, kFromOwn = 2, kFromRest = 3, kOdd = 4 };
 struct Open {  // of a row whose token is still to be drawn
     Weigh w;
     float inv_t, s, u;
@@ -573,7 +574,7 @@ __device__ __forceinline__ RowNumbers row_numbers(const ChoiceArgs &a, int64_t r
 }
 
 template <typename T>
-__device__ __forceinline__ Verdict judge(const ChoiceArgs &a, int64_t row, const RowNumbers &r, bool writes, Open *open) {
+__device__ __forceinline__ int judge(const ChoiceArgs &a, int64_t row, const RowNumbers &r, bool writes, Open *open) {
     const int lane = threadIdx.x & 31;
     const Heat heat(r.temperature);
     const bool drafted = r.d >= 0 && !heat.greedy, lookup = drafted && a.draft_logits == nullptr;
@@ -622,41 +623,38 @@ __device__ __forceinline__ Verdict judge(const ChoiceArgs &a, int64_t row, const
             a.tokens[row] = token;
             if (a.logp) a.logp[row] = logp;
         }
-        if (odd) count_bad();
     }
-    return v;
+    return odd ? v | kOdd : v;
 }
 
-// max(0, p - q) added over the columns of a step; all of a warp.
+// max(0, p - q) added over the columns of half a step; all of a warp. Two
+// exponentials a column, at 16 per clock and SM: 30 million columns (235 rows of
+// 128256) take 13 us of them.
 template <typename T>
-__device__ __forceinline__ float residual_of_step(const RowGrid<T> &g, const RowGrid<T> &d, const Beside<T> &beside, int step,
+__device__ __forceinline__ float residual_of_half(const RowGrid<T> &g, const RowGrid<T> &d, const Beside<T> &beside, int half,
                                                   const Weigh &w) {
     constexpr int kU = kScan / 2;
-    const int lane = threadIdx.x & 31, end = min(g.nq, (step + 1) * kStep);
+    const int lane = threadIdx.x & 31, q = half * 32 * kU, end = min(g.nq, q + 32 * kU);
     float sum = 0.0f;
     float e[Vec<T>::kN];
-#pragma unroll 1
-    for (int q = step * kStep; q < end; q += 32 * kU) {
-        const int to = min(end, q + 32 * kU);
-        if (g.whole(q, to) && beside.whole(q, to)) {
-            uint4 x[kU], y[kU];
+    if (g.whole(q, end) && beside.whole(q, end)) {
+        uint4 x[kU], y[kU];
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                const int v = q + 32 * u + lane;
-                x[u] = v < to ? g.load(v) : Vec<T>::lowest();
-                y[u] = v < to ? beside.load(v) : Vec<T>::lowest();
-            }
+        for (int u = 0; u < kU; ++u) {
+            const int v = q + 32 * u + lane;
+            x[u] = v < end ? g.load(v) : Vec<T>::lowest();
+            y[u] = v < end ? beside.load(v) : Vec<T>::lowest();
+        }
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                weights_of<T, true>(e, x[u], y[u], 0, w);
-                sum += sum_of(e);
-            }
-        } else {
-            for (int v = q + lane; v < to; v += 32) {
-                const int j = g.column(v);
-                weights_of<T, true>(e, columns_from(g.p, g.n, j), columns_from(d.p, d.n, j), 0, w);
-                sum += sum_of(e);
-            }
+        for (int u = 0; u < kU; ++u) {
+            weights_of<T, true>(e, x[u], y[u], 0, w);
+            sum += sum_of(e);
+        }
+    } else {
+        for (int v = q + lane; v < end; v += 32) {
+            const int j = g.column(v);
+            weights_of<T, true>(e, columns_from(g.p, g.n, j), columns_from(d.p, d.n, j), 0, w);
+            sum += sum_of(e);
         }
     }
     return warp_sum(sum);
@@ -692,10 +690,10 @@ __global__ void __launch_bounds__(kDrawThreads, 4) k_decide(ChoiceArgs a) {
             if (r < lo || r >= hi) silent(r);
     if (s >= a.requests) return;
     int64_t stop = good ? -1 : 0;
-    int by = -1;  // the warp that judged a row whose token is still to be drawn
+    int by = 0, verdict = kAccepted;  // the warp that judged row `stop`, and what it came to
     for (int64_t r = r0; good && r < r1 && stop < 0; r += kRows) {
         const int64_t row = r + warp;
-        Verdict v = kKnown;
+        int v = kKnown;
         if (r > r0) __syncthreads();  // the verdicts before have been read
         if (has_states(row)) {
             if (r > r0) numbers = row_numbers<T>(a, row);
@@ -708,7 +706,8 @@ __global__ void __launch_bounds__(kDrawThreads, 4) k_decide(ChoiceArgs a) {
         for (int i = 0; i < kRows && r + i < r1; ++i)
             if (verdicts[i] != kAccepted) {
                 stop = r + i;
-                if (verdicts[i] != kKnown) by = i;
+                verdict = verdicts[i];
+                by = i;
                 break;
             }
     }
@@ -716,13 +715,14 @@ __global__ void __launch_bounds__(kDrawThreads, 4) k_decide(ChoiceArgs a) {
     if (writes) {
         if (threadIdx.x == 0) {
             a.accepted[s] = good ? stop - r0 : -1;
-            if (!good) count_bad();
+            if (!good || (verdict & kOdd)) count_bad();
         }
         for (int64_t r = stop + 1 + threadIdx.x; good && r < r1; r += kDrawThreads) silent(r);
     }
-    if (by < 0) return;
+    verdict &= ~kOdd;
+    if (verdict == kAccepted || verdict == kKnown) return;
     const Open o = opens[by];
-    const bool rest = verdicts[by] == kFromRest;
+    const bool rest = verdict == kFromRest;
     const RowGrid<T> g = target_row<T>(a, stop);
     Found f{};
     int step = o.step;
@@ -736,9 +736,10 @@ __global__ void __launch_bounds__(kDrawThreads, 4) k_decide(ChoiceArgs a) {
             cluster_arrive();
             cluster_wait();
         }
-        for (int i = static_cast<int>(rank) * kRows + warp; i < a.steps; i += static_cast<int>(C) * kRows) {
-            const float sum = residual_of_step(g, d, beside, i, o.w);
-            if (lane == 0) __stcg(&states[i].x, sum);
+        float *halves = reinterpret_cast<float *>(states);
+        for (int i = static_cast<int>(rank) * kRows + warp; i < 2 * a.steps; i += static_cast<int>(C) * kRows) {
+            const float sum = residual_of_half(g, d, beside, i, o.w);
+            if (lane == 0) __stcg(halves + i, sum);
         }
         if (C > 1) {
             cluster_arrive_release();
@@ -747,7 +748,8 @@ __global__ void __launch_bounds__(kDrawThreads, 4) k_decide(ChoiceArgs a) {
             __syncthreads();
         }
         if (!writes) return;
-        step = Steps(states, a.steps).draw(kUnitShares, o.u, [&](float2 v) { return v.x; }, t);
+        // steps the halves of which lie behind the row were given sums of 0
+        step = Steps(states, a.steps).draw(kUnitShares, o.u, [&](float2 v) { return v.x + v.y; }, t);
         if (step >= 0) {
             f = column_of<T, true>(g, d, step, o.w, t, sums);
         } else {  // nothing left: the two rows are the same, and the draw is from p
@@ -1191,13 +1193,16 @@ int64_t capped(int64_t clusters, int64_t cap) {
     return std::max<int64_t>(1, cap > 0 ? std::min(clusters, cap) : clusters);
 }
 
-// Steps per warp: two where that leaves more warps than the GPU holds at once.
-// Measured (us, whole calls, 1 / 2 / 3 / 4 / 6 / 8 / 12 steps): sample_rows 1 x
-// 32000 bf16 5.7 / 6.3 / 6.9 / 7.6 / 8.8 / 9.9 / 12; 256 x 151936 19.2 / 19.1 /
-// 19.4 / 18.7 / 19.2 / 20.2 / 22.3; verify_drafts 256 requests of up to 7 drafts
-// of 128256 119.5 / 115.1 / 115.5 / 115.7 / 116.7 / 115.8 / 118.
+// Steps per warp: as many as let the GPU hold all warps at once, up to four; two
+// where that takes more. Measured (us, whole calls, 1 / 2 / 3 / 4 / 6 / 8 / 12
+// steps): sample_rows 1 x 32000 bf16 5.7 / 6.3 / 6.9 / 7.6 / 8.8 / 9.9 / 12; 256 x
+// 151936 19.2 / 19.1 / 19.4 / 18.7 / 19.2 / 20.2 / 22.3; verify_drafts 32
+// requests of up to 6 looked-up drafts of 50257 f32 12.0 / 11.5 / 11.9 / 12.4 /
+// 13.5 / 14.9 / 17.7; 256 of up to 7 drafts of 128256 bf16 119.5 / 115.1 / 115.5
+// / 115.7 / 116.7 / 115.8 / 118.
 int unit_of(int64_t steps, int64_t rows, const DeviceInfo &dev) {
-    return steps * rows > 2 * 8 * kWarps * static_cast<int64_t>(dev.sms) ? 2 : 1;
+    const int64_t resident = 8 * kWarps * static_cast<int64_t>(dev.sms), unit = (steps * rows + resident - 1) / resident;
+    return unit <= 4 ? static_cast<int>(std::max<int64_t>(1, unit)) : 2;
 }
 
 template <typename T>
