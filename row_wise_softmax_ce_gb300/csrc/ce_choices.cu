@@ -1089,16 +1089,90 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(V)) k_route(RouteArg
     }
 }
 
-// k_route_grad: with G = scale * (gates' gradient), s the scores, c the chosen
-// experts, f the chosen's share of their sum and D = sum of f G:
+// The gates' gradient: with G = scale * (gradient of the gates), s the scores, c
+// the chosen experts, f the chosen's share of their sum and D = sum of f G:
 //   renormalised  softmax: dz_c = f (G - D), 0 elsewhere
 //                 sigmoid: dz_c = f (G - D) (1 - s_c), 0 elsewhere
-//   otherwise     softmax: dz_j = s_j ([j chosen] G - sum of s_c G_c)
-//                 sigmoid: dz_c = s_c (1 - s_c) G, 0 elsewhere
-// Only the softmax scores themselves need the whole row; the others read the
-// chosen experts' logits.
-template <typename T, int L, int V>
+//   otherwise     sigmoid: dz_c = s_c (1 - s_c) G, 0 elsewhere
+//                 softmax: dz_j = s_j ([j chosen] G - sum of s_c G_c)
+// Only the last needs the whole row (k_route_grad_full); the others read the
+// chosen experts' logits and write a row that is 0 but for them.
+struct Slot {  // lane i of a row: its i-th expert (-1: none) and G there
+    int c;
+    float G;
+};
+__device__ __forceinline__ Slot slot_at(const RouteArgs &a, int64_t row, int sub) {
+    Slot x{-1, 0.0f};
+    if (row < a.rows && sub < a.k && !(a.weights && a.weights[row] == 0.0f)) {
+        const int64_t at = a.chosen[row * a.k + sub];
+        x.G = a.gates_grad[row * a.k + sub] * a.scale;
+        if (at >= a.experts || at < -1)
+            count_bad();
+        else
+            x.c = static_cast<int>(at);
+    }
+    return x;
+}
+
+// k_route_grad: L lanes per row for its slots. A warp's rows are zeroed and
+// filled in shared memory in the gradient's type and written in whole vectors,
+// side by side in memory where the gradient is dense.
+template <typename T, int L>
 __global__ void __launch_bounds__(kRouteThreads) k_route_grad(RouteArgs a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    constexpr int R = 32 / L, N = Vec<T>::kN;
+    const int lane = threadIdx.x & 31, sub = lane & (L - 1), E = a.experts;
+    const int pitch = (R * E + N - 1) / N;  // vectors of a warp's rows
+    uint4 *vecs = reinterpret_cast<uint4 *>(smem) + (threadIdx.x >> 5) * pitch;
+    T *rows = reinterpret_cast<T *>(vecs), *mine = rows + lane / L * E;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteWarps * R;
+    for (int64_t first = (blockIdx.x * int64_t(kRouteWarps) + (threadIdx.x >> 5)) * R; first < a.rows; first += step) {
+        const int64_t row = first + lane / L;
+        const Slot x = slot_at(a, row, sub);
+        const T *p = static_cast<const T *>(a.logits) + row * a.stride;
+        const float z = x.c >= 0 ? Vec<T>::to_float(p[x.c]) : -INFINITY;
+        for (int i = lane; i < pitch; i += 32) vecs[i] = make_uint4(0, 0, 0, 0);
+        float v = 0.0f;
+        if (a.renormalise) {
+            const float f = share_of<L>(z, a.sigmoid);
+            const float D = row_sum<L>(x.c >= 0 ? f * x.G : 0.0f);
+            v = f * (x.G - D);
+            if (a.sigmoid) v *= sigmoid(-z);
+        } else {
+            v = sigmoid(z) * sigmoid(-z) * x.G;
+        }
+        // an expert that a row names twice: its first lane adds up the others', in
+        // the order of the slots
+        unsigned same = __match_any_sync(kFullMask, x.c >= 0 ? lane / L * E + x.c : -1 - lane);
+        const bool leads = __ffs(same) - 1 == lane;
+        if (__any_sync(kFullMask, !leads)) {
+            float sum = 0.0f;
+            for (int i = 0; i < 32; ++i) {
+                const float o = __shfl_sync(kFullMask, v, i);
+                if (same >> i & 1u) sum += o;
+            }
+            v = sum;
+        }
+        __syncwarp();
+        if (x.c >= 0 && leads) mine[x.c] = Vec<T>::from_float(v);
+        __syncwarp();
+        T *to = static_cast<T *>(a.grad) + first * a.grad_stride;
+        const int here = static_cast<int>(min(int64_t(R), a.rows - first));  // rows
+        if (a.grad_stride == E && (reinterpret_cast<uintptr_t>(to) & 15) == 0) {
+            const int whole = here * E / N;
+            for (int i = lane; i < whole; i += 32) reinterpret_cast<uint4 *>(to)[i] = vecs[i];
+            for (int i = whole * N + lane; i < here * E; i += 32) to[i] = rows[i];
+        } else {
+            for (int r = 0; r < here; ++r)
+                for (int i = lane; i < E; i += 32) to[r * a.grad_stride + i] = rows[r * E + i];
+        }
+        __syncwarp();
+    }
+}
+
+// k_route_grad_full: lanes as in k_route.
+template <typename T, int L, int V>
+__global__ void __launch_bounds__(kRouteThreads) k_route_grad_full(RouteArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int R = 32 / L, kRow = L * V;
     const int lane = threadIdx.x & 31, sub = lane & (L - 1), E = a.experts, j0 = sub * V;
@@ -1108,65 +1182,41 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad(RouteArgs a) {
         const int64_t row = first + lane / L;
         const bool live = row < a.rows && !(a.weights && a.weights[row] == 0.0f);
         const T *p = static_cast<const T *>(a.logits) + row * a.stride;
-        int c = -1;
-        float G = 0.0f;
-        if (live && sub < a.k) {
-            const int64_t at = a.chosen[row * a.k + sub];
-            G = a.gates_grad[row * a.k + sub] * a.scale;
-            if (at >= E || at < -1)
-                count_bad();
-            else
-                c = static_cast<int>(at);
-        }
-        const float z = c >= 0 ? Vec<T>::to_float(p[c]) : -INFINITY;
+        uint4 raw[V / Vec<T>::kN];
+#pragma unroll
+        for (int i = 0; i < V / Vec<T>::kN; ++i) raw[i] = Vec<T>::lowest();
+        if (live) load_columns<T, V>(raw, p, j0, E);
+        const Slot x = slot_at(a, row, sub);
+        const float z = x.c >= 0 ? Vec<T>::to_float(p[x.c]) : -INFINITY;
         float out[V];
+        unpack_columns<T, V>(out, raw);
+        float m = out[0], s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) out[i] = 0.0f;
-        float v = 0.0f;  // the gradient at the chosen expert
-        if (a.renormalise) {
-            const float f = share_of<L>(z, a.sigmoid);
-            const float D = row_sum<L>(c >= 0 ? f * G : 0.0f);
-            if (c >= 0) v = f * (G - D);
-            if (a.sigmoid && c >= 0) v *= sigmoid(-z);
-        } else if (a.sigmoid) {
-            if (c >= 0) v = sigmoid(z) * sigmoid(-z) * G;
-        } else {
-            float m = -INFINITY, s = 0.0f;
-            if (live) {
-                uint4 raw[V / Vec<T>::kN];
-                load_columns<T, V>(raw, p, j0, E);
-                unpack_columns<T, V>(out, raw);
-            } else {
+        for (int i = 1; i < V; ++i) m = fmaxf(m, out[i]);
+        m = row_max<L>(m);
+        if (m == -INFINITY) m = 0.0f;
 #pragma unroll
-                for (int i = 0; i < V; ++i) out[i] = -INFINITY;
-            }
-#pragma unroll
-            for (int i = 0; i < V; ++i) m = fmaxf(m, out[i]);
-            m = row_max<L>(m);
-            if (m == -INFINITY) m = 0.0f;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                out[i] = exp_of(out[i] - m);
-                s += out[i];
-            }
-            s = row_sum<L>(s);
-            const float rs = s > 0.0f || isnan(s) ? 1.0f / s : 0.0f;
-            v = c >= 0 ? exp_of(z - m) * rs * G : 0.0f;
-            const float D = row_sum<L>(v);
-#pragma unroll
-            for (int i = 0; i < V; ++i) out[i] *= -rs * D;
+        for (int i = 0; i < V; ++i) {
+            out[i] = exp_of(out[i] - m);
+            s += out[i];
         }
-        // add v to its column: through shared memory; a column that a row names
+        s = row_sum<L>(s);
+        const float rs = s > 0.0f || isnan(s) ? 1.0f / s : 0.0f;
+        const float v = x.c >= 0 ? exp_of(z - m) * rs * x.G : 0.0f;
+        const float by = -rs * row_sum<L>(v);
+        // v is added to its column through shared memory; a column that a row names
         // twice one after the other, in the order of the slots
 #pragma unroll
-        for (int i = 0; i < V; i += 4) *reinterpret_cast<float4 *>(mine + j0 + i) = make_float4(out[i], out[i + 1], out[i + 2], out[i + 3]);
+        for (int i = 0; i < V; i += 4)
+            *reinterpret_cast<float4 *>(mine + j0 + i) =
+                make_float4(out[i] * by, out[i + 1] * by, out[i + 2] * by, out[i + 3] * by);
         __syncwarp();
-        const unsigned same = __match_any_sync(kFullMask, c >= 0 ? (lane / L) * kRow + c : -1 - lane);
+        const unsigned same = __match_any_sync(kFullMask, x.c >= 0 ? lane / L * kRow + x.c : -1 - lane);
         if (!__any_sync(kFullMask, (same & (same - 1)) != 0)) {
-            if (c >= 0) mine[c] += v;
+            if (x.c >= 0) mine[x.c] += v;
         } else {
             for (int i = 0; i < a.k; ++i) {
-                if (sub == i && c >= 0) mine[c] += v;
+                if (sub == i && x.c >= 0) mine[x.c] += v;
                 __syncwarp();
             }
         }
@@ -1247,9 +1297,10 @@ cudaError_t verify_as(ChoiceArgs a, const DeviceInfo &dev, cudaStream_t s) {
     return cudaLaunchKernelExC(&l.cfg, Kernels<T>::decide(), args);
 }
 
+// lanes per row, columns per lane
 template <typename T, int L, int V>
 const void *route_kernel_v(bool grad) {
-    return grad ? reinterpret_cast<const void *>(&k_route_grad<T, L, V>) : reinterpret_cast<const void *>(&k_route<T, L, V>);
+    return grad ? reinterpret_cast<const void *>(&k_route_grad_full<T, L, V>) : reinterpret_cast<const void *>(&k_route<T, L, V>);
 }
 template <typename T>
 const void *route_kernel_t(int lanes, int v, bool grad) {
@@ -1258,27 +1309,39 @@ const void *route_kernel_t(int lanes, int v, bool grad) {
     if (lanes == 32) return route_kernel_v<T, 32, 8>(grad);
     return lanes == 16 ? route_kernel_v<T, 16, 8>(grad) : route_kernel_v<T, 8, 8>(grad);
 }
+const void *route_kernel(DType t, int lanes, int v, bool grad) {
+    return t == kF32    ? route_kernel_t<float>(lanes, v, grad)
+           : t == kBF16 ? route_kernel_t<__nv_bfloat16>(lanes, v, grad)
+                        : route_kernel_t<__half>(lanes, v, grad);
+}
+template <typename T>
+const void *route_grad_t(int lanes) {
+    return lanes == 32   ? reinterpret_cast<const void *>(&k_route_grad<T, 32>)
+           : lanes == 16 ? reinterpret_cast<const void *>(&k_route_grad<T, 16>)
+                         : reinterpret_cast<const void *>(&k_route_grad<T, 8>);
+}
+const void *route_grad_kernel(DType t, int lanes) {
+    return t == kF32    ? route_grad_t<float>(lanes)
+           : t == kBF16 ? route_grad_t<__nv_bfloat16>(lanes)
+                        : route_grad_t<__half>(lanes);
+}
 
-cudaError_t launch_route_any(DType t, const RouteArgs &a, bool grad, const DeviceInfo &dev, cudaStream_t s) {
-    g_launched.note(dev);
-    // eight columns a lane, as few lanes as hold the row and its k slots
-    int lanes = 8, v = 8;
-    while (lanes < 32 && (lanes * v < a.experts || lanes < a.k)) lanes *= 2;
-    while (lanes * v < a.experts) v *= 2;
-    const void *fn = t == kF32    ? route_kernel_t<float>(lanes, v, grad)
-                     : t == kBF16 ? route_kernel_t<__nv_bfloat16>(lanes, v, grad)
-                                  : route_kernel_t<__half>(lanes, v, grad);
-    const int per = kRouteWarps * (32 / lanes);  // rows of a CTA
+// CTAs of kRouteWarps warps with 32 / lanes rows each, `resident` per SM at most.
+cudaError_t launch_route_rows(const void *fn, const RouteArgs &a, int lanes, int resident, int smem, bool dependent,
+                              const DeviceInfo &dev, cudaStream_t s) {
+    const int per = kRouteWarps * (32 / lanes);
     const int64_t need = (a.rows + per - 1) / per;
-    const int resident = grad ? 8 : route_ctas(v);
     const int64_t ctas = capped(std::min<int64_t>(need, resident * static_cast<int64_t>(dev.sms)), a.grid_cap);
-    const int smem = grad ? 4 * per * lanes * v
-                          : 4 * ((a.bias ? lanes * v : 0) + (a.counts ? a.experts : 0) +
-                                 (a.top_groups < a.groups ? per * a.experts : 0));
     RouteArgs aa = a;
     void *args[] = {&aa};
-    LaunchConfig l(ctas, kRouteThreads, 0, a.counts != nullptr, s, smem);
+    LaunchConfig l(ctas, kRouteThreads, 0, dependent, s, smem);
     return cudaLaunchKernelExC(&l.cfg, fn, args);
+}
+
+// Eight columns a lane, as few lanes as hold the row and its k slots.
+void route_shape(const RouteArgs &a, int *lanes, int *v) {
+    for (*lanes = 8; *lanes < 32 && (*lanes * 8 < a.experts || *lanes < a.k);) *lanes *= 2;
+    for (*v = 8; *lanes * *v < a.experts;) *v *= 2;
 }
 
 }  // namespace
@@ -1322,11 +1385,28 @@ cudaError_t launch_route(DType t, const RouteArgs &a, const DeviceInfo &dev, cud
         const cudaError_t e = cudaLaunchKernelEx(&l.cfg, k_zero, a.counts, a.experts);
         if (e != cudaSuccess || a.rows == 0) return e;
     }
-    return launch_route_any(t, a, false, dev, s);
+    int lanes, v;
+    route_shape(a, &lanes, &v);
+    const int smem = 4 * ((a.bias ? lanes * v : 0) + (a.counts ? a.experts : 0) +
+                          (a.top_groups < a.groups ? kRouteWarps * (32 / lanes) * a.experts : 0));
+    return launch_route_rows(route_kernel(t, lanes, v, false), a, lanes, route_ctas(v), smem, a.counts != nullptr, dev, s);
 }
 
 cudaError_t launch_route_grad(DType t, const RouteArgs &a, const DeviceInfo &dev, cudaStream_t s) {
-    return launch_route_any(t, a, true, dev, s);
+    g_launched.note(dev);
+    int lanes, v;
+    if (!a.sigmoid && !a.renormalise) {
+        route_shape(a, &lanes, &v);
+        return launch_route_rows(route_kernel(t, lanes, v, true), a, lanes, 8, 4 * kRouteWarps * 32 * v, false, dev, s);
+    }
+    for (lanes = 8; lanes < a.k;) lanes *= 2;
+    const int N = 16 / elem_size(t), smem = 16 * kRouteWarps * ((32 / lanes * a.experts + N - 1) / N);
+    const void *fn = route_grad_kernel(t, lanes);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, dev.max_smem_optin);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_route_rows(fn, a, lanes, 8, smem, false, dev, s);
 }
 
 cudaError_t read_choice_status(unsigned long long out[2], const DeviceInfo &dev, cudaStream_t s) {
