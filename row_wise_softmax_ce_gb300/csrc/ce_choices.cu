@@ -845,9 +845,9 @@ __device__ __forceinline__ unsigned row_ballot(bool b) {
     return L == 32 ? all : (all >> (threadIdx.x & 31 & ~(L - 1))) & ((1u << (L & 31)) - 1u);
 }
 // a NaN wins
-__device__ __forceinline__ float max_nan(float a, float b) {
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
@@ -879,35 +879,6 @@ __device__ __forceinline__ float share_of(float z, bool sigmoid_scores) {
     return e / (all > 0.0f || isnan(all) ? all : 1.0f);
 }
 
-// The two largest of a lane's values that are not taken, the lower of equals
-// first, and the value of the third.
-template <int V>
-struct Best {
-    float b1, b2, b3;
-    int i1, i2;
-    __device__ __forceinline__ void find(const float (&by)[V], unsigned taken) {
-        b1 = b2 = b3 = -INFINITY;
-        i1 = i2 = 0;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float v = taken >> i & 1u ? -INFINITY : by[i];
-            const bool first = v > b1, second = v > b2;
-            i2 = first ? i1 : second ? i : i2;
-            i1 = first ? i : i1;
-            b3 = fmaxf(b3, fminf(b2, v));
-            b2 = fmaxf(b2, fminf(b1, v));
-            b1 = fmaxf(b1, v);
-        }
-    }
-    // the largest is given away; the third's column is looked for when it is asked for
-    __device__ __forceinline__ void give() {
-        b1 = b2, i1 = i2;
-        b2 = b3, i2 = -1;
-        b3 = -INFINITY;
-    }
-    __device__ __forceinline__ void none() { b1 = b2 = b3 = -INFINITY; }
-};
-
 // The counts are zeroed by a kernel that k_route, launched as its programmatic
 // dependent, runs beside and waits for before it adds to them (a memset before
 // k_route: 4 us more).
@@ -917,53 +888,58 @@ __global__ void __launch_bounds__(kRouteThreads) k_zero(unsigned long long *coun
 }
 
 // CTAs of an SM, by the columns a lane holds.
-__host__ __device__ constexpr int route_ctas(int v) { return v > 16 ? 1 : v > 8 ? 2 : 4; }
+__host__ __device__ constexpr int route_ctas(int v) { return v > 16 ? 3 : 4; }
+// Floats of a row in shared memory: its lanes' columns, 16 bytes apart by bank.
+__host__ __device__ constexpr int route_row(int lanes, int v) { return lanes * (v + 4); }
 
-// k_route: bound by the instructions of the choice, so several rows share a
-// warp's instructions, and each lane keeps its two best columns at hand, and the
-// value of the third: a lane is searched again only when its third is chosen.
+// k_route: bound by the instructions of the choice, most of them compares at half
+// rate. So as many rows as there are slots share a warp's instructions, and a
+// lane keeps the largest of each eight of its columns only: the columns lie in
+// shared memory, where the lane that gives one looks for it among eight, takes
+// it out and has the largest of the rest. Measured (us, 16384 x 256 bf16, k = 8,
+// sigmoid scores with a bias, 4 of 8 groups): this 11.6; a row a warp, with each
+// lane's two best columns and the value of its third in registers, 16.0. Counts
+// add 1.1 us, and 1.4 more with a CTA per 32 rows than with three an SM.
 template <typename T, int L, int V>
 __global__ void __launch_bounds__(kRouteThreads, route_ctas(V)) k_route(RouteArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
-    constexpr int R = 32 / L, kVecs = V / Vec<T>::kN;  // rows of a warp
+    constexpr int R = 32 / L, kVecs = V / Vec<T>::kN, kBlocks = V / 8, kLane = V + 4;  // rows of a warp
     const int lane = threadIdx.x & 31, sub = lane & (L - 1), row0 = lane & ~(L - 1), E = a.experts, j0 = sub * V;
     const int per = E / a.groups;
     const bool grouped = a.top_groups < a.groups;
     // groups of whole lanes, a power of two of them
     const int wide = per / V;
     const bool by_lanes = grouped && per % V == 0 && (wide & (wide - 1)) == 0 && wide <= L;
-    float *bias = reinterpret_cast<float *>(smem);           // [L V], if there is one
-    int *counts = reinterpret_cast<int *>(bias + (a.bias ? L * V : 0));  // [experts], if wanted
-    // group scores by way of shared memory: [rows of the CTA, experts]
-    float *mine = reinterpret_cast<float *>(counts + (a.counts ? E : 0)) + ((threadIdx.x >> 5) * R + lane / L) * E;
+    float *all = reinterpret_cast<float *>(smem);
+    float *row_keys = all + ((threadIdx.x >> 5) * R + lane / L) * route_row(L, V), *mine = row_keys + sub * kLane;
+    float *bias = all + kRouteWarps * R * route_row(L, V);  // as a row, if there is one
+    int *counts = reinterpret_cast<int *>(bias + (a.bias ? route_row(L, V) : 0));  // [experts], if wanted
     if (a.bias || a.counts) {
         if (a.bias)
-            for (int j = threadIdx.x; j < L * V; j += kRouteThreads) bias[j] = j < E ? a.bias[j] : 0.0f;
+            for (int j = threadIdx.x; j < L * V; j += kRouteThreads) {
+                const float b = j < E ? a.bias[j] : 0.0f;
+                bias[j / V * kLane + j % V] = isnan(b) ? -INFINITY : b;
+            }
         if (a.counts)
             for (int j = threadIdx.x; j < E; j += kRouteThreads) counts[j] = 0;
         __syncthreads();
     }
     const int64_t step = static_cast<int64_t>(gridDim.x) * kRouteWarps * R;
-    uint4 next[kVecs];
-    // a row's logits, asked for a row ahead: -inf for a padding row or none
-    auto load = [&](int64_t row) {
-        if (row < a.rows && !(a.weights && a.weights[row] == 0.0f)) {
-            load_columns<T, V>(next, static_cast<const T *>(a.logits) + row * a.stride, j0, E);
-        } else {
-#pragma unroll
-            for (int i = 0; i < kVecs; ++i) next[i] = Vec<T>::lowest();
-        }
-    };
-    int64_t first = (blockIdx.x * int64_t(kRouteWarps) + (threadIdx.x >> 5)) * R;
-    load(first + lane / L);
-    for (; first < a.rows; first += step) {
+    for (int64_t first = (blockIdx.x * int64_t(kRouteWarps) + (threadIdx.x >> 5)) * R; first < a.rows; first += step) {
         const int64_t row = first + lane / L;
         float z[V];
-        unpack_columns<T, V>(z, next);
-        if (first + step < a.rows) load(row + step);
-        float m = z[0];
+        {
+            uint4 raw[kVecs];  // -inf for a padding row or none
 #pragma unroll
-        for (int i = 1; i < V; ++i) m = max_nan(m, z[i]);
+            for (int i = 0; i < kVecs; ++i) raw[i] = Vec<T>::lowest();
+            if (row < a.rows && !(a.weights && a.weights[row] == 0.0f))
+                load_columns<T, V>(raw, static_cast<const T *>(a.logits) + row * a.stride, j0, E);
+            unpack_columns<T, V>(z, raw);
+        }
+        float m = max_nan(z[0], z[1], z[2]);
+#pragma unroll
+        for (int i = 3; i + 1 < V; i += 2) m = max_nan(m, z[i], z[i + 1]);
+        m = max_nan(m, z[V - 1], z[V - 1]);
         const bool odd = row_ballot<L>(!(m < INFINITY)) != 0;  // a NaN or +inf
         if (odd) {
             m = -INFINITY;
@@ -982,61 +958,40 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(V)) k_route(RouteArg
         // what the choice goes by, from here on in z: the biased score, or, without a
         // bias, the logit, which orders the experts as their scores do and is exact
         if (a.bias) {
-            auto biased = [&](float c, int i) { return z[i] > -INFINITY && c > -INFINITY ? c : -INFINITY; };
+            const float *b = bias + sub * kLane;
             if (a.sigmoid) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) z[i] = biased(sigmoid(z[i]) + bias[j0 + i], i);
+                for (int i = 0; i < V; i += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(b + i);
+                    z[i] = z[i] > -INFINITY ? sigmoid(z[i]) + f.x : -INFINITY;
+                    z[i + 1] = z[i + 1] > -INFINITY ? sigmoid(z[i + 1]) + f.y : -INFINITY;
+                    z[i + 2] = z[i + 2] > -INFINITY ? sigmoid(z[i + 2]) + f.z : -INFINITY;
+                    z[i + 3] = z[i + 3] > -INFINITY ? sigmoid(z[i + 3]) + f.w : -INFINITY;
+                }
             } else {
 #pragma unroll
-                for (int i = 0; i < V; ++i) z[i] = biased(exp_of(z[i] - m) * rs + bias[j0 + i], i);
-            }
-        }
-        auto ranked = [&](float v) { return a.bias || v == -INFINITY ? v : relative_score(v, m, a.sigmoid); };
-        Best<V> best;
-        unsigned taken = 0;
-        if (grouped && !by_lanes) {
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (j0 + i < E) mine[j0 + i] = ranked(z[i]);
-            __syncwarp();
-            auto group_score = [&](int g) {
-                float g1 = -INFINITY, g2 = -INFINITY;
-                for (int i = 0; i < per; ++i) {
-                    const float v = mine[g * per + i];
-                    g2 = fmaxf(g2, fminf(v, g1));
-                    g1 = fmaxf(g1, v);
+                for (int i = 0; i < V; i += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(b + i);
+                    z[i] = z[i] > -INFINITY ? exp_of(z[i] - m) * rs + f.x : -INFINITY;
+                    z[i + 1] = z[i + 1] > -INFINITY ? exp_of(z[i + 1] - m) * rs + f.y : -INFINITY;
+                    z[i + 2] = z[i + 2] > -INFINITY ? exp_of(z[i + 2] - m) * rs + f.z : -INFINITY;
+                    z[i + 3] = z[i + 3] > -INFINITY ? exp_of(z[i + 3] - m) * rs + f.w : -INFINITY;
                 }
-                return a.group_top == 2 && g2 > -INFINITY ? g1 + g2 : g1;
-            };
-            // lane i of the row has groups i, i + L, ..: their scores first, over
-            // their first members, then how many come before each
-            constexpr int kMost = kMaxGroups / L;
-            float rank_by[kMost];
-#pragma unroll
-            for (int h = 0; h < kMost; ++h) rank_by[h] = sub + h * L < a.groups ? group_score(sub + h * L) : -INFINITY;
-            __syncwarp();
-#pragma unroll
-            for (int h = 0; h < kMost; ++h)
-                if (sub + h * L < a.groups) mine[sub + h * L] = rank_by[h];
-            __syncwarp();
-            unsigned kept = 0;
-#pragma unroll
-            for (int h = 0; h < kMost; ++h) {
-                const int own = sub + h * L;
-                int before = 0;
-                for (int g = 0; g < a.groups; ++g) before += mine[g] > rank_by[h] || (mine[g] == rank_by[h] && g < own);
-                if (own < a.groups && before < a.top_groups) kept |= 1u << own;
             }
-#pragma unroll
-            for (int o = L / 2; o > 0; o >>= 1) kept |= __shfl_xor_sync(kFullMask, kept, o);
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (j0 + i >= E || !(kept >> ((j0 + i) / per) & 1u)) z[i] = -INFINITY;
         }
-        best.find(z, 0u);
+#pragma unroll
+        for (int i = 0; i < V; i += 4) *reinterpret_cast<float4 *>(mine + i) = make_float4(z[i], z[i + 1], z[i + 2], z[i + 3]);
+        auto ranked = [&](float v) { return a.bias || v == -INFINITY ? v : relative_score(v, m, a.sigmoid); };
+        bool dropped = false;
         if (by_lanes) {
-            float g1 = ranked(best.b1), g2 = ranked(best.b2);
+            float g1 = -INFINITY, g2 = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                g2 = fmaxf(g2, fminf(g1, z[i]));
+                g1 = fmaxf(g1, z[i]);
+            }
+            g1 = ranked(g1);
+            g2 = ranked(g2);
             for (int o = 1; o < wide; o <<= 1) {
                 const float o1 = __shfl_xor_sync(kFullMask, g1, o), o2 = __shfl_xor_sync(kFullMask, g2, o);
                 g2 = fmaxf(fminf(g1, o1), fmaxf(g2, o2));
@@ -1049,23 +1004,93 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(V)) k_route(RouteArg
                 const float o = __shfl_sync(kFullMask, rank_by, row0 + g * wide);
                 before += o > rank_by || (o == rank_by && g < own);
             }
-            if (before >= a.top_groups || own >= a.groups) best.none();
+            dropped = before >= a.top_groups || own >= a.groups;
+        } else if (grouped) {
+            __syncwarp();
+            auto group_score = [&](int g) {
+                float g1 = -INFINITY, g2 = -INFINITY;
+                for (int j = g * per; j < g * per + per; ++j) {
+                    const float v = row_keys[j / V * kLane + j % V];
+                    g2 = fmaxf(g2, fminf(v, g1));
+                    g1 = fmaxf(g1, v);
+                }
+                g1 = ranked(g1);
+                g2 = ranked(g2);
+                return a.group_top == 2 && g2 > -INFINITY ? g1 + g2 : g1;
+            };
+            // lane i of the row has groups i, i + L, ..
+            constexpr int kMost = kMaxGroups / L;
+            float rank_by[kMost];
+            int before[kMost];
+#pragma unroll
+            for (int h = 0; h < kMost; ++h) {
+                rank_by[h] = sub + h * L < a.groups ? group_score(sub + h * L) : -INFINITY;
+                before[h] = 0;
+            }
+#pragma unroll
+            for (int other = 0; other < kMost; ++other)
+                for (int l = 0; l < L && other * L + l < a.groups; ++l) {
+                    const float o = __shfl_sync(kFullMask, rank_by[other], row0 + l);
+#pragma unroll
+                    for (int h = 0; h < kMost; ++h)
+                        before[h] += o > rank_by[h] || (o == rank_by[h] && other * L + l < sub + h * L);
+                }
+            unsigned kept = 0;
+#pragma unroll
+            for (int h = 0; h < kMost; ++h)
+                if (sub + h * L < a.groups && before[h] < a.top_groups) kept |= 1u << (sub + h * L);
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) kept |= __shfl_xor_sync(kFullMask, kept, o);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (j0 + i >= E || !(kept >> ((j0 + i) / per) & 1u)) z[i] = mine[i] = -INFINITY;
         }
+        float top_of[kBlocks], best = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+            float t = z[8 * b];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) t = fmaxf(t, z[8 * b + i]);
+            top_of[b] = t;
+            best = fmaxf(best, t);
+        }
+        if (dropped) best = -INFINITY;
         // the k best, one after another: the largest, the lowest column of equals
         int expert = -1;  // lane i of the row: the i-th
         for (int n = 0; n < a.k; ++n) {
-            const float top = row_max<L>(best.b1);
-            const int owner = __ffs(row_ballot<L>(best.b1 == top)) - 1;
-            const bool gives = sub == owner && top > -INFINITY, unknown = gives && best.i1 < 0;
-            if (__any_sync(kFullMask, unknown)) {
-                if (unknown) best.find(z, taken);
+            const float top = row_max<L>(best);
+            const int owner = __ffs(row_ballot<L>(best == top)) - 1;
+            int j = 0;
+            if (sub == owner && top > -INFINITY) {
+                int block = kBlocks - 1;
+#pragma unroll
+                for (int b = kBlocks - 2; b >= 0; --b)
+                    if (top_of[b] == top) block = b;
+                float4 *at = reinterpret_cast<float4 *>(mine + 8 * block);
+                const float4 lo = at[0], hi = at[1];
+                float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                int i = 7;
+                // the second largest of the eight, which is the largest again if two share it
+                float one = v[0], rest = -INFINITY;
+#pragma unroll
+                for (int h = 1; h < 8; ++h) {
+                    rest = fmaxf(rest, fminf(one, v[h]));
+                    one = fmaxf(one, v[h]);
+                }
+#pragma unroll
+                for (int h = 6; h >= 0; --h)
+                    if (v[h] == top) i = h;
+                reinterpret_cast<float *>(at)[i] = -INFINITY;
+                best = -INFINITY;
+#pragma unroll
+                for (int b = 0; b < kBlocks; ++b) {
+                    if (b == block) top_of[b] = rest;
+                    best = fmaxf(best, top_of[b]);
+                }
+                j = j0 + 8 * block + i;
             }
-            const int j = __shfl_sync(kFullMask, best.i1, row0 + owner);
-            if (sub == n && top > -INFINITY) expert = owner * V + j;
-            if (gives) {
-                taken |= 1u << best.i1;
-                best.give();
-            }
+            j = __shfl_sync(kFullMask, j, row0 + owner);
+            if (sub == n && top > -INFINITY) expert = j;
         }
         const T *p = static_cast<const T *>(a.logits) + row * a.stride;
         const float zc = expert >= 0 ? Vec<T>::to_float(p[expert]) : -INFINITY;
@@ -1080,6 +1105,7 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(V)) k_route(RouteArg
         }
         if (odd && sub == 0) count_bad();
         if (a.counts && expert >= 0) atomicAdd(&counts[expert], 1);
+        __syncwarp();  // the row's columns are written anew
     }
     if (a.counts) {
         __syncthreads();
@@ -1297,22 +1323,34 @@ cudaError_t verify_as(ChoiceArgs a, const DeviceInfo &dev, cudaStream_t s) {
     return cudaLaunchKernelExC(&l.cfg, Kernels<T>::decide(), args);
 }
 
-// lanes per row, columns per lane
-template <typename T, int L, int V>
-const void *route_kernel_v(bool grad) {
-    return grad ? reinterpret_cast<const void *>(&k_route_grad_full<T, L, V>) : reinterpret_cast<const void *>(&k_route<T, L, V>);
+template <typename T, int L>
+const void *route_kernel_l(int v) {
+    return v == 32   ? reinterpret_cast<const void *>(&k_route<T, L, 32>)
+           : v == 16 ? reinterpret_cast<const void *>(&k_route<T, L, 16>)
+                     : reinterpret_cast<const void *>(&k_route<T, L, 8>);
 }
 template <typename T>
-const void *route_kernel_t(int lanes, int v, bool grad) {
-    if (v == 32) return route_kernel_v<T, 32, 32>(grad);
-    if (v == 16) return route_kernel_v<T, 32, 16>(grad);
-    if (lanes == 32) return route_kernel_v<T, 32, 8>(grad);
-    return lanes == 16 ? route_kernel_v<T, 16, 8>(grad) : route_kernel_v<T, 8, 8>(grad);
+const void *route_kernel_t(int lanes, int v) {
+    return lanes == 32 ? route_kernel_l<T, 32>(v) : lanes == 16 ? route_kernel_l<T, 16>(v) : route_kernel_l<T, 8>(v);
 }
-const void *route_kernel(DType t, int lanes, int v, bool grad) {
-    return t == kF32    ? route_kernel_t<float>(lanes, v, grad)
-           : t == kBF16 ? route_kernel_t<__nv_bfloat16>(lanes, v, grad)
-                        : route_kernel_t<__half>(lanes, v, grad);
+const void *route_kernel(DType t, int lanes, int v) {
+    return t == kF32    ? route_kernel_t<float>(lanes, v)
+           : t == kBF16 ? route_kernel_t<__nv_bfloat16>(lanes, v)
+                        : route_kernel_t<__half>(lanes, v);
+}
+// at eight columns a lane, more where 32 lanes do not hold the row
+template <typename T>
+const void *route_full_t(int lanes, int v) {
+    return v == 32       ? reinterpret_cast<const void *>(&k_route_grad_full<T, 32, 32>)
+           : v == 16     ? reinterpret_cast<const void *>(&k_route_grad_full<T, 32, 16>)
+           : lanes == 32 ? reinterpret_cast<const void *>(&k_route_grad_full<T, 32, 8>)
+           : lanes == 16 ? reinterpret_cast<const void *>(&k_route_grad_full<T, 16, 8>)
+                         : reinterpret_cast<const void *>(&k_route_grad_full<T, 8, 8>);
+}
+const void *route_full_kernel(DType t, int lanes, int v) {
+    return t == kF32    ? route_full_t<float>(lanes, v)
+           : t == kBF16 ? route_full_t<__nv_bfloat16>(lanes, v)
+                        : route_full_t<__half>(lanes, v);
 }
 template <typename T>
 const void *route_grad_t(int lanes) {
@@ -1338,10 +1376,22 @@ cudaError_t launch_route_rows(const void *fn, const RouteArgs &a, int lanes, int
     return cudaLaunchKernelExC(&l.cfg, fn, args);
 }
 
-// Eight columns a lane, as few lanes as hold the row and its k slots.
-void route_shape(const RouteArgs &a, int *lanes, int *v) {
-    for (*lanes = 8; *lanes < 32 && (*lanes * 8 < a.experts || *lanes < a.k);) *lanes *= 2;
+// As few lanes as hold a row's k slots, and its columns at `most` each.
+void route_shape(const RouteArgs &a, int most, int *lanes, int *v) {
+    for (*lanes = 8; *lanes < 32 && (*lanes * most < a.experts || *lanes < a.k);) *lanes *= 2;
     for (*v = 8; *lanes * *v < a.experts;) *v *= 2;
+}
+
+// Columns of a lane at most: 32, where rows are many and instructions count; 8
+// where they are few, a row's latency counts and lanes are to spare. Measured
+// (us, bf16, k = 8, sigmoid scores with a bias, 8 / 32 columns): 256 experts in 8
+// groups, 32 rows 4.2 / 5.7, 1024 4.4 / 5.9, 2048 5.3 / 6.0, 4096 7.6 / 6.2, 8192
+// 13.1 / 7.9, 16384 20.8 / 11.9, 65536 76 / 34; 512 experts, 1024 rows 5.0 / 6.3,
+// 4096 8.6 / 7.8, 16384 24 / 18.
+int route_most(const RouteArgs &a, const DeviceInfo &dev) {
+    int lanes, v;
+    route_shape(a, 8, &lanes, &v);
+    return a.rows * lanes <= 12 * 32 * static_cast<int64_t>(dev.sms) ? 8 : 32;
 }
 
 }  // namespace
@@ -1386,18 +1436,18 @@ cudaError_t launch_route(DType t, const RouteArgs &a, const DeviceInfo &dev, cud
         if (e != cudaSuccess || a.rows == 0) return e;
     }
     int lanes, v;
-    route_shape(a, &lanes, &v);
-    const int smem = 4 * ((a.bias ? lanes * v : 0) + (a.counts ? a.experts : 0) +
-                          (a.top_groups < a.groups ? kRouteWarps * (32 / lanes) * a.experts : 0));
-    return launch_route_rows(route_kernel(t, lanes, v, false), a, lanes, route_ctas(v), smem, a.counts != nullptr, dev, s);
+    route_shape(a, route_most(a, dev), &lanes, &v);
+    const int smem = 4 * ((kRouteWarps * (32 / lanes) + (a.bias ? 1 : 0)) * route_row(lanes, v) +
+                          (a.counts ? a.experts : 0));  // at most 45568 bytes
+    return launch_route_rows(route_kernel(t, lanes, v), a, lanes, route_ctas(v), smem, a.counts != nullptr, dev, s);
 }
 
 cudaError_t launch_route_grad(DType t, const RouteArgs &a, const DeviceInfo &dev, cudaStream_t s) {
     g_launched.note(dev);
     int lanes, v;
     if (!a.sigmoid && !a.renormalise) {
-        route_shape(a, &lanes, &v);
-        return launch_route_rows(route_kernel(t, lanes, v, true), a, lanes, 8, 4 * kRouteWarps * 32 * v, false, dev, s);
+        route_shape(a, 8, &lanes, &v);
+        return launch_route_rows(route_full_kernel(t, lanes, v), a, lanes, 8, 4 * kRouteWarps * 32 * v, false, dev, s);
     }
     for (lanes = 8; lanes < a.k;) lanes *= 2;
     const int N = 16 / elem_size(t), smem = 16 * kRouteWarps * ((32 / lanes * a.experts + N - 1) / N);
