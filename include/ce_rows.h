@@ -501,8 +501,8 @@ CE_API int preference_step(const void *logits, int dtype, int64_t rows, int64_t 
  *
  *  - Logits are CE_F32, CE_BF16 or CE_F16, rows as above, fewer than 2^31 of
  *    them; arithmetic is f32, sums over a row of 32 bits or more.
- *  - The random numbers are inputs: f32 in [0, 1); a number outside counts as
- *    the nearest inside, NaN as 0.
+ *  - The random numbers are inputs: f32 in [0, 1); of a number that draws, one
+ *    outside counts as the nearest inside, NaN as 0.
  *  - Tokens and experts are int64; -1: none. Of equal columns the lowest wins.
  *  - A row holding a NaN or +inf, or nothing above -inf, is no distribution:
  *    its token is -1 and its log-probability NaN, and the device counter
@@ -546,7 +546,8 @@ CE_API int sample_rows(const void *logits, int dtype, int64_t rows, int64_t voca
  * Request s is rows offsets[s] .. offsets[s + 1] - 1. With p and q the softmax
  * of a row and of its draft row at the row's temperature, (a, u) its two random
  * numbers and d its draft:
- *     d is accepted where a q_d < p_d;
+ *     d is accepted where a q_d < p_d (a as it is given: a NaN accepts
+ *     nothing) and p_d > 0;
  *     otherwise a token is drawn by u, as sample_rows draws it, from
  *     max(0, p_j - q_j) in proportion.
  * A request emits its accepted drafts, row by row, up to the first row that

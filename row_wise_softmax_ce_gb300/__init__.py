@@ -684,7 +684,7 @@ def verify_drafts(logits: torch.Tensor, drafts: torch.Tensor, offsets: torch.Ten
     a request's last draft), ``draft_logits`` the logits that they were drawn
     from, row by row, in the logits' type; None: they were looked up.
     ``uniforms`` f32 ``[rows, 2]``: the number that accepts and the one that draws.
-    A row accepts where ``uniforms[0] * q < p``; a request emits its accepted
+    A row accepts where ``uniforms[0] * q < p`` and ``p > 0``; a request emits its accepted
     drafts and, at the first row that accepts none, a token drawn from the rest,
     max(0, p - q), or from p where there is no draft. ``temperature`` as in
     ``sample_rows``. Returns ``(accepted, tokens, logp)``: int64 ``[requests]``,

@@ -7,16 +7,26 @@
 //   route_grad      the gradient of the gates
 //
 // Kernels (none uses tensor cores):
-//   k_states        every row in steps of 4 KB, a state (m, s) for each step: one
-//                   read of the logits, and of the draft rows, in parts of any
-//                   number of warps
-//   k_sample        sample_rows: a warp per row merges its states, draws a step by
-//                   their masses and re-reads that step
-//   k_decide        verify_drafts: a cluster per request merges its rows' states,
-//                   finds the first that accepts no draft, and draws its token: from
-//                   p, or from max(0, p - q), which reads the two rows once more
-//   k_route         route_rows, a warp per row
-//   k_route_grad    route_grad, a warp per row
+//   k_states           every row in steps of 4 KB, a state (m, s) for each step: one
+//                      read of the logits, and of the draft rows, in parts of any
+//                      number of warps
+//   k_sample           sample_rows: a CTA per row merges its states, draws a step by
+//                      their masses and re-reads that step
+//   k_sample_row       both for few short rows, a CTA a row
+//   k_decide           verify_drafts: a cluster per request merges its rows' states,
+//                      finds the first that accepts no draft, and draws its token:
+//                      from p, or from max(0, p - q), which reads the two rows once
+//                      more
+//   k_route            route_rows: 8 to 32 lanes per row, its columns in shared memory
+//   k_zero             its counts
+//   k_route_grad       route_grad where only the chosen experts get any
+//   k_route_grad_full  where all do
+//
+// A row is not one CTA's, or one cluster's: rows end together then, and hold their
+// share of an SM through the latencies of a merge and a draw (a cluster of warps
+// per row, one kernel: sampling 256 x 151936 21.6 us, verification of 64 x 4
+// drafts 62 us, of 256 x 7 195). Its states go to memory instead (0.2% of the
+// logits), and a kernel that starts as the streaming one ends takes them up.
 #include <algorithm>
 #include <cstdint>
 
@@ -49,8 +59,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 __device__ __forceinline__ void count_bad() { atomicAdd(&g_choice_status[0], 1ull); }
 
 // ---------------------------------------------------------------------------
-// Drawing a column. A row is split into segments in column order (a warp's part,
-// a lane's run, a column); a segment's mass is the sum of its weights as a fixed
+// Drawing a column. A row is split into segments in column order (a step, 32
+// vectors, a vector, a column); a segment's mass is the sum of its weights as a fixed
 // point number, rounded down to 2^-36 of the largest weight (2^-60 of the whole
 // for weights that add up to at most 1). Fixed point sums are exact: the
 // segments' running sums meet without a gap, and a number below the total lies
@@ -644,8 +654,8 @@ __device__ __forceinline__ int judge(const ChoiceArgs &a, int64_t row, const Row
         o.u = r.u;
         const bool from = drafted && (lookup || is_distribution(q));  // else not accepted, the token drawn from p
         odd |= drafted && !from;
-        const float qd = lookup ? 1.0f : ex2_ftz((r.yd - q.m) * heat.k) / q.s;
-        if (from && r.accept * qd < ex2_ftz((r.xd - p.m) * heat.k) / p.s) {
+        const float pd = ex2_ftz((r.xd - p.m) * heat.k) / p.s, qd = lookup ? 1.0f : ex2_ftz((r.yd - q.m) * heat.k) / q.s;
+        if (from && pd > 0.0f && r.accept * qd < pd) {
             v = kAccepted;
         } else {
             v = from && !lookup ? kFromRest : kFromOwn;

@@ -134,7 +134,7 @@ def check_verified(logits, drafts, offsets, uniforms, draft_logits, temperatures
                         q, q_each, q_border = softmax64(draft_logits[r], T)
                 side = float(uniforms[r][0]) * float(q[d]) - float(p[d])
                 slack = abs(float(uniforms[r][0])) * float(q_each[d]) + float(each[d]) + 4 * U * float(p[d])
-                if not drawn:
+                if not drawn or float(p[d]) == 0:
                     assert not took, what
                 elif abs(side) > slack:
                     assert took == (side < 0), (what, side)

@@ -280,6 +280,73 @@ def test_verify_one_column_left():
 
 
 @pytest.mark.parametrize("lookup", [False, True])
+def test_verify_drafts_that_cannot_be(lookup):
+    """A draft that the target bans is not accepted, whatever the number; one that the draft row bans is."""
+    x, drafts, _, u, y, t = drafted([6], 900, torch.float32, 4, lookup)
+    drafts = torch.full((6,), 33)
+    x[:, 33] = -math.inf
+    for a in (0.0, -1.0, -math.inf, 0.5, math.nan, math.inf):
+        u[:, 0] = a
+        accepted, tokens, _ = verified(x, drafts, torch.arange(7), u, y, 1.0)
+        assert accepted.tolist() == [0] * 6 and bool((tokens != 33).all()) and bool((tokens >= 0).all())
+    if not lookup:
+        x[:, 33] = 0.0
+        y[:, 33] = -math.inf
+        u[:, 0] = 0.999
+        accepted, tokens, _ = verified(x, drafts, torch.arange(7), u, y, 1.0)
+        assert accepted.tolist() == [1] * 6 and tokens.tolist() == [33] * 6
+
+
+def test_longest_rows():
+    """2^24 columns: more steps than a warp holds at hand."""
+    V = 1 << 24
+    x = torch.randn(3, V, device=DEV)
+    x[1, :V - 5] = -math.inf
+    u = torch.tensor([0.3, 0.6, 0.999])
+    tokens, logp = sampled(x, u, 0.9)
+    check_all(x, u, 0.9, tokens, logp)
+    assert int(ce.sample_rows(x, u.to(DEV), temperature=0.0)[2]) == int(x[2].argmax())
+    y = (x + 0.3 * torch.randn(3, V, device=DEV)).nan_to_num(neginf=-50.0)
+    drafts = torch.tensor([int(y[0].argmax()), 5, -1])
+    check_batch((x, drafts, torch.tensor([0, 1, 2, 3]), torch.tensor([[0.99, 0.2], [0.5, 0.5], [0.0, 0.7]]), y, torch.ones(3)), T=1.0)
+
+
+def test_past_2_31_elements():
+    """Rows that cross the 2^31st element and lie behind it."""
+    rows, V = 17000, 131073
+    x = torch.empty(rows, V + 7, dtype=torch.bfloat16, device=DEV)
+    for a in range(0, rows, 2000):
+        x[a:a + 2000].normal_(generator=torch.Generator(DEV).manual_seed(a))
+    x = x[:, :V]
+    g = gen(1)
+    u = torch.rand(rows, generator=g)
+    tokens, logp = sampled(x, u, 0.5)
+    assert int(tokens.min()) >= 0 and int(tokens.max()) < V
+    some = [0, 16382, 16383, 16384, 16999]
+    for r in some:
+        R.check_sampled(x[r].cpu(), float(u[r]), 0.5, int(tokens[r]), float(logp[r]), r)
+    drafts = torch.full((rows,), -1)
+    drafts[some] = torch.tensor([int(x[r].argmax()) for r in some])
+    pairs = torch.stack([u, u.flip(0)], 1)
+    pairs[:, 0] *= 1e-5
+    accepted, got, _ = verified(x, drafts, torch.arange(rows + 1), pairs, x, 0.5, logp=False)
+    assert accepted.nonzero()[:, 0].tolist() == some and got[some].tolist() == drafts[some].tolist()
+    del x
+    z = torch.empty(2100000, 1024, dtype=torch.bfloat16, device=DEV).normal_(generator=torch.Generator(DEV).manual_seed(5))
+    chosen, gates, counts = ce.route_rows(z, 4, counts=True)
+    assert int(counts.sum()) == 4 * z.shape[0]
+    tail = ce.route_rows(z[-64:], 4)
+    assert torch.equal(chosen[-64:], tail[0]) and torch.equal(gates[-64:], tail[1])
+    G = torch.ones_like(gates)
+    G[:, 0] = 2.0
+    for renorm in (True, False):
+        end = ce.route_grad(z[-64:], tail[0], G[-64:], renormalise=renorm)
+        got = ce.route_grad(z, chosen, G, renormalise=renorm)
+        assert torch.equal(got[-64:], end)
+        del got
+
+
+@pytest.mark.parametrize("lookup", [False, True])
 def test_verify_whole_distribution(lookup):
     """Over a grid of number pairs and every draft, what is emitted is distributed as the target."""
     V, n = 5, 96
