@@ -584,6 +584,77 @@ def test_route_grad_bad_experts():
     assert bool(((got.cpu().double() - want).abs() <= err + 2.0 ** -24 * want.abs()).all())
 
 
+# -- drawn cases ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("seed", range(20))
+def test_drawn_choices(seed):
+    """Drawn sizes, types, strides, phases, masks, temperatures and requests."""
+    import random
+    rng = random.Random(seed)
+    g = gen(seed)
+    dtype = rng.choice(list(TYPES.values()))
+    vocab = int(round(math.exp(rng.uniform(0, math.log(40000)))))
+    pad, lead = rng.choice([0, 0, 1, 5, 64]), rng.randint(0, 9)
+    lengths = [rng.choice([0, 1, 1, 2, 3, 5, 9]) for _ in range(rng.randint(1, 12))]
+    rows = sum(lengths)
+    per = torch.tensor([rng.choice([0.0, 0.5, 1.0, 1.0, 1.7, 30.0]) for _ in lengths])
+    T = per.repeat_interleave(torch.tensor(lengths))
+    mask = rng.choice([0.0, 0.0, 0.3, 0.97])
+    lookup = rng.random() < 0.3
+    x, drafts, ends, u, y, t = drafted(lengths, vocab, dtype, seed, lookup, noise=rng.choice([0.2, 1.0, 3.0]), stride=vocab + pad,
+                                       lead=lead, q_lead=rng.choice([lead, 0, 3]), tail=0, T=T, mask=mask)
+    check_batch((x, drafts, ends, u, y, T))
+    if rows:
+        draws = torch.rand(rows, generator=g)
+        tokens, logp = sampled(x, draws, T)
+        check_all(x, draws, T, tokens, logp)
+
+
+@pytest.mark.parametrize("seed", range(20))
+def test_drawn_routing(seed):
+    import random
+    rng = random.Random(1000 + seed)
+    g = gen(seed)
+    dtype = rng.choice(list(TYPES.values()))
+    G = rng.choice([1, 1, 2, 4, 5, 8, 16, 32])
+    E = G * rng.randint(1, max(1, min(60, 1024 // G)))
+    tg = rng.randint(1, G)
+    k = rng.randint(1, min(32, tg * (E // G)))
+    rows = rng.choice([1, 3, 17, 64])
+    pad = rng.choice([0, 0, 1, 8])
+    kw = dict(score=rng.choice(["softmax", "sigmoid"]), renormalise=rng.random() < 0.5, scale=rng.choice([1.0, 2.5, -0.5]))
+    x = rows_of(rows, E, dtype, g, stride=E + pad, lead=rng.randint(0, 9), sigma=rng.choice([0.3, 1.5, 6.0]), mask=rng.choice([0.0, 0.2, 0.9]))
+    if rng.random() < 0.4:  # few different values
+        x.copy_(x.float().nan_to_num(neginf=-9.0).round().clamp(-2, 2))
+    b = rng.choice([0.0, 0.1, 5.0]) * torch.randn(E, generator=g) if rng.random() < 0.5 else None
+    w = (torch.rand(rows, generator=g) > 0.2).float() if rng.random() < 0.5 else None
+    dw = None if w is None else w.to(DEV)
+    chosen, gates, counts = ce.route_rows(x, k, bias=None if b is None else b.to(DEV), groups=G, top_groups=tg,
+                                          group_top=rng.choice([1, 2]) if tg == G else (top := rng.choice([1, 2])), weights=dw, counts=True, **kw)
+    R.check_routed(x.cpu(), k, chosen.cpu(), gates.cpu(), counts.cpu(), bias=b, groups=G, top_groups=tg,
+                   group_top=2 if tg == G else top, weights=w, **kw)
+    grads = torch.randn(rows, k, generator=g)
+    got = ce.route_grad(x, chosen, grads.to(DEV), weights=dw, **kw)
+    want, err = R.route_grad64(x.cpu(), chosen.cpu(), grads, weights=w, **kw)
+    bound = err + HALF_STEP[dtype] * (want.abs() + err) + LEAST[dtype]
+    assert bool(((got.cpu().double() - want).abs() <= bound).all())
+
+
+def test_route_many_rows():
+    """Row counts around those that change the shape, against calls of a few rows."""
+    g = gen(2)
+    for E, kw in ((256, dict(score="sigmoid", groups=8, top_groups=4)), (60, dict(renormalise=False)), (128, dict())):
+        x = rows_of(3001, E, torch.bfloat16, g, sigma=1.5)
+        b = (0.1 * torch.randn(E, generator=g)).to(DEV)
+        chosen, gates, counts = ce.route_rows(x, 8, bias=b, counts=True, **kw)
+        total = torch.zeros_like(counts)
+        for a in range(0, 3001, 100):
+            c, t, n = ce.route_rows(x[a:a + 100], 8, bias=b, counts=True, **kw)
+            assert torch.equal(c, chosen[a:a + 100]) and torch.equal(t, gates[a:a + 100])
+            total += n
+        assert torch.equal(total, counts)
+
+
 # -- together, and how they are called ---------------------------------------------------
 
 def step(x, y, ends, u, draws, router, w, G):
