@@ -111,6 +111,8 @@ __device__ __forceinline__ int warp_segment(Mass m, float w, Mass &t) {
     return top > 0.0f ? __ffs(__ballot_sync(kFullMask, w == top)) - 1 : -1;
 }
 
+__device__ __forceinline__ void prefetch_l1(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+
 // A row as 16-byte vectors on its own grid: vector q holds columns N q - off ..
 // N q - off + N - 1. Vectors [qa, qb) lie in the row; the columns of a partial
 // one at either end are loaded one by one, a lane each.
@@ -187,8 +189,11 @@ struct Beside {
     __device__ Beside(const RowGrid<T> &g, const RowGrid<T> &d_) : d(d_) {
         r = (d.off - g.off + N) % N;
         by = d.off < g.off ? -1 : 0;
+        lo = max(g.qa, d.qa - by);
+        hi = max(lo, min(g.qb, d.qb - by - (r ? 1 : 0)));
     }
-    __device__ bool whole(int q, int end) const { return d.whole(q + by, end + by + (r ? 1 : 0)); }
+    // the vectors [lo, hi) are whole, the row's and what lies beside them
+    int lo, hi;
     __device__ uint4 load(int q) const {
         const uint4 v = d.load(q + by);
         return r == 0 ? v : shift_pair<T>(v, d.load(q + by + 1), r);
@@ -254,7 +259,7 @@ __device__ __forceinline__ Found column_of(const RowGrid<T> &g, const RowGrid<T>
     else if (q < g.nq)
         x = columns_from(g.p, g.n, g.column(q));
     if (kResidual) {
-        if (beside.whole(q, q + 1))
+        if (q >= beside.lo && q < beside.hi)
             y = beside.load(q);
         else if (q < g.nq)
             y = columns_from(d.p, d.n, g.column(q));
@@ -317,6 +322,7 @@ __device__ __forceinline__ void scan_step(TokState &st, const RowGrid<T> &g, int
     constexpr int N = Vec<T>::kN;
     uint4 v[kScan];
     const bool whole = g.whole(q, q + kStep);
+    int head = -1, tail = -1;  // of the row's partial vectors, a column a lane
     if (whole) {
 #pragma unroll
         for (int u = 0; u < kScan; ++u) v[u] = g.load(q + 32 * u + lane);
@@ -326,6 +332,11 @@ __device__ __forceinline__ void scan_step(TokState &st, const RowGrid<T> &g, int
             const int i = q + 32 * u + lane;
             v[u] = g.whole(i) ? g.load(i) : Vec<T>::lowest();
         }
+        head = q == 0 && g.qa > 0 ? g.edge_column(0, lane) : -1;
+        tail = g.qb < g.nq && g.qb >= max(q, g.qa) && g.qb < q + kStep ? g.edge_column(g.qb, lane) : -1;
+        // on their way beside the vectors, no register held
+        if (head >= 0) prefetch_l1(g.p + head);
+        if (tail >= 0) prefetch_l1(g.p + tail);
     }
     const int skip_q = skip < 0 ? -1 : (skip + g.off) / N;
     if (skip_q >= q && skip_q < q + kStep) {
@@ -343,9 +354,7 @@ __device__ __forceinline__ void scan_step(TokState &st, const RowGrid<T> &g, int
             }
     }
     tok_push<T, false, kScan>(st, v, k);
-    if (!whole) {  // the row's partial vectors
-        const int head = q == 0 && g.qa > 0 ? g.edge_column(0, lane) : -1;
-        const int tail = g.qb < g.nq && g.qb >= max(q, g.qa) && g.qb < q + kStep ? g.edge_column(g.qb, lane) : -1;
+    if (!whole) {
         if (head >= 0 && head != skip) tok_push1<false>(st, g.at(head), k);
         if (tail >= 0 && tail != skip) tok_push1<false>(st, g.at(tail), k);
     }
@@ -680,33 +689,48 @@ __device__ __forceinline__ int judge(const ChoiceArgs &a, int64_t row, const Row
 // exponentials a column, at 16 per clock and SM: 30 million columns (235 rows of
 // 128256) take 13 us of them.
 template <typename T>
+__device__ __forceinline__ float residual_of_vectors(const RowGrid<T> &g, const Beside<T> &beside, int q, int from, int to,
+                                                     const Weigh &w) {
+    constexpr int kU = kScan / 2;
+    const int lane = threadIdx.x & 31;
+    uint4 x[kU], y[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        const int v = q + 32 * u + lane;
+        x[u] = v >= from && v < to ? g.load(v) : Vec<T>::lowest();
+        y[u] = v >= from && v < to ? beside.load(v) : Vec<T>::lowest();
+    }
+    float sum = 0.0f, e[Vec<T>::kN];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        weights_of<T, true>(e, x[u], y[u], 0, w);
+        sum += sum_of(e);
+    }
+    return sum;
+}
+// The half of a step that holds an end of the row, or of the whole vectors beside
+// it: what is left of either end a column a lane, at most three vectors, or all of
+// a row that is hardly longer.
+template <typename T>
+__device__ __noinline__ float residual_at_end(const T *p, const T *draft, int n, int q, const Weigh &w) {
+    const RowGrid<T> g(p, n), d(draft, n);
+    const Beside<T> beside(g, d);
+    const int lane = threadIdx.x & 31, end = min(g.nq, q + 32 * (kScan / 2));
+    float sum = 0.0f;
+    auto columns = [&](int from, int to) {
+        for (int j = max(0, g.column(from)) + lane; j < min(n, g.column(to)); j += 32)
+            sum += fmaxf(0.0f, ex2_ftz(__fmaf_rn(g.at(j) - w.m, w.k, w.c)) - ex2_ftz(__fmaf_rn(d.at(j) - w.mq, w.k, w.cq)));
+    };
+    if (q < beside.lo) columns(q, min(end, beside.lo));
+    if (end > beside.hi) columns(max(q, beside.hi), end);
+    return sum + residual_of_vectors(g, beside, q, beside.lo, min(end, beside.hi), w);
+}
+template <typename T>
 __device__ __forceinline__ float residual_of_half(const RowGrid<T> &g, const RowGrid<T> &d, const Beside<T> &beside, int half,
                                                   const Weigh &w) {
-    constexpr int kU = kScan / 2;
-    const int lane = threadIdx.x & 31, q = half * 32 * kU, end = min(g.nq, q + 32 * kU);
-    float sum = 0.0f;
-    float e[Vec<T>::kN];
-    if (g.whole(q, end) && beside.whole(q, end)) {
-        uint4 x[kU], y[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int v = q + 32 * u + lane;
-            x[u] = v < end ? g.load(v) : Vec<T>::lowest();
-            y[u] = v < end ? beside.load(v) : Vec<T>::lowest();
-        }
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            weights_of<T, true>(e, x[u], y[u], 0, w);
-            sum += sum_of(e);
-        }
-    } else {
-        for (int v = q + lane; v < end; v += 32) {
-            const int j = g.column(v);
-            weights_of<T, true>(e, columns_from(g.p, g.n, j), columns_from(d.p, d.n, j), 0, w);
-            sum += sum_of(e);
-        }
-    }
-    return warp_sum(sum);
+    const int q = half * 32 * (kScan / 2), end = min(g.nq, q + 32 * (kScan / 2));
+    return warp_sum(q >= beside.lo && end <= beside.hi ? residual_of_vectors(g, beside, q, q, end, w)
+                                                       : residual_at_end(g.p, d.p, g.n, q, w));
 }
 
 // k_decide: a cluster per request, behind k_states. Every CTA's warps judge a row
@@ -1374,9 +1398,12 @@ cudaError_t verify_as(ChoiceArgs a, const DeviceInfo &dev, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
     const bool drawn = a.draft_logits != nullptr;
     if (a.rows > 0 && (e = launch_steps(Kernels<T>::states(), a, drawn ? 2 * a.rows : a.rows, false, dev, s))) return e;
-    // CTAs per request: as many as an SM holds, four, with a step for each of their warps
+    // CTAs per request: three an SM or more (it holds four), with a step for each of
+    // their warps. Measured (us, whole calls, 1 / 2 / 4 / 8): 64 requests of up to 4
+    // drafts of 151936 bf16 53.2 / 42.0 / 39.0 / 39.0; 256 of up to 7 of 128256 125 /
+    // 116 / 119 / 126.
     int c = 1;
-    while (drawn && c < 8 && 2 * c * a.requests <= 4 * dev.sms && 2 * c * (kDrawThreads / 32) <= a.steps) c *= 2;
+    while (drawn && c < 8 && c * a.requests < 3 * dev.sms && 2 * c * (kDrawThreads / 32) <= a.steps) c *= 2;
     void *args[] = {&a};
     LaunchConfig l(std::max<int64_t>(1, a.requests) * c, kDrawThreads, c, a.rows > 0, s);
     return cudaLaunchKernelExC(&l.cfg, Kernels<T>::decide(), args);
