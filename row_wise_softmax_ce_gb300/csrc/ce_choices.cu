@@ -10,9 +10,9 @@
 //   k_states           every row in steps of 4 KB, a state (m, s) for each step: one
 //                      read of the logits, and of the draft rows, in parts of any
 //                      number of warps
-//   k_sample           sample_rows: a CTA per row merges its states, draws a step by
+//   k_sample           sample_rows: a warp per row merges its states, draws a step by
 //                      their masses and re-reads that step
-//   k_sample_row       both for few short rows, a CTA a row
+//   k_sample_row       states and draw of short rows, a CTA a row
 //   k_decide           verify_drafts: a cluster per request merges its rows' states,
 //                      finds the first that accepts no draft, and draws its token:
 //                      from p, or from max(0, p - q), which reads the two rows once
@@ -519,74 +519,95 @@ __device__ __forceinline__ float logp_of(float x, const TokState &st, const Heat
     return heat.greedy ? 0.0f : (x - st.m) * heat.inv_t - logf(st.s);
 }
 
-// A row's token by a CTA, its first kScan warps at least: the first merges the
-// row's states and finds the step.
-struct RowDraw {
-    float sums[kScan];
-    TokState state;
-    int step;
-    Mass t;
-};
+// A row's token, by a warp. A lane weighs eight vectors that lie side by side, so
+// one running sum over the lanes, then the lane's vectors and the vector's columns.
 template <typename T, bool kShared>
-__device__ __forceinline__ void draw_row(const ChoiceArgs &a, int64_t row, const RowGrid<T> &g, const Heat &heat, float u,
-                                         const float2 *states, RowDraw &x) {
-    Weigh w{0.0f, heat.k, -1, 0.0f, 0.0f, 0.0f};
-    if (threadIdx.x < 32) {
-        const StepsOf<kShared> steps(states, a.steps);
-        const TokState st = steps.merged(heat.k);
-        int step = -1, column = -1;
-        Mass t = 0;
-        if (heat.ok && is_distribution(st)) {
-            w.m = st.m;
-            if (heat.greedy)
-                column = first_largest(g, steps, st.m);
-            else
-                step = own_step(steps, w, u, t);
-        }
-        if (threadIdx.x == 0) {
-            x.state = st;
-            x.step = step;
-            x.t = t;
-            if (step < 0) {
-                a.tokens[row] = column;
-                if (a.logp) a.logp[row] = column < 0 ? nan_f() : 0.0f;
-                if (column < 0) count_bad();
+__device__ __forceinline__ void draw_token(const ChoiceArgs &a, int64_t row, const RowGrid<T> &g, const Heat &heat, float u,
+                                           const float2 *states) {
+    constexpr int N = Vec<T>::kN;
+    const int lane = threadIdx.x & 31;
+    const StepsOf<kShared> steps(states, a.steps);
+    const TokState st = steps.merged(heat.k);
+    int column = -1;
+    float logp = nan_f();
+    if (heat.ok && is_distribution(st)) {
+        if (heat.greedy) {
+            column = first_largest(g, steps, st.m);
+            logp = 0.0f;
+        } else {
+            const Weigh w{st.m, heat.k, -1, 0.0f, 0.0f, 0.0f};
+            Mass t;
+            const int q = own_step(steps, w, u, t) * kStep + kScan * lane;
+            uint4 x[kScan];
+#pragma unroll
+            for (int i = 0; i < kScan; ++i) x[i] = g.whole(q + i) ? g.load_cached(q + i) : Vec<T>::lowest();
+            if (q < g.qa || q + kScan > g.qb) {
+#pragma unroll
+                for (int i = 0; i < kScan; ++i)
+                    if (q + i < g.nq && !g.whole(q + i)) x[i] = columns_from(g.p, g.n, g.column(q + i));
+            }
+            float sum[kScan], all = 0.0f, e[N];
+            Mass m = 0;
+#pragma unroll
+            for (int i = 0; i < kScan; ++i) {
+                weights_of<T, false>(e, x[i], x[i], 0, w);
+                sum[i] = sum_of(e);
+                all += sum[i];
+                m += mass_of(sum[i], kUnitWeights);
+            }
+            const int l = warp_segment(m, all, t);
+            if (l >= 0) {
+                const int at = walk(sum, kUnitWeights, t);
+                uint4 v = x[0];
+#pragma unroll
+                for (int i = 1; i < kScan; ++i)
+                    if (i == at) v = x[i];
+                weights_of<T, false>(e, v, v, 0, w);
+                const int j = walk(e, kUnitWeights, t);
+                float xj = 0.0f;
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    const float2 xx = Vec<T>::pair(v, i);
+                    if (2 * i == j) xj = xx.x;
+                    if (2 * i + 1 == j) xj = xx.y;
+                }
+                column = __shfl_sync(kFullMask, g.column(q + at) + j, l);
+                logp = logp_of(__shfl_sync(kFullMask, xj, l), st, heat);
             }
         }
     }
-    __syncthreads();
-    if (x.step < 0) return;
-    const TokState st = x.state;
-    w.m = st.m;
-    const Found f = column_of<T, false>(g, g, x.step, w, x.t, x.sums);
-    if (!f.mine || (threadIdx.x & 31) != 0) return;
-    a.tokens[row] = f.column;
-    if (a.logp) a.logp[row] = f.column < 0 ? nan_f() : logp_of(f.x, st, heat);
+    if (lane == 0) {
+        a.tokens[row] = column;
+        if (a.logp) a.logp[row] = logp;
+        if (column < 0) count_bad();
+    }
 }
 
-// k_sample: a CTA of kScan warps per row, behind k_states, kCtas of them on an SM:
-// five in the registers that it wants, eight, with spills, where more rows than
-// that would wait for others to end. Measured (us, whole calls, 5 / 8): 256 x
-// 151936 bf16 19.2 / 20.5, 1024 x 50257 f32 40.2 / 38.3.
-template <typename T, int kCtas>
-__global__ void __launch_bounds__(kDrawThreads, kCtas) k_sample(ChoiceArgs a) {
-    __shared__ RowDraw x;
-    const int64_t row = blockIdx.x;
+// k_sample: a warp per row, behind k_states. Bound by a row's latencies, over the
+// warps resident: a CTA of eight warps per row, as k_decide draws, takes 20.1 us
+// for 19.3 (whole calls, 256 x 151936 bf16), 42.3 for 37.1 (1024 x 50257 f32), 18.9
+// for 9.1 (2048 x 1076 bf16).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_sample(ChoiceArgs a) {
+    const int64_t row = blockIdx.x * int64_t(kWarps) + (threadIdx.x >> 5);
+    if (row >= a.rows) return;
     const RowGrid<T> g = target_row<T>(a, row);
     const Heat heat(temperature_of(a, row));
     const float u = a.uniforms[row];
     wait_prerequisites();
-    draw_row<T, false>(a, row, g, heat, u, states_of(a, row), x);
+    draw_token<T, false>(a, row, g, heat, u, states_of(a, row));
 }
 
 // k_sample_row: a row of at most 32 steps by one CTA, a warp a step: the states
-// stay in shared memory. One launch in place of two, for calls of few rows, which
-// the host's launches bound: 1 x 32000 bf16 8.2 -> 6.1 us a call, 5.0 -> 5.3 us on
-// the GPU alone (152 rows 8.0 -> 6.9; 152 rows of 8000 6.1 -> 5.0).
+// stay in shared memory, and one launch does. Taken while the SMs hold the warps,
+// 32 each, and short rows somewhat longer (us, on the GPU, k_states and k_sample /
+// this, 152 / 600 / 2048 rows: of 1000 f32, one step, 5.3 / 4.1, 5.6 / 4.8, 8.7 /
+// 6.9; of 8000 bf16, four, 5.9 / 4.8, 7.8 / 6.3, 14.0 / 12.8; of 16000, eight, 6.3 /
+// 5.3, 10.1 / 7.7, 18.8 / 21.4; of 32000, sixteen, 7.7 / 6.5, 13.4 / 13.9, 29.8 /
+// 39.6).
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) k_sample_row(ChoiceArgs a) {
     __shared__ float2 states[kRowSteps];
-    __shared__ RowDraw x;
     const int64_t row = blockIdx.x;
     const RowGrid<T> g = target_row<T>(a, row);
     const float u = a.uniforms[row];
@@ -599,12 +620,7 @@ __global__ void __launch_bounds__(kRowThreads) k_sample_row(ChoiceArgs a) {
         if (lane == 0) states[warp] = make_float2(st.m, st.s);
     }
     __syncthreads();
-    if (warp >= kScan) {  // draw_row's barriers, two where a step is drawn
-        __syncthreads();
-        if (x.step >= 0) __syncthreads();
-        return;
-    }
-    draw_row<T, true>(a, row, g, heat, u, states, x);
+    if (warp == 0) draw_token<T, true>(a, row, g, heat, u, states);
 }
 
 // What becomes of a row: its draft is accepted; or it ends its request, with a
@@ -1363,10 +1379,11 @@ template <typename T>
 struct Kernels {
     static const void *states() { return reinterpret_cast<const void *>(&k_states<T>); }
     static const void *sample_row() { return reinterpret_cast<const void *>(&k_sample_row<T>); }
-    static const void *sample(bool many) {
-        return many ? reinterpret_cast<const void *>(&k_sample<T, 8>) : reinterpret_cast<const void *>(&k_sample<T, 5>);
+    static const void *sample() { return reinterpret_cast<const void *>(&k_sample<T>); }
+    static Kernel &decide() {
+        static Kernel k(reinterpret_cast<const void *>(&k_decide<T>), false);
+        return k;
     }
-    static const void *decide() { return reinterpret_cast<const void *>(&k_decide<T>); }
 };
 
 cudaError_t launch(const void *fn, int64_t ctas, bool dependent, cudaStream_t s, void **args, int threads = kThreads) {
@@ -1387,10 +1404,10 @@ cudaError_t launch_steps(const void *fn, ChoiceArgs &a, int64_t rows, bool depen
 template <typename T>
 cudaError_t sample_as(ChoiceArgs a, const DeviceInfo &dev, cudaStream_t s) {
     void *args[] = {&a};
-    if (a.rows <= dev.sms && a.steps <= kRowSteps)
-        return launch(Kernels<T>::sample_row(), a.rows, false, s, args, kRowThreads);
+    if (a.steps <= kRowSteps && a.rows * a.steps <= (a.steps <= 8 ? 56 : 32) * static_cast<int64_t>(dev.sms))
+        return launch(Kernels<T>::sample_row(), a.rows, false, s, args, 32 * a.steps);
     if (cudaError_t e = launch_steps(Kernels<T>::states(), a, a.rows, false, dev, s); e != cudaSuccess) return e;
-    return launch(Kernels<T>::sample(a.rows > 5 * dev.sms), a.rows, true, s, args, kDrawThreads);
+    return launch(Kernels<T>::sample(), ctas_of(a.rows), true, s, args);
 }
 
 template <typename T>
@@ -1398,15 +1415,17 @@ cudaError_t verify_as(ChoiceArgs a, const DeviceInfo &dev, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
     const bool drawn = a.draft_logits != nullptr;
     if (a.rows > 0 && (e = launch_steps(Kernels<T>::states(), a, drawn ? 2 * a.rows : a.rows, false, dev, s))) return e;
-    // CTAs per request: three an SM or more (it holds four), with a step for each of
-    // their warps. Measured (us, whole calls, 1 / 2 / 4 / 8): 64 requests of up to 4
+    // CTAs per request: three an SM or more (it holds four), with half a step for each
+    // of their warps. Measured (us, whole calls, 1 / 2 / 4 / 8): 64 requests of up to 4
     // drafts of 151936 bf16 53.2 / 42.0 / 39.0 / 39.0; 256 of up to 7 of 128256 125 /
     // 116 / 119 / 126.
     int c = 1;
-    while (drawn && c < 8 && c * a.requests < 3 * dev.sms && 2 * c * (kDrawThreads / 32) <= a.steps) c *= 2;
+    while (drawn && c < kMaxCluster && c * a.requests < 3 * dev.sms && c * (kDrawThreads / 32) <= a.steps) c *= 2;
+    Kernel &k = Kernels<T>::decide();
+    if ((e = ready(k, dev))) return e;
     void *args[] = {&a};
     LaunchConfig l(std::max<int64_t>(1, a.requests) * c, kDrawThreads, c, a.rows > 0, s);
-    return cudaLaunchKernelExC(&l.cfg, Kernels<T>::decide(), args);
+    return cudaLaunchKernelExC(&l.cfg, k.fn, args);
 }
 
 template <typename T, int L>
