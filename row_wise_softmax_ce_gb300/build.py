@@ -28,7 +28,7 @@ LIB = os.path.join(PKG, "libcerows.so")
 BINDING = os.path.join(PKG, "_binding.so")
 BINDING_FOR = os.path.join(BUILD, "binding_for.txt")  # what the binding was built against
 
-SOURCES = ["ce_kernels.cu", "ce_objectives.cu", "ce_choices.cu", "ce_api.cu"]
+SOURCES = ["ce_kernels.cu", "ce_objectives.cu", "ce_choices.cu", "ce_router.cu", "ce_api.cu"]
 HEADERS = ["ce_device.cuh", "ce_objectives.cuh", "ce_internal.h", "ce_launch.h"]
 BINDING_SOURCE = "binding.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1180,11 +1180,13 @@ static int read_counter(ce_stream_t stream, int which, int64_t *out) {
     DeviceInfo dev;
     int st = current_device(&dev);
     if (st) return st;
-    unsigned long long v[2] = {0ull, 0ull}, o[2] = {0ull, 0ull}, c[2] = {0ull, 0ull};
+    unsigned long long v[2] = {0ull, 0ull}, o[2] = {0ull, 0ull}, c = 0ull, r = 0ull;
     if ((st = cuda_status(read_status(v, stream)))) return st;
     if ((st = cuda_status(read_objective_status(o, dev, stream)))) return st;
-    if ((st = cuda_status(read_choice_status(c, dev, stream)))) return st;
-    *out = static_cast<int64_t>(v[which] + o[which] + c[which]);
+    // the choices wait for nothing that could give up
+    if (which == 0 && (st = cuda_status(read_choice_status(&c, dev, stream)))) return st;
+    if (which == 0 && (st = cuda_status(read_router_status(&r, dev, stream)))) return st;
+    *out = static_cast<int64_t>(v[which] + o[which] + c + r);
     return CE_OK;
 }
 
@@ -1198,7 +1200,8 @@ int ce_device_error_reset(ce_stream_t stream) {
     if (st) return st;
     if ((st = cuda_status(reset_status(stream)))) return st;
     if ((st = cuda_status(reset_objective_status(dev, stream)))) return st;
-    return cuda_status(reset_choice_status(dev, stream));
+    if ((st = cuda_status(reset_choice_status(dev, stream)))) return st;
+    return cuda_status(reset_router_status(dev, stream));
 }
 
 int ce_debug_force(int path, int cluster, int threads) {

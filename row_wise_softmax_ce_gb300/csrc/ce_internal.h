@@ -149,7 +149,7 @@ cudaError_t launch_weighted_sum(const float *loss, const float *weights, int64_t
 cudaError_t read_objective_status(unsigned long long out[2], const DeviceInfo &dev, cudaStream_t s);
 cudaError_t reset_objective_status(const DeviceInfo &dev, cudaStream_t s);
 
-// -- the choices made from a row's softmax (ce_choices.cu) -----------------------
+// -- the choices made from a row's softmax (ce_choices.cu, ce_router.cu) -----------------------
 // Arguments of sample_rows and verify_drafts; unused pointers are null.
 struct ChoiceArgs {
     const void *logits;
@@ -203,9 +203,11 @@ cudaError_t launch_sample(DType t, const ChoiceArgs &a, void *work, const Device
 cudaError_t launch_verify(DType t, const ChoiceArgs &a, void *work, const DeviceInfo &dev, cudaStream_t s);
 cudaError_t launch_route(DType t, const RouteArgs &a, const DeviceInfo &dev, cudaStream_t s);
 cudaError_t launch_route_grad(DType t, const RouteArgs &a, const DeviceInfo &dev, cudaStream_t s);
-// nothing to read or reset on a device that has launched no choice
-cudaError_t read_choice_status(unsigned long long out[2], const DeviceInfo &dev, cudaStream_t s);
+// nothing to read or reset on a device that has launched none of them
+cudaError_t read_choice_status(unsigned long long *out, const DeviceInfo &dev, cudaStream_t s);
 cudaError_t reset_choice_status(const DeviceInfo &dev, cudaStream_t s);
+cudaError_t read_router_status(unsigned long long *out, const DeviceInfo &dev, cudaStream_t s);
+cudaError_t reset_router_status(const DeviceInfo &dev, cudaStream_t s);
 
 cudaError_t set_kernel_attributes(const DeviceInfo &dev);
 cudaError_t max_active_clusters(const Plan &p, Op op, int *n);

@@ -1,4 +1,4 @@
-// ce_launch.h -- what the launchers of ce_objectives.cu and ce_choices.cu share:
+// ce_launch.h -- what the launchers of ce_objectives.cu, ce_choices.cu and ce_router.cu share:
 // a launch's configuration, a kernel's attributes, and the devices on which a
 // file's kernels have been launched.
 #pragma once

@@ -723,6 +723,40 @@ def test_captured_and_replayed():
     assert all(torch.equal(p, q) for p, q in zip(outs[0], want[1]))
 
 
+def test_first_calls_captured():
+    """No call of the process before the capture: the graph's results are the eager calls'."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    program = """
+import sys
+sys.path[:0] = ['.', 'tests']
+import torch
+import test_gpu_choices as C
+import row_wise_softmax_ce_gb300 as ce
+inputs = C.step_inputs(4)
+wide = torch.randn(40, 1000, device='cuda')
+def everything():
+    return C.step(*inputs) + [ce.sample_rows(wide, torch.full((40,), 0.4, device='cuda'))] + list(
+        ce.route_rows(wide, 32, counts=True)) + [ce.route_grad(wide, torch.zeros(40, 8, dtype=torch.int64, device='cuda'),
+        torch.ones(40, 8, device='cuda'))] + [ce.route_grad(wide, torch.zeros(40, 1, dtype=torch.int64, device='cuda'),
+        torch.ones(40, 1, device='cuda'), renormalise=False)]
+ce.lib()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = everything()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, everything()))
+print("same", *ce.device_error_count())
+"""
+    r = subprocess.run([sys.executable, "-c", program], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert r.stdout.split() == ["same", "0", "0"]
+
+
 def test_streams_and_threads():
     """The same bits on every stream and from every thread, side by side."""
     sets = [step_inputs(s, vocab=20011) for s in range(4)]
