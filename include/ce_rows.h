@@ -587,7 +587,7 @@ enum ce_route_score { CE_ROUTE_SOFTMAX = 0, CE_ROUTE_SIGMOID = 1 };
 /* A router: the scores, experts per row k (1..32), the experts' groups (1..32,
  * a divisor of the experts), how many of them a row keeps (top_groups), by the
  * sum of how many of their best members (group_top: 1 or 2); whether the gates
- * are renormalised, and their scale (finite). */
+ * are renormalised, and their scale (finite in f32). */
 typedef struct ce_route {
     int score, k, groups, top_groups, group_top, renormalise;
     double scale;

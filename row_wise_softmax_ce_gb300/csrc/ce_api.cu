@@ -1026,7 +1026,8 @@ static int check_route(const void *logits, int dtype, int64_t rows, int64_t expe
     int st = check_choice_rows(logits, dtype, rows, experts, stride, kMaxExperts);
     if (st) return st;
     if (route->score != CE_ROUTE_SOFTMAX && route->score != CE_ROUTE_SIGMOID) return CE_EINVAL;
-    if (route->k < 1 || route->k > kMaxChosen || route->k > experts || !std::isfinite(route->scale)) return CE_EINVAL;
+    if (route->k < 1 || route->k > kMaxChosen || route->k > experts) return CE_EINVAL;
+    if (!std::isfinite(static_cast<float>(route->scale))) return CE_EINVAL;
     if (misaligned(weights, 4)) return CE_EALIGN;
     *a = RouteArgs{};
     a->logits = logits;

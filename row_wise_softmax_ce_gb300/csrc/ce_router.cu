@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(V)) k_route(RouteArg
         __syncthreads();
         wait_prerequisites();  // k_zero is done
         for (int j = threadIdx.x; j < E; j += kRouteThreads)
-            if (counts[j]) atomicAdd(&a.counts[j], static_cast<unsigned long long>(counts[j]));
+            if (counts[j]) atomicAdd(&a.counts[j], static_cast<unsigned long long>(static_cast<unsigned>(counts[j])));
     }
 }
 
@@ -495,6 +495,10 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_grad_full(RouteArgs a) 
         if (live) load_columns<T, V>(raw, p, j0, E);
         const Slot x = slot_at(a, row, sub);
         const float z = x.c >= 0 ? Vec<T>::to_float(p[x.c]) : -INFINITY;
+        if (row_ballot<L>(x.c >= 0) == 0) {  // no experts: zeros, whatever the row holds
+#pragma unroll
+            for (int i = 0; i < V / Vec<T>::kN; ++i) raw[i] = Vec<T>::lowest();
+        }
         float out[V];
         unpack_columns<T, V>(out, raw);
         float m = out[0], s = 0.0f;

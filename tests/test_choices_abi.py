@@ -113,7 +113,7 @@ def test_verify_alignment_refused(lib, bad):
 
 
 @pytest.mark.parametrize("bad", [dict(par=False), dict(score=2), dict(score=-1), dict(k=0), dict(k=13), dict(k=33, cols=64, stride=64),
-                                 dict(scale=math.nan), dict(scale=math.inf), dict(cols=1025, stride=1025)], ids=str)
+                                 dict(scale=math.nan), dict(scale=math.inf), dict(scale=-1e39), dict(cols=1025, stride=1025)], ids=str)
 @pytest.mark.parametrize("call", [route, grad])
 def test_router_refused(lib, call, bad):
     assert call(lib, **{"gs": 1025, **bad} if call is grad else bad) == ce.CE_EINVAL

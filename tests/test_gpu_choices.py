@@ -584,6 +584,25 @@ def test_route_grad_bad_experts():
     assert bool(((got.cpu().double() - want).abs() <= err + 2.0 ** -24 * want.abs()).all())
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E,k", [(40, 5), (256, 8), (600, 20)])
+def test_route_grad_no_experts(dtype, score, renorm, E, k):
+    """Zeros in a row that chose nothing, whatever it holds, beside rows that did."""
+    x = torch.randn(6, E, generator=gen(E)).to(TYPES[dtype]).to(DEV)
+    x[1, 5] = math.nan
+    x[2, 6] = math.inf
+    x[3] = -math.inf
+    x[4, :] = torch.finfo(TYPES[dtype]).max
+    kw = dict(score=score, renormalise=renorm)
+    chosen, _, _ = ce.route_rows(x, k, **kw)
+    chosen[4] = -1
+    assert (chosen[:, 0] >= 0).tolist() == [True, False, False, False, False, True]
+    got = ce.route_grad(x, chosen, torch.full((6, k), math.nan, device=DEV).where(chosen < 0, torch.ones((), device=DEV)), **kw)
+    assert bool((got[1:5] == 0).all()) and not bool(torch.isnan(got).any())
+
+
 # -- drawn cases ---------------------------------------------------------------------------
 
 @pytest.mark.parametrize("seed", range(20))
