@@ -620,6 +620,8 @@ enum Verdict : int { kAccepted = 0, kKnown = 1, kFromOwn = 2, kFromRest = 3, kOd
 struct Open {  // of a row whose token is still to be drawn
     Weigh w;
     float inv_t, s, u;
+    int step;  // kLookup: where u falls, and t from its start on
+    Mass t;
 };
 
 // A row's own inputs, asked for before the states are there.
@@ -629,25 +631,26 @@ struct RowNumbers {
     Heat heat;
     int d;  // the draft, -1: none
 };
-template <typename T>
+template <typename T, bool kLookup>
 __device__ __forceinline__ RowNumbers row_numbers(const ChoiceArgs &a, int64_t row) {
     RowNumbers r{a.drafts[row], a.uniforms[2 * row], a.uniforms[2 * row + 1], 0.0f, 0.0f, Heat(temperature_of(a, row)), -1};
     r.d = r.draft >= 0 && r.draft < a.vocab ? static_cast<int>(r.draft) : -1;
     if (r.d >= 0) {
         r.xd = target_row<T>(a, row).at(r.d);
-        if (a.draft_logits) r.yd = draft_row<T>(a, row).at(r.d);
+        if (!kLookup) r.yd = draft_row<T>(a, row).at(r.d);
     }
     return r;
 }
 
-template <typename T>
+// kLookup: a verification without draft rows.
+template <typename T, bool kLookup>
 __device__ __forceinline__ int judge(const ChoiceArgs &a, int64_t row, const RowNumbers &r, bool writes, Open *open) {
     const int lane = threadIdx.x & 31;
     const Heat heat = r.heat;
-    const bool drafted = r.d >= 0 && !heat.greedy, lookup = drafted && a.draft_logits == nullptr;
+    const bool drafted = r.d >= 0 && !heat.greedy, lookup = kLookup && drafted;
     const Steps steps(states_of(a, row), a.steps);
     TokState q{};
-    if (drafted && !lookup) q = Steps(draft_states_of(a, row), a.steps).merged(heat.k);
+    if (!kLookup && drafted) q = Steps(draft_states_of(a, row), a.steps).merged(heat.k);
     TokState p = steps.merged(heat.k);
     if (lookup) tok_push1<false>(p, r.xd, heat.k);  // its column is not among the states
     Verdict v = kKnown;
@@ -673,6 +676,16 @@ __device__ __forceinline__ int judge(const ChoiceArgs &a, int64_t row, const Row
             v = kAccepted;
         } else {
             v = from && !lookup ? kFromRest : kFromOwn;
+            // without draft rows all tokens come from p: the step while the states are at
+            // hand, in a row that turns out not to be the request's last as well, and its
+            // vectors on their way (32 requests of up to 6 drafts of 50257 f32: 10.9 us
+            // for 11.4)
+            if (kLookup) {
+                o.step = own_step(steps, o.w, r.u, o.t);
+                const RowGrid<T> g = target_row<T>(a, row);
+                const int q = o.step * kStep + kScan * lane;  // a line a lane
+                if (o.step >= 0 && q < g.nq) prefetch_l1(g.p - g.off + g.N * q);
+            }
         }
         if (v == kAccepted) {
             token = r.d;
@@ -743,7 +756,7 @@ __device__ __forceinline__ float residual_of_half(const RowGrid<T> &g, const Row
 // same; the first writes). That row's token is then drawn: from p by the first
 // CTA; where it comes from what q leaves of p, the cluster's warps add that up
 // over the row's steps first.
-template <typename T>
+template <typename T, bool kLookup>
 __global__ void __launch_bounds__(kDrawThreads, 4) k_decide(ChoiceArgs a) {
     constexpr int kRows = kDrawThreads / 32;
     __shared__ int verdicts[kRows];
@@ -761,7 +774,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4) k_decide(ChoiceArgs a) {
     // a row outside [lo, hi) has no states: of a table that decreases
     auto has_states = [&](int64_t row) { return good && row < r1 && row >= lo && row < hi; };
     RowNumbers numbers{0, 0.0f, 0.0f, 0.0f, 0.0f, Heat(1.0f), -1};
-    if (has_states(r0 + warp)) numbers = row_numbers<T>(a, r0 + warp);
+    if (has_states(r0 + warp)) numbers = row_numbers<T, kLookup>(a, r0 + warp);
     wait_prerequisites();
     if (s == 0 && writes)  // rows in no request
         for (int64_t r = threadIdx.x; r < a.rows; r += kDrawThreads)
@@ -774,8 +787,8 @@ __global__ void __launch_bounds__(kDrawThreads, 4) k_decide(ChoiceArgs a) {
         int v = kKnown;
         if (r > r0) __syncthreads();  // the verdicts before have been read
         if (has_states(row)) {
-            if (r > r0) numbers = row_numbers<T>(a, row);
-            v = judge<T>(a, row, numbers, writes, &opens[warp]);
+            if (r > r0) numbers = row_numbers<T, kLookup>(a, row);
+            v = judge<T, kLookup>(a, row, numbers, writes, &opens[warp]);
         } else if (row < r1 && writes && lane == 0) {
             silent(row);
         }
@@ -800,11 +813,11 @@ __global__ void __launch_bounds__(kDrawThreads, 4) k_decide(ChoiceArgs a) {
     verdict &= ~kOdd;
     if (verdict == kAccepted || verdict == kKnown) return;
     const Open o = opens[by];
-    const bool rest = verdict == kFromRest;
+    const bool rest = !kLookup && verdict == kFromRest;
     const RowGrid<T> g = target_row<T>(a, stop);
     Found f{};
-    int step;
-    Mass t;
+    int step = o.step;
+    Mass t = o.t;
     bool own = !rest;
     if (rest) {
         const RowGrid<T> d = draft_row<T>(a, stop);
@@ -837,7 +850,7 @@ __global__ void __launch_bounds__(kDrawThreads, 4) k_decide(ChoiceArgs a) {
         return;
     }
     if (own) {
-        step = own_step(Steps(states_of(a, stop), a.steps), o.w, o.u, t);
+        if (!kLookup) step = own_step(Steps(states_of(a, stop), a.steps), o.w, o.u, t);
         if (step >= 0)
             f = column_of<T, false>(g, g, step, o.w, t, sums);
         else  // nothing but the looked-up draft weighs anything: it is the row's largest
@@ -873,9 +886,10 @@ struct Kernels {
     static const void *states() { return reinterpret_cast<const void *>(&k_states<T>); }
     static const void *sample_row() { return reinterpret_cast<const void *>(&k_sample_row<T>); }
     static const void *sample() { return reinterpret_cast<const void *>(&k_sample<T>); }
-    static Kernel &decide() {
-        static Kernel k(reinterpret_cast<const void *>(&k_decide<T>), false);
-        return k;
+    static Kernel &decide(bool lookup) {
+        static Kernel drawn(reinterpret_cast<const void *>(&k_decide<T, false>), false);
+        static Kernel looked_up(reinterpret_cast<const void *>(&k_decide<T, true>), false);
+        return lookup ? looked_up : drawn;
     }
 };
 
@@ -914,7 +928,7 @@ cudaError_t verify_as(ChoiceArgs a, const DeviceInfo &dev, cudaStream_t s) {
     // 116 / 119 / 126.
     int c = 1;
     while (drawn && c < kMaxCluster && c * a.requests < 3 * dev.sms && c * (kDrawThreads / 32) <= a.steps) c *= 2;
-    Kernel &k = Kernels<T>::decide();
+    Kernel &k = Kernels<T>::decide(!drawn);
     if ((e = ready(k, dev))) return e;
     void *args[] = {&a};
     LaunchConfig l(std::max<int64_t>(1, a.requests) * c, kDrawThreads, c, a.rows > 0, s);
