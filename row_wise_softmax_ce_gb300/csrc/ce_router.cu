@@ -117,6 +117,17 @@ __device__ __forceinline__ float exp_of(float d) { return ex2_ftz(d * 1.44269504
 // 1 / (1 + e^-z) without a difference from 1, for any z
 __device__ __forceinline__ float sigmoid(float z) { return rcp_of(1.0f + exp_of(-z)); }
 
+// both, two columns at a time
+__device__ __forceinline__ float2 exp2_of(float2 d) {
+    const float2 t = __fmul2_rn(d, make_float2(1.44269504f, 1.44269504f));
+    return make_float2(ex2_ftz(t.x), ex2_ftz(t.y));
+}
+__device__ __forceinline__ float2 sigmoid2(float2 z) {
+    const float2 t = __fmul2_rn(z, make_float2(-1.44269504f, -1.44269504f));
+    const float2 s = __fadd2_rn(make_float2(ex2_ftz(t.x), ex2_ftz(t.y)), make_float2(1.0f, 1.0f));
+    return make_float2(rcp_of(s.x), rcp_of(s.y));
+}
+
 // A score over a factor that those of a row (or of its chosen) have in common,
 // `top` the largest of their logits: nothing overflows, and what is next to
 // nothing beside 1 is not so beside the others.
@@ -145,8 +156,9 @@ __global__ void __launch_bounds__(kRouteThreads) k_zero(unsigned long long *coun
 
 // CTAs of an SM, by the columns a lane holds.
 __host__ __device__ constexpr int route_ctas(int v) { return v > 16 ? 3 : 4; }
-// Words of a row in shared memory: its lanes' columns, 16 bytes apart by bank.
-__host__ __device__ constexpr int route_row(int lanes, int v) { return lanes * (v + 4); }
+// Words of a row in shared memory: its lanes' columns, 16 bytes apart by bank, the
+// rows of a warp 32.
+__host__ __device__ constexpr int route_row(int lanes, int v) { return lanes * (v + 4) + (lanes < 32 ? 8 : 0); }
 
 // k_route: bound by the instructions of the choice, most of them compares at half
 // rate. So up to four rows share a warp's instructions, and a lane keeps the
@@ -218,36 +230,54 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(V)) k_route(RouteArg
         // bias, the logit, which orders the experts as their scores do and is exact
         if (a.bias) {
             const float *b = bias + sub * kLane;
-            if (a.sigmoid) {
+            auto biased = [&](auto score) {  // two columns at a time
 #pragma unroll
                 for (int i = 0; i < V; i += 4) {
                     const float4 f = *reinterpret_cast<const float4 *>(b + i);
-                    z[i] = z[i] > -INFINITY ? sigmoid(z[i]) + f.x : -INFINITY;
-                    z[i + 1] = z[i + 1] > -INFINITY ? sigmoid(z[i + 1]) + f.y : -INFINITY;
-                    z[i + 2] = z[i + 2] > -INFINITY ? sigmoid(z[i + 2]) + f.z : -INFINITY;
-                    z[i + 3] = z[i + 3] > -INFINITY ? sigmoid(z[i + 3]) + f.w : -INFINITY;
+                    const float2 lo = __fadd2_rn(score(make_float2(z[i], z[i + 1])), make_float2(f.x, f.y));
+                    const float2 hi = __fadd2_rn(score(make_float2(z[i + 2], z[i + 3])), make_float2(f.z, f.w));
+                    z[i] = z[i] > -INFINITY ? lo.x : -INFINITY;
+                    z[i + 1] = z[i + 1] > -INFINITY ? lo.y : -INFINITY;
+                    z[i + 2] = z[i + 2] > -INFINITY ? hi.x : -INFINITY;
+                    z[i + 3] = z[i + 3] > -INFINITY ? hi.y : -INFINITY;
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; i += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(b + i);
-                    z[i] = z[i] > -INFINITY ? exp_of(z[i] - m) * rs + f.x : -INFINITY;
-                    z[i + 1] = z[i + 1] > -INFINITY ? exp_of(z[i + 1] - m) * rs + f.y : -INFINITY;
-                    z[i + 2] = z[i + 2] > -INFINITY ? exp_of(z[i + 2] - m) * rs + f.z : -INFINITY;
-                    z[i + 3] = z[i + 3] > -INFINITY ? exp_of(z[i + 3] - m) * rs + f.w : -INFINITY;
-                }
-            }
+            };
+            if (a.sigmoid)
+                biased([](float2 x) { return sigmoid2(x); });
+            else
+                biased([&](float2 x) {
+                    const float2 d = exp2_of(__fadd2_rn(x, make_float2(-m, -m)));
+                    return __fmul2_rn(d, make_float2(rs, rs));
+                });
         }
 #pragma unroll
         for (int i = 0; i < V; i += 4) *reinterpret_cast<float4 *>(mine + i) = make_float4(z[i], z[i + 1], z[i + 2], z[i + 3]);
         auto ranked = [&](float v) { return a.bias || v == -INFINITY ? v : relative_score(v, m, a.sigmoid); };
         bool dropped = false;
+        float top_of[kBlocks];  // the largest of each eight
         if (by_lanes) {
+            // the two largest, of pairs, of eights and of the lane's
             float g1 = -INFINITY, g2 = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                g2 = fmaxf(g2, fminf(g1, z[i]));
-                g1 = fmaxf(g1, z[i]);
+            for (int b = 0; b < kBlocks; ++b) {
+                float t1 = -INFINITY, t2 = -INFINITY;
+#pragma unroll
+                for (int i = 8 * b; i < 8 * b + 8; i += 2) {
+                    const float hi = fmaxf(z[i], z[i + 1]), lo = fminf(z[i], z[i + 1]);
+                    if (i == 8 * b) {
+                        t1 = hi, t2 = lo;
+                    } else {
+                        t2 = fmaxf(fmaxf(t2, lo), fminf(t1, hi));
+                        t1 = fmaxf(t1, hi);
+                    }
+                }
+                top_of[b] = t1;
+                if (b == 0) {
+                    g1 = t1, g2 = t2;
+                } else {
+                    g2 = fmaxf(fmaxf(g2, t2), fminf(g1, t1));
+                    g1 = fmaxf(g1, t1);
+                }
             }
             g1 = ranked(g1);
             g2 = ranked(g2);
@@ -267,11 +297,16 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(V)) k_route(RouteArg
         } else if (grouped) {
             __syncwarp();
             auto group_score = [&](int g) {
+                auto key = [&](int j) { return row_keys[j + (kLane - V) * (j / V)]; };
                 float g1 = -INFINITY, g2 = -INFINITY;
-                for (int j = g * per; j < g * per + per; ++j) {
-                    const float v = row_keys[j / V * kLane + j % V];
-                    g2 = fmaxf(g2, fminf(v, g1));
-                    g1 = fmaxf(g1, v);
+                int j = g * per;
+                if (per & 1) g1 = key(j++);
+#pragma unroll 4
+                for (int end = g * per + per; j < end; j += 2) {
+                    const float x = key(j), y = key(j + 1);
+                    const float hi = fmaxf(x, y), lo = fminf(x, y);
+                    g2 = fmaxf(fmaxf(g2, lo), fminf(g1, hi));
+                    g1 = fmaxf(g1, hi);
                 }
                 g1 = ranked(g1);
                 g2 = ranked(g2);
@@ -300,19 +335,30 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(V)) k_route(RouteArg
                 if (sub + h * L < a.groups && before[h] < a.top_groups) kept |= 1u << (sub + h * L);
 #pragma unroll
             for (int o = L / 2; o > 0; o >>= 1) kept |= __shfl_xor_sync(kFullMask, kept, o);
+            // a lane's columns, from group to group
+            __syncwarp();
+            int g = j0 / per, left = per - j0 % per;
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (j0 + i >= E || !(kept >> ((j0 + i) / per) & 1u)) z[i] = mine[i] = -INFINITY;
+            for (int i = 0; i < V; i += 4) {
+#pragma unroll
+                for (int h = i; h < i + 4; ++h) {
+                    if (g >= a.groups || !(kept >> g & 1u)) z[h] = -INFINITY;
+                    if (--left == 0) left = per, ++g;
+                }
+                *reinterpret_cast<float4 *>(mine + i) = make_float4(z[i], z[i + 1], z[i + 2], z[i + 3]);
+            }
         }
-        float top_of[kBlocks], best = -INFINITY;
+        if (!by_lanes) {
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-            float t = z[8 * b];
+            for (int b = 0; b < kBlocks; ++b) {
+                top_of[b] = z[8 * b];
 #pragma unroll
-            for (int i = 1; i < 8; ++i) t = fmaxf(t, z[8 * b + i]);
-            top_of[b] = t;
-            best = fmaxf(best, t);
+                for (int i = 1; i < 8; ++i) top_of[b] = fmaxf(top_of[b], z[8 * b + i]);
+            }
         }
+        float best = top_of[0];
+#pragma unroll
+        for (int b = 1; b < kBlocks; ++b) best = fmaxf(best, top_of[b]);
         if (dropped) best = -INFINITY;
         // the k best, one after another: the largest, the lowest column of equals
 #pragma unroll
