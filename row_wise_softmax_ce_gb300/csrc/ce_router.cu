@@ -9,6 +9,7 @@
 // None uses tensor cores: a row is a few hundred columns, and its choice compares.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "ce_internal.h"
 #include "ce_launch.h"
@@ -207,17 +208,26 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(V)) k_route(RouteArg
                 load_columns<T, V>(raw, static_cast<const T *>(a.logits) + row * a.stride, j0, E);
             unpack_columns<T, V>(z, raw);
         }
-        float m = max_nan(z[0], z[1], z[2]);
+        // 0 z adds up to 0 unless something of the warp's is infinite or NaN
+        float2 probe = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 3; i + 1 < V; i += 2) m = max_nan(m, z[i], z[i + 1]);
-        m = max_nan(m, z[V - 1], z[V - 1]);
-        const bool odd = row_ballot<L>(!(m < INFINITY)) != 0;  // a NaN or +inf
-        if (odd) {
-            m = -INFINITY;
+        for (int i = 0; i < V; i += 2) probe = __ffma2_rn(make_float2(z[i], z[i + 1]), make_float2(0.0f, 0.0f), probe);
+        const bool plain = !__any_sync(kFullMask, isnan(probe.x + probe.y));
+        float m = 0.0f;
+        bool odd = false;
+        if (!plain || !a.sigmoid || !a.bias) {
+            m = max_nan(z[0], z[1], z[2]);
 #pragma unroll
-            for (int i = 0; i < V; ++i) z[i] = -INFINITY;
+            for (int i = 3; i + 1 < V; i += 2) m = max_nan(m, z[i], z[i + 1]);
+            m = max_nan(m, z[V - 1], z[V - 1]);
+            odd = row_ballot<L>(!(m < INFINITY)) != 0;  // a NaN or +inf
+            if (odd) {
+                m = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < V; ++i) z[i] = -INFINITY;
+            }
+            m = row_max<L>(m);
         }
-        m = row_max<L>(m);
         float rs = 0.0f;  // softmax: 1 / s, where the scores themselves are asked for
         if (!a.sigmoid && (a.bias || !a.renormalise)) {
             const float mm = m == -INFINITY ? 0.0f : m;
@@ -230,25 +240,31 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(V)) k_route(RouteArg
         // bias, the logit, which orders the experts as their scores do and is exact
         if (a.bias) {
             const float *b = bias + sub * kLane;
-            auto biased = [&](auto score) {  // two columns at a time
+            auto biased = [&](auto score, auto masked) {  // two columns at a time
 #pragma unroll
                 for (int i = 0; i < V; i += 4) {
                     const float4 f = *reinterpret_cast<const float4 *>(b + i);
                     const float2 lo = __fadd2_rn(score(make_float2(z[i], z[i + 1])), make_float2(f.x, f.y));
                     const float2 hi = __fadd2_rn(score(make_float2(z[i + 2], z[i + 3])), make_float2(f.z, f.w));
-                    z[i] = z[i] > -INFINITY ? lo.x : -INFINITY;
-                    z[i + 1] = z[i + 1] > -INFINITY ? lo.y : -INFINITY;
-                    z[i + 2] = z[i + 2] > -INFINITY ? hi.x : -INFINITY;
-                    z[i + 3] = z[i + 3] > -INFINITY ? hi.y : -INFINITY;
+                    z[i] = !masked || z[i] > -INFINITY ? lo.x : -INFINITY;
+                    z[i + 1] = !masked || z[i + 1] > -INFINITY ? lo.y : -INFINITY;
+                    z[i + 2] = !masked || z[i + 2] > -INFINITY ? hi.x : -INFINITY;
+                    z[i + 3] = !masked || z[i + 3] > -INFINITY ? hi.y : -INFINITY;
                 }
             };
-            if (a.sigmoid)
-                biased([](float2 x) { return sigmoid2(x); });
-            else
-                biased([&](float2 x) {
-                    const float2 d = exp2_of(__fadd2_rn(x, make_float2(-m, -m)));
-                    return __fmul2_rn(d, make_float2(rs, rs));
-                });
+            if (a.sigmoid) {
+                if (plain)
+                    biased([](float2 x) { return sigmoid2(x); }, std::false_type());
+                else
+                    biased([](float2 x) { return sigmoid2(x); }, std::true_type());
+            } else {
+                biased(
+                    [&](float2 x) {
+                        const float2 d = exp2_of(__fadd2_rn(x, make_float2(-m, -m)));
+                        return __fmul2_rn(d, make_float2(rs, rs));
+                    },
+                    std::true_type());
+            }
         }
 #pragma unroll
         for (int i = 0; i < V; i += 4) *reinterpret_cast<float4 *>(mine + i) = make_float4(z[i], z[i + 1], z[i + 2], z[i + 3]);
