@@ -155,7 +155,9 @@ __global__ void __launch_bounds__(kRouteThreads) k_zero(unsigned long long *coun
     for (int j = threadIdx.x; j < n; j += kRouteThreads) counts[j] = 0;
 }
 
-// CTAs of an SM, by the columns a lane holds.
+// CTAs of an SM, by the columns a lane holds: 80 registers a thread at 32 of them
+// (16384 x 256, us, of 2 / 3 / 4 CTAs: 12.7 / 12.0 / 12.8), 64 else (30011 x 60, of
+// 2 / 3 / 4 / 5: 9.4 / 8.3 / 8.3 / 10.0).
 __host__ __device__ constexpr int route_ctas(int v) { return v > 16 ? 3 : 4; }
 // Words of a row in shared memory: its lanes' columns, 16 bytes apart by bank, the
 // rows of a warp 32.
@@ -166,9 +168,11 @@ __host__ __device__ constexpr int route_row(int lanes, int v) { return lanes * (
 // largest of each eight of its columns only: the columns lie in shared memory,
 // where the lane that gives one looks for it among eight, takes it out and has the
 // largest of the rest. Measured (us, 16384 x 256 bf16, k = 8,
-// sigmoid scores with a bias, 4 of 8 groups): this 11.6; a row a warp, with each
+// sigmoid scores with a bias, 4 of 8 groups): this 9.9; a row a warp, with each
 // lane's two best columns and the value of its third in registers, 16.0. Counts
-// add 1.1 us, and 1.4 more with a CTA per 32 rows than with three an SM.
+// add 1.1 us, and 1.4 more with a CTA per 32 rows than with three an SM. The eight
+// searched by the row's lanes, a column each, take fewer instructions in a longer
+// chain: 0.3 us slower here, 6% faster at four times the rows.
 template <typename T, int L, int V, int kPer>  // kPer slots a lane
 __global__ void __launch_bounds__(kRouteThreads, route_ctas(V)) k_route(RouteArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -680,13 +684,13 @@ void route_shape(const RouteArgs &a, int most, int slots, int *lanes, int *v) {
 // Columns of a lane at most: 32, where rows are many and instructions count; 8
 // where they are few, a row's latency counts and lanes are to spare. Measured
 // (us, bf16, k = 8, sigmoid scores with a bias, 8 / 32 columns): 256 experts in 8
-// groups, 32 rows 4.2 / 5.7, 1024 4.4 / 5.9, 2048 5.3 / 6.0, 4096 7.6 / 6.2, 8192
-// 13.1 / 7.9, 16384 20.8 / 11.9, 65536 76 / 34; 512 experts, 1024 rows 5.0 / 6.3,
-// 4096 8.6 / 7.8, 16384 24 / 18.
+// groups, 32 rows 3.7 / 4.8, 1024 3.9 / 5.1, 2048 4.7 / 5.1, 4096 7.0 / 5.4, 8192
+// 11.8 / 6.9, 16384 18.7 / 10.0, 65536 68 / 29; 512 experts, 1024 rows 4.5 / 5.5,
+// 4096 7.8 / 7.0, 16384 21.1 / 15.9.
 int route_most(const RouteArgs &a, const DeviceInfo &dev) {
     int lanes, v;
     route_shape(a, 8, 1, &lanes, &v);
-    return a.rows * lanes <= 12 * 32 * static_cast<int64_t>(dev.sms) ? 8 : 32;
+    return a.rows * lanes <= 14 * 32 * static_cast<int64_t>(dev.sms) ? 8 : 32;
 }
 
 }  // namespace
