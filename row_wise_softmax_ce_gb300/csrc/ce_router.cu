@@ -1,7 +1,7 @@
 // ce_router.cu -- sm_103a kernels of the routing of rows to experts, and their
 // launchers.
 //
-//   k_route            route_rows: 8 to 32 lanes per row, its columns in shared memory
+//   k_route            route_rows: 4 to 32 lanes per row, its columns in shared memory
 //   k_zero             its counts
 //   k_route_grad       route_grad where only the chosen experts get any
 //   k_route_grad_full  where all do
@@ -34,18 +34,19 @@ template <typename T, int V>
 __device__ __forceinline__ void load_columns(uint4 (&v)[V / Vec<T>::kN], const T *p, int j, int n) {
     constexpr int N = Vec<T>::kN;
     static_assert(V % N == 0, "whole vectors");
-    if (j + V <= n && (reinterpret_cast<uintptr_t>(p + j) & 15) == 0) {
+    const bool vectors = (reinterpret_cast<uintptr_t>(p + j) & 15) == 0;
 #pragma unroll
-        for (int i = 0; i < V / N; ++i) v[i] = *reinterpret_cast<const uint4 *>(p + j + N * i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V / N; ++i)
+    for (int i = 0; i < V / N; ++i) {
+        if (vectors && j + N * i + N <= n) {
+            v[i] = *reinterpret_cast<const uint4 *>(p + j + N * i);
+        } else {
 #pragma unroll
             for (int h = 0; h < N / 2; ++h) {
                 const int c = j + N * i + 2 * h;
                 Vec<T>::set_pair(v[i], h, make_float2(c < n ? Vec<T>::to_float(p[c]) : -INFINITY,
                                                       c + 1 < n ? Vec<T>::to_float(p[c + 1]) : -INFINITY));
             }
+        }
     }
 }
 template <typename T, int V>
@@ -64,18 +65,19 @@ __device__ __forceinline__ void unpack_columns(float (&z)[V], const uint4 (&v)[V
 template <typename T, int V>
 __device__ __forceinline__ void store_columns(T *p, int j, int n, const float (&z)[V]) {
     constexpr int N = Vec<T>::kN;
-    if (j + V <= n && (reinterpret_cast<uintptr_t>(p + j) & 15) == 0) {
+    const bool vectors = (reinterpret_cast<uintptr_t>(p + j) & 15) == 0;
 #pragma unroll
-        for (int i = 0; i < V / N; ++i) {
+    for (int i = 0; i < V / N; ++i) {
+        if (vectors && j + N * i + N <= n) {
             uint4 v = make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int h = 0; h < N / 2; ++h) Vec<T>::set_pair(v, h, make_float2(z[N * i + 2 * h], z[N * i + 2 * h + 1]));
             *reinterpret_cast<uint4 *>(p + j + N * i) = v;
-        }
-    } else {
+        } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (j + i < n) p[j + i] = Vec<T>::from_float(z[i]);
+            for (int h = N * i; h < N * i + N; ++h)
+                if (j + h < n) p[j + h] = Vec<T>::from_float(z[h]);
+        }
     }
 }
 
@@ -156,12 +158,12 @@ __global__ void __launch_bounds__(kRouteThreads) k_zero(unsigned long long *coun
 }
 
 // CTAs of an SM, by the columns a lane holds: 80 registers a thread at 32 of them
-// (16384 x 256, us, of 2 / 3 / 4 CTAs: 12.7 / 12.0 / 12.8), 64 else (30011 x 60, of
-// 2 / 3 / 4 / 5: 9.4 / 8.3 / 8.3 / 10.0).
+// (16384 x 256, us, of 2 / 3 / 4 CTAs: 12.7 / 12.0 / 12.8), 64 else (65536 x 64 at
+// eight a lane, of 2 / 3 / 4 / 5: 22.2 / 18.6 / 18.6 / 23.4).
 __host__ __device__ constexpr int route_ctas(int v) { return v > 16 ? 3 : 4; }
 // Words of a row in shared memory: its lanes' columns, 16 bytes apart by bank, the
 // rows of a warp 32.
-__host__ __device__ constexpr int route_row(int lanes, int v) { return lanes * (v + 4) + (lanes < 32 ? 8 : 0); }
+__host__ __device__ constexpr int route_row(int lanes, int v) { return lanes * (v + 4) + (lanes == 8 || lanes == 16 ? 8 : 0); }
 
 // k_route: bound by the instructions of the choice, most of them compares at half
 // rate. So up to four rows share a warp's instructions, and a lane keeps the
@@ -177,7 +179,7 @@ template <typename T, int L, int V, int kPer>  // kPer slots a lane
 __global__ void __launch_bounds__(kRouteThreads, route_ctas(V)) k_route(RouteArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     constexpr int R = 32 / L, kVecs = V / Vec<T>::kN, kBlocks = V / 8, kLane = V + 4;  // rows of a warp
-    static_assert(kPer == 1 || kPer * L == kMaxChosen, "slots");
+    static_assert(kPer * L <= kMaxChosen, "slots");
     const int lane = threadIdx.x & 31, sub = lane & (L - 1), row0 = lane & ~(L - 1), E = a.experts, j0 = sub * V;
     const int per = E / a.groups;
     const bool grouped = a.top_groups < a.groups;
@@ -250,10 +252,10 @@ __global__ void __launch_bounds__(kRouteThreads, route_ctas(V)) k_route(RouteArg
                     const float4 f = *reinterpret_cast<const float4 *>(b + i);
                     const float2 lo = __fadd2_rn(score(make_float2(z[i], z[i + 1])), make_float2(f.x, f.y));
                     const float2 hi = __fadd2_rn(score(make_float2(z[i + 2], z[i + 3])), make_float2(f.z, f.w));
-                    z[i] = !masked || z[i] > -INFINITY ? lo.x : -INFINITY;
-                    z[i + 1] = !masked || z[i + 1] > -INFINITY ? lo.y : -INFINITY;
-                    z[i + 2] = !masked || z[i + 2] > -INFINITY ? hi.x : -INFINITY;
-                    z[i + 3] = !masked || z[i + 3] > -INFINITY ? hi.y : -INFINITY;
+                    z[i] = !decltype(masked)::value || z[i] > -INFINITY ? lo.x : -INFINITY;
+                    z[i + 1] = !decltype(masked)::value || z[i + 1] > -INFINITY ? lo.y : -INFINITY;
+                    z[i + 2] = !decltype(masked)::value || z[i + 2] > -INFINITY ? hi.x : -INFINITY;
+                    z[i + 3] = !decltype(masked)::value || z[i + 3] > -INFINITY ? hi.y : -INFINITY;
                 }
             };
             if (a.sigmoid) {
@@ -629,6 +631,7 @@ const void *route_kernel_l(int v) {
 template <typename T>
 const void *route_kernel_t(int lanes, int v, int k) {
     if (lanes == 32) return route_kernel_l<T, 32, 1>(v);
+    if (lanes == 4) return k <= 4 ? route_kernel_l<T, 4, 1>(v) : route_kernel_l<T, 4, 2>(v);
     if (lanes == 16) return k <= 16 ? route_kernel_l<T, 16, 1>(v) : route_kernel_l<T, 16, 2>(v);
     return k <= 8 ? route_kernel_l<T, 8, 1>(v) : route_kernel_l<T, 8, 4>(v);
 }
@@ -675,9 +678,9 @@ cudaError_t launch_route_rows(const void *fn, const RouteArgs &a, int lanes, int
     return cudaLaunchKernelExC(&l.cfg, fn, args);
 }
 
-// As few lanes as hold a row's columns at `most` each, and `slots` at one each.
-void route_shape(const RouteArgs &a, int most, int slots, int *lanes, int *v) {
-    for (*lanes = 8; *lanes < 32 && (*lanes * most < a.experts || *lanes < slots);) *lanes *= 2;
+// As few lanes, `least` or more, as hold a row's columns at `most` each, and `slots` at one each.
+void route_shape(const RouteArgs &a, int least, int most, int slots, int *lanes, int *v) {
+    for (*lanes = least; *lanes < 32 && (*lanes * most < a.experts || *lanes < slots);) *lanes *= 2;
     for (*v = 8; *lanes * *v < a.experts;) *v *= 2;
 }
 
@@ -686,11 +689,11 @@ void route_shape(const RouteArgs &a, int most, int slots, int *lanes, int *v) {
 // (us, bf16, k = 8, sigmoid scores with a bias, 8 / 32 columns): 256 experts in 8
 // groups, 32 rows 3.7 / 4.8, 1024 3.9 / 5.1, 2048 4.7 / 5.1, 4096 7.0 / 5.4, 8192
 // 11.8 / 6.9, 16384 18.7 / 10.0, 65536 68 / 29; 512 experts, 1024 rows 4.5 / 5.5,
-// 4096 7.8 / 7.0, 16384 21.1 / 15.9.
+// 4096 7.8 / 7.0, 16384 21.1 / 15.9; 128 experts, 4096 rows 6.6 / 5.6.
 int route_most(const RouteArgs &a, const DeviceInfo &dev) {
     int lanes, v;
-    route_shape(a, 8, 1, &lanes, &v);
-    return a.rows * lanes <= 14 * 32 * static_cast<int64_t>(dev.sms) ? 8 : 32;
+    route_shape(a, 8, 8, 1, &lanes, &v);
+    return a.rows * lanes <= 12 * 32 * static_cast<int64_t>(dev.sms) ? 8 : 32;
 }
 
 }  // namespace
@@ -703,7 +706,14 @@ cudaError_t launch_route(DType t, const RouteArgs &a, const DeviceInfo &dev, cud
         if (e != cudaSuccess || a.rows == 0) return e;
     }
     int lanes, v;
-    route_shape(a, route_most(a, dev), 1, &lanes, &v);
+    // Four lanes a row, of many rows of up to 128 columns, so that eight share a warp's
+    // instructions: for eight slots at most, two a lane, and not where groups would be
+    // parts of a lane. Measured (us, bf16, sigmoid scores with a bias, 8 / 4 lanes): 32
+    // experts, k = 2, 16384 rows 4.6 / 3.4, 30000 6.2 / 4.1; 64, k = 6, 10000 5.0 / 4.7,
+    // 16384 5.8 / 4.9, 30000 8.3 / 6.7; 128, k = 8, 16384 7.4 / 6.5, 30000 10.8 / 9.6.
+    const int most = route_most(a, dev);
+    route_shape(a, most == 32 && a.k <= 8 ? 4 : 8, most, 1, &lanes, &v);
+    if (a.top_groups < a.groups && a.experts / a.groups % v != 0) route_shape(a, 8, most, 1, &lanes, &v);
     const int rows = kRouteWarps * (32 / lanes);
     const int smem = 4 * (rows * (route_row(lanes, v) + kMaxChosen) + (a.bias ? route_row(lanes, v) : 0) +
                           (a.counts ? a.experts : 0));  // at most 46592 bytes
@@ -714,7 +724,7 @@ cudaError_t launch_route_grad(DType t, const RouteArgs &a, const DeviceInfo &dev
     g_launched.note(dev);
     int lanes, v;
     if (!a.sigmoid && !a.renormalise) {
-        route_shape(a, 8, a.k, &lanes, &v);
+        route_shape(a, 8, 8, a.k, &lanes, &v);
         return launch_route_rows(route_full_kernel(t, lanes, v), a, lanes, 8, 4 * kRouteWarps * 32 * v, false, dev, s);
     }
     for (lanes = 8; lanes < a.k;) lanes *= 2;
