@@ -674,6 +674,36 @@ def test_route_many_rows():
         assert torch.equal(total, counts)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("E,k,G,t", [(16, 4, 1, 1), (31, 1, 1, 1), (32, 8, 4, 1), (60, 4, 1, 1), (60, 4, 4, 2), (64, 6, 1, 1), (64, 8, 4, 2),
+                                     (64, 3, 8, 3), (100, 5, 1, 1), (128, 8, 4, 2), (127, 2, 1, 1), (128, 9, 1, 1)])
+def test_route_small_rows_in_numbers(dtype, E, k, G, t):
+    """Many rows of few experts, eight to a warp: a part of them against the definition, the rest among themselves."""
+    g = gen(E + k)
+    rows, part = 10007, 48
+    x = rows_of(part, E, TYPES[dtype], g, sigma=1.5, mask=0.05)
+    x[3] = -math.inf
+    x[7, E // 2] = math.nan
+    x[8, E - 1] = math.inf
+    x[9:20] = x[9:20].float().round().to(TYPES[dtype])  # ties
+    w = torch.ones(part)
+    w[30], w[44] = 0.0, 0.0
+    b = 0.2 * torch.randn(E, generator=g)
+    at = torch.arange(rows) % part
+    for score, bias, renorm, pad in (("sigmoid", b, True, 0), ("softmax", None, False, 1), ("softmax", b, True, 0)):
+        many = torch.zeros(rows, E + pad, dtype=TYPES[dtype])
+        many[:, :E] = x.cpu()[at]
+        kw = dict(score=score, groups=G, top_groups=t, renormalise=renorm)
+        chosen, gates, counts = ce.route_rows(many.to(DEV)[:, :E], k, bias=None if bias is None else bias.to(DEV),
+                                              weights=w[at].to(DEV), counts=True, **kw)
+        assert torch.equal(counts, torch.bincount(chosen[chosen >= 0], minlength=E))
+        chosen, gates = chosen.cpu(), gates.cpu()
+        of = torch.bincount(chosen[:part][chosen[:part] >= 0], minlength=E)
+        R.check_routed(x.cpu(), k, chosen[:part], gates[:part], of, bias=bias, weights=w, **kw)
+        assert torch.equal(chosen, chosen[:part][at])
+        assert torch.equal(gates.view(torch.int32), gates[:part][at].view(torch.int32))
+
+
 # -- together, and how they are called ---------------------------------------------------
 
 def step(x, y, ends, u, draws, router, w, G):
