@@ -549,7 +549,9 @@ CE_API int sample_rows(const void *logits, int dtype, int64_t rows, int64_t voca
  *     d is accepted where a q_d < p_d (a as it is given: a NaN accepts
  *     nothing) and p_d > 0;
  *     otherwise a token is drawn by u, as sample_rows draws it, from
- *     max(0, p_j - q_j) in proportion.
+ *     max(0, p_j - q_j) in proportion; the columns beside a looked-up draft are
+ *     weighed by the largest of them, and count as 0 where that one is below
+ *     2^-126 of the draft's weight.
  * A request emits its accepted drafts, row by row, up to the first row that
  * accepts none, and that row's drawn token. A row without a draft draws from p:
  * the row behind the last draft of a request has none. A row at temperature 0

@@ -138,7 +138,7 @@ struct RowGrid {
 // What a column weighs in a draw: 2^((x - m) k), a looked-up draft's column
 // (skip) 0; or, kResidual, what its draft row leaves of it, max(0, p - q).
 struct Weigh {
-    float m, k;        // the row's
+    float m, k;        // the largest that may be drawn, and the row's factor
     int skip;          // -1: none
     float c, mq, cq;   // kResidual: -log2 s, the draft row's max and its -log2 s
 };
@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(kRowThreads) k_sample_row(ChoiceArgs a) {
 enum Verdict : int { kAccepted = 0, kKnown = 1, kFromOwn = 2, kFromRest = 3, kOdd = 4 };
 struct Open {  // of a row whose token is still to be drawn
     Weigh w;
-    float inv_t, s, u;
+    float m, inv_t, s, u;  // m: the row's max, of w.m's columns and a looked-up draft's
     int step;  // kLookup: where u falls, and t from its start on
     Mass t;
 };
@@ -652,6 +652,7 @@ __device__ __forceinline__ int judge(const ChoiceArgs &a, int64_t row, const Row
     TokState q{};
     if (!kLookup && drafted) q = Steps(draft_states_of(a, row), a.steps).merged(heat.k);
     TokState p = steps.merged(heat.k);
+    const float others = p.m;
     if (lookup) tok_push1<false>(p, r.xd, heat.k);  // its column is not among the states
     Verdict v = kKnown;
     bool odd = r.draft >= a.vocab;
@@ -665,7 +666,13 @@ __device__ __forceinline__ int judge(const ChoiceArgs &a, int64_t row, const Row
         if (token == r.d) v = kAccepted;
     } else {
         Open o{};
-        o.w = Weigh{p.m, heat.k, lookup ? r.d : -1, -log2f(p.s), q.m, -log2f(q.s)};
+        // The columns beside a looked-up draft are weighed by the largest of them: their
+        // masses would be too coarse beside a draft that holds nearly all of the row (a
+        // rest of 2^-18 of it, or less). Where that one itself weighs nothing beside the
+        // draft, as where it is masked, none does.
+        const float m = lookup && ex2_ftz((others - p.m) * heat.k) > 0.0f ? others : p.m;
+        o.w = Weigh{m, heat.k, lookup ? r.d : -1, -log2f(p.s), q.m, -log2f(q.s)};
+        o.m = p.m;
         o.inv_t = heat.inv_t;
         o.s = p.s;
         o.u = r.u;
@@ -854,11 +861,11 @@ __global__ void __launch_bounds__(kDrawThreads, 4) k_decide(ChoiceArgs a) {
         if (step >= 0)
             f = column_of<T, false>(g, g, step, o.w, t, sums);
         else  // nothing but the looked-up draft weighs anything: it is the row's largest
-            f = Found{warp == 0, o.w.skip, o.w.m};
+            f = Found{warp == 0, o.w.skip, o.m};
     }
     if (f.mine && lane == 0) {
         a.tokens[stop] = f.column;
-        if (a.logp) a.logp[stop] = f.column < 0 ? nan_f() : (f.x - o.w.m) * o.inv_t - logf(o.s);
+        if (a.logp) a.logp[stop] = f.column < 0 ? nan_f() : (f.x - o.m) * o.inv_t - logf(o.s);
     }
 }
 
