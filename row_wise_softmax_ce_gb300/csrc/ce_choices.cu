@@ -383,11 +383,19 @@ __device__ __forceinline__ float2 *draft_states_of(const ChoiceArgs &a, int64_t 
     return a.states + (a.rows + row) * a.steps;
 }
 
+// A row that emits nothing.
+__device__ __forceinline__ void silence(const ChoiceArgs &a, int64_t row) {
+    a.tokens[row] = -1;
+    if (a.logp) a.logp[row] = 0.0f;
+}
+
 // k_states: HBM-bound (591 MB of bf16 rows 87 us, 6.8 TB/s; 78 MB 14 us, as a plain
 // read of them). A warp per `unit` steps of a row: (m, s) of each step, its m the
 // largest value up to the step's end. Rows [0, rows) are the target's, and, of a
 // verification with draft logits, rows [rows, 2 rows) the drafts'; a row in no
-// request, and the draft row of a row without a draft, are not read.
+// request, and the draft row of a row without a draft, are not read. A row of a
+// verification emits nothing until k_decide gives it a token, whatever the offsets
+// hold.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 8) k_states(ChoiceArgs a, int unit, int units, int64_t warps) {
     launch_dependents();
@@ -401,7 +409,10 @@ __global__ void __launch_bounds__(kThreads, 8) k_states(ChoiceArgs a, int unit, 
     float temperature = a.temperature;
     if (a.offsets) {
         draft = row >= a.rows;
-        if (draft) row -= a.rows;
+        if (draft)
+            row -= a.rows;
+        else if (first == 0 && lane == 0)
+            silence(a, row);
         // asked for together: one latency before the row's own
         const int64_t lo = a.offsets[0], hi = a.offsets[a.requests], d = a.drafts[row];
         temperature = temperature_of(a, row);
@@ -772,21 +783,13 @@ __global__ void __launch_bounds__(kDrawThreads, 4) k_decide(ChoiceArgs a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank(), C = cluster_size();
     const int64_t s = cluster_id_x(), lo = a.offsets[0], hi = a.offsets[a.requests];
-    const int64_t r0 = s < a.requests ? a.offsets[s] : 0, r1 = s < a.requests ? a.offsets[s + 1] : 0;
+    const int64_t r0 = a.offsets[s], r1 = a.offsets[s + 1];
     const bool good = r0 >= 0 && r1 >= r0 && r1 <= a.rows, writes = rank == 0;
-    auto silent = [&](int64_t row) {
-        a.tokens[row] = -1;
-        if (a.logp) a.logp[row] = 0.0f;
-    };
     // a row outside [lo, hi) has no states: of a table that decreases
     auto has_states = [&](int64_t row) { return good && row < r1 && row >= lo && row < hi; };
     RowNumbers numbers{0, 0.0f, 0.0f, 0.0f, 0.0f, Heat(1.0f), -1};
     if (has_states(r0 + warp)) numbers = row_numbers<T, kLookup>(a, r0 + warp);
     wait_prerequisites();
-    if (s == 0 && writes)  // rows in no request
-        for (int64_t r = threadIdx.x; r < a.rows; r += kDrawThreads)
-            if (r < lo || r >= hi) silent(r);
-    if (s >= a.requests) return;
     int64_t stop = good ? -1 : 0;
     int by = 0, verdict = kAccepted;  // the warp that judged row `stop`, and what it came to
     for (int64_t r = r0; good && r < r1 && stop < 0; r += kRows) {
@@ -796,8 +799,6 @@ __global__ void __launch_bounds__(kDrawThreads, 4) k_decide(ChoiceArgs a) {
         if (has_states(row)) {
             if (r > r0) numbers = row_numbers<T, kLookup>(a, row);
             v = judge<T, kLookup>(a, row, numbers, writes, &opens[warp]);
-        } else if (row < r1 && writes && lane == 0) {
-            silent(row);
         }
         if (lane == 0) verdicts[warp] = v;
         __syncthreads();
@@ -815,7 +816,9 @@ __global__ void __launch_bounds__(kDrawThreads, 4) k_decide(ChoiceArgs a) {
             a.accepted[s] = good ? stop - r0 : -1;
             if (!good || (verdict & kOdd)) count_bad();
         }
-        for (int64_t r = stop + 1 + threadIdx.x; good && r < r1; r += kDrawThreads) silent(r);
+        // rows judged beside it that lie behind it
+        const int64_t behind = stop + 1 + threadIdx.x;
+        if (good && behind < min(r1, stop - by + kRows)) silence(a, behind);
     }
     verdict &= ~kOdd;
     if (verdict == kAccepted || verdict == kKnown) return;
@@ -935,10 +938,11 @@ cudaError_t verify_as(ChoiceArgs a, const DeviceInfo &dev, cudaStream_t s) {
     // 116 / 119 / 126.
     int c = 1;
     while (drawn && c < kMaxCluster && c * a.requests < 3 * dev.sms && c * (kDrawThreads / 32) <= a.steps) c *= 2;
+    if (a.requests == 0) return cudaSuccess;
     Kernel &k = Kernels<T>::decide(!drawn);
     if ((e = ready(k, dev))) return e;
     void *args[] = {&a};
-    LaunchConfig l(std::max<int64_t>(1, a.requests) * c, kDrawThreads, c, a.rows > 0, s);
+    LaunchConfig l(a.requests * c, kDrawThreads, c, a.rows > 0, s);
     return cudaLaunchKernelExC(&l.cfg, k.fn, args);
 }
 
