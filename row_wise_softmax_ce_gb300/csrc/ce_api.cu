@@ -935,8 +935,8 @@ static int check_outputs_apart(std::initializer_list<Rows> rows, std::initialize
 
 int64_t choice_work(int dtype, int64_t rows, int64_t vocab, int64_t requests) {
     if (dtype != CE_F32 && dtype != CE_BF16 && dtype != CE_F16) return CE_EINVAL;
-    if (rows < 0 || vocab < 1 || vocab > kMaxVocab || requests < -1 || requests > INT32_MAX) return CE_EINVAL;
-    if (rows > (INT64_MAX / 64) / (vocab / 512 + 2)) return CE_EINVAL;
+    if (rows < 0 || rows > INT32_MAX || vocab < 1 || vocab > kMaxVocab) return CE_EINVAL;
+    if (requests < -1 || requests > INT32_MAX) return CE_EINVAL;
     return choice_bytes(static_cast<DType>(dtype), rows, vocab, requests);
 }
 
