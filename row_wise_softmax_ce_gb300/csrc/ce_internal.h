@@ -174,8 +174,8 @@ struct ChoiceArgs {
 };
 
 constexpr int kMaxExperts = 1024;
-constexpr int kMaxChosen = 32;  // experts of a row: a lane each
-constexpr int kMaxGroups = 32;  // a lane each
+constexpr int kMaxChosen = 32;  // experts of a row: its slots in shared memory; of the gradient a lane each
+constexpr int kMaxGroups = 32;  // a bit each of what a row keeps
 
 // Arguments of route_rows and route_grad; unused pointers are null.
 struct RouteArgs {

@@ -622,11 +622,13 @@ int64_t capped(int64_t clusters, int64_t cap) {
     return std::max<int64_t>(1, cap > 0 ? std::min(clusters, cap) : clusters);
 }
 
+// 8, 16 or 32 columns a lane; 16 lanes have 8 (to 128 columns) or 32 (257 to 512)
 template <typename T, int L, int kPer>
 const void *route_kernel_l(int v) {
-    return v == 32   ? reinterpret_cast<const void *>(&k_route<T, L, 32, kPer>)
-           : v == 16 ? reinterpret_cast<const void *>(&k_route<T, L, 16, kPer>)
-                     : reinterpret_cast<const void *>(&k_route<T, L, 8, kPer>);
+    if constexpr (L != 16)
+        if (v == 16) return reinterpret_cast<const void *>(&k_route<T, L, 16, kPer>);
+    return v == 32 ? reinterpret_cast<const void *>(&k_route<T, L, 32, kPer>)
+                   : reinterpret_cast<const void *>(&k_route<T, L, 8, kPer>);
 }
 template <typename T>
 const void *route_kernel_t(int lanes, int v, int k) {
