@@ -525,8 +525,9 @@ CE_API int64_t choice_work(int dtype, int64_t rows, int64_t vocab, int64_t reque
  * e_j = exp((x_j - m) / T), m = max_j x_j and S = sum_j e_j, row i's token is
  *     the first k with e_0 + ... + e_k > u_i S
  * (columns in order; e_j below 2^-126 counts as 0). T = 0 is the row's argmax.
- * Where u_i S lies within the rounding of a border between two columns (a few
- * 2^-24 of S) either may be taken; the same call gives the same tokens always.
+ * Where u_i S lies within the rounding of a border between two columns either may
+ * be taken; the same call gives the same tokens always. A border is off by less
+ * than 2^-15 of S if all roundings add up, by less than 2^-24 as measured.
  *   uniforms: [rows] f32, the u_i.
  *   temperature: 0, or in [1e-6, 1e6].   temperatures: [rows] f32, likewise,
  *     instead of it, or NULL; a row whose entry is neither counts as no
