@@ -567,8 +567,9 @@ CE_API int sample_rows(const void *logits, int dtype, int64_t rows, int64_t voca
  *   offsets: [requests + 1] int64 on the device, non-decreasing, within
  *     [0, rows]. A request may have no rows. Nothing is read or written out of
  *     range whatever the table holds: a range that is not valid is counted and
- *     its request's `accepted` is -1. A row that such a table leaves to no request
- *     emits nothing; one that it gives to several may emit any one's token, or none.
+ *     its request's `accepted` is -1. A row that such a table leaves to no request,
+ *     or outside offsets[0] .. offsets[requests], emits nothing; one that it gives to
+ *     several may emit any one's token, or none.
  *   uniforms: [rows, 2] f32, the pairs (a, u).   temperature, temperatures: as
  *     in sample_rows.
  *   accepted: [requests] int64, the drafts accepted.

@@ -157,24 +157,27 @@ __global__ void __launch_bounds__(kRouteThreads) k_zero(unsigned long long *coun
     for (int j = threadIdx.x; j < n; j += kRouteThreads) counts[j] = 0;
 }
 
-// CTAs of an SM, by the columns a lane holds: 80 registers a thread at 32 of them
-// (16384 x 256, us, of 2 / 3 / 4 CTAs: 12.7 / 12.0 / 12.8), 64 else (65536 x 64 at
-// eight a lane, of 2 / 3 / 4 / 5: 22.2 / 18.6 / 18.6 / 23.4).
+// CTAs of an SM, by the columns a lane holds: 80 registers a thread at 32 of them,
+// 64 else. Measured (us, with counts, of 2 / 3 / 4 / 5 CTAs): 16384 x 256 bf16, 32 a
+// lane, 11.8 / 11.2 / 12.0 / 13.8; 65536 x 64, 16 a lane, 12.7 / 11.3 / 12.1 / 12.3.
 __host__ __device__ constexpr int route_ctas(int v) { return v > 16 ? 3 : 4; }
 // Words of a row in shared memory: its lanes' columns, 16 bytes apart by bank, the
 // rows of a warp 32.
 __host__ __device__ constexpr int route_row(int lanes, int v) { return lanes * (v + 4) + (lanes == 8 || lanes == 16 ? 8 : 0); }
 
-// k_route: bound by the instructions of the choice, most of them compares at half
-// rate. So up to four rows share a warp's instructions, and a lane keeps the
+// k_route: bound by the instructions of the choice, many of them compares at half
+// rate, in waves of a chain of latencies (half of the issue slots are taken). So up
+// to eight rows share a warp's instructions, and a lane keeps the
 // largest of each eight of its columns only: the columns lie in shared memory,
 // where the lane that gives one looks for it among eight, takes it out and has the
-// largest of the rest. Measured (us, 16384 x 256 bf16, k = 8,
-// sigmoid scores with a bias, 4 of 8 groups): this 9.9; a row a warp, with each
-// lane's two best columns and the value of its third in registers, 16.0. Counts
-// add 1.1 us, and 1.4 more with a CTA per 32 rows than with three an SM. The eight
-// searched by the row's lanes, a column each, take fewer instructions in a longer
-// chain: 0.3 us slower here, 6% faster at four times the rows.
+// largest of the rest. Measured (us, replayed, 16384 x 256 bf16, k = 8, sigmoid
+// scores with a bias, 4 of 8 groups, a tenth of the rows padding): 10.6 without
+// counts, 11.6 with them; a row a warp, with each lane's two best columns and the
+// value of its third in registers, took 16.0 without counts where the first form of
+// this took 11.6. 14592 rows, what three CTAs an SM hold at once, take 8.4 without
+// counts, 15000 10.2. Counts take 1.4 us more with a CTA per 32 rows than with three an
+// SM. The eight searched by the row's lanes, a column each, take fewer instructions
+// in a longer chain: 0.3 us slower here, 6% faster at four times the rows.
 template <typename T, int L, int V, int kPer>  // kPer slots a lane
 __global__ void __launch_bounds__(kRouteThreads, route_ctas(V)) k_route(RouteArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
@@ -689,9 +692,10 @@ void route_shape(const RouteArgs &a, int least, int most, int slots, int *lanes,
 // Columns of a lane at most: 32, where rows are many and instructions count; 8
 // where they are few, a row's latency counts and lanes are to spare. Measured
 // (us, bf16, k = 8, sigmoid scores with a bias, 8 / 32 columns): 256 experts in 8
-// groups, 32 rows 3.7 / 4.8, 1024 3.9 / 5.1, 2048 4.7 / 5.1, 4096 7.0 / 5.4, 8192
-// 11.8 / 6.9, 16384 18.7 / 10.0, 65536 68 / 29; 512 experts, 1024 rows 4.5 / 5.5,
-// 4096 7.8 / 7.0, 16384 21.1 / 15.9; 128 experts, 4096 rows 6.6 / 5.6.
+// groups, 32 rows 3.7 / 5.1, 1024 3.9 / 5.5, 2048 5.0 / 5.4, 4096 7.0 / 5.5, 8192
+// 11.9 / 7.0, 16384 18.8 / 10.2, 65536 68 / 30; 512 experts in 8 groups, 1024 rows
+// 4.6 / 5.6, 4096 7.8 / 7.2, 16384 21.0 / 16.1; 128 experts, 2048 rows 4.2 / 4.4,
+// 4096 5.0 / 4.5.
 int route_most(const RouteArgs &a, const DeviceInfo &dev) {
     int lanes, v;
     route_shape(a, 8, 8, 1, &lanes, &v);
@@ -711,8 +715,8 @@ cudaError_t launch_route(DType t, const RouteArgs &a, const DeviceInfo &dev, cud
     // Four lanes a row, of many rows of up to 128 columns, so that eight share a warp's
     // instructions: for eight slots at most, two a lane, and not where groups would be
     // parts of a lane. Measured (us, bf16, sigmoid scores with a bias, 8 / 4 lanes): 32
-    // experts, k = 2, 16384 rows 4.6 / 3.4, 30000 6.2 / 4.1; 64, k = 6, 10000 5.0 / 4.7,
-    // 16384 5.8 / 4.9, 30000 8.3 / 6.7; 128, k = 8, 16384 7.4 / 6.5, 30000 10.8 / 9.6.
+    // experts, k = 2, 16384 rows 4.5 / 3.3, 30000 6.1 / 4.1; 64, k = 6, 10000 5.1 / 4.8,
+    // 16384 6.0 / 5.0, 30000 8.4 / 6.8; 128, k = 8, 16384 7.4 / 6.7, 30000 10.9 / 9.8.
     const int most = route_most(a, dev);
     route_shape(a, most == 32 && a.k <= 8 ? 4 : 8, most, 1, &lanes, &v);
     if (a.top_groups < a.groups && a.experts / a.groups % v != 0) route_shape(a, 8, most, 1, &lanes, &v);
